@@ -563,6 +563,131 @@ kvmm_status topk_stability_rco(const kvmm_shape* shape, const int32_t* hist_idx,
                                float unstable_frac, float* rco_unit, float* stability, uint8_t* unstable,
                                int32_t* err, kvmm_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Appending with the position rotation, and a cache held in 4 bits.
+ *
+ * The pages take keys as stored (rotated by position); these calls take them
+ * as a projection leaves them.  They have no counterpart in the pages.
+ *
+ * kvmm_rows -- bf16 rows [batch][token][head] of D consecutive channels each,
+ * any of the three axes outermost: element strides (multiples of 8, >= 0),
+ * data 16-byte aligned.  Views of one projection's output are such rows.
+ *
+ * kvmm_rope -- the rotation.  table [rows][2][dim/2] float (16-byte aligned):
+ * for each position its dim/2 cosines, then its dim/2 sines.  The first dim
+ * channels of a row turn (dim a multiple of 32, 32 <= dim <= D), the others
+ * pass: channels (i, i + dim/2) form a pair, or (2i, 2i + 1) with interleaved
+ * != 0, and pair i becomes
+ *     (a cos_i - b sin_i, b cos_i + a sin_i)
+ * in fp32, every product and their sum rounded (no fused multiply-add, so the
+ * bits depend on nothing but the inputs).  A token's position is its index in
+ * the sequence, or positions[b * n_new + j] for row j of batch b when
+ * positions ([B][n_new] int32) is not NULL.  A row whose position lies
+ * outside [0, rows) sets KVMM_ERR_OUT_OF_RANGE and is not written (neither
+ * its query nor its key and value).
+ */
+typedef struct kvmm_rows {
+    const kvmm_bf16* data;
+    int64_t batch_stride, token_stride, head_stride;
+} kvmm_rows;
+
+typedef struct kvmm_rope {
+    const float* table;
+    const int32_t* positions;
+    int32_t rows, dim, interleaved;
+} kvmm_rope;
+
+/* kv_append_rope -- rotate the new tokens' queries and keys by their
+ * positions, write the keys and values to their pages and refresh the MinMax
+ * of the pages they reach: kv_minmax_update with the rotation, strided rows
+ * and the step's queries.
+ *
+ * new_k, new_v: rows [B][n_new][Hkv] (kvmm_rows); q: rows [B][n_new][Hq], or
+ * NULL for none, whose rotated rows go to q_out [B][n_new][Hq][D] bf16 (for
+ * n_new = 1 the q of the calls above; it may be q's own dense memory).
+ * Tokens, ranges, table entries and MinMax are treated as kv_minmax_update
+ * treats them: token tok_begin[b] + j takes row j, j < tok_end[b] -
+ * tok_begin[b] <= n_new; rows behind that are neither read nor written.
+ * rope NULL: nothing turns.  A rotated channel is rounded to bf16 once
+ * (nearest even).  meta NULL: no MinMax is kept.  A query row is written
+ * whatever its keys' table entries are.
+ */
+kvmm_status kv_append_rope(const kvmm_shape* shape, int32_t layer, const kvmm_rows* q, const kvmm_rows* new_k,
+                           const kvmm_rows* new_v, int32_t n_new, const int32_t* tok_begin, const int32_t* tok_end,
+                           const kvmm_rope* rope, kvmm_bf16* q_out, kvmm_bf16* k_pool, kvmm_bf16* v_pool,
+                           const int32_t* block_table, kvmm_bf16* meta, int32_t* err, kvmm_stream stream);
+
+/* The 4-bit cache: one pool of uint8 [n_phys][kvmm_kv4_page_bytes(shape)],
+ * 16-byte aligned, whose page holds, one after another,
+ *     key codes    [T][D/2]    channel 2i in the low nibble of byte i
+ *     key scales   [T][D/16]   e4m3, one for 16 channels
+ *     value codes  [T][D/2]
+ *     value scales [T][D/16]
+ * A code is e2m1: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 for 0..7, bit 3 the
+ * sign.  The value held is code * scale * k_scale (or v_scale), where k_scale
+ * and v_scale are factors of the call (finite, > 0; one for a layer's keys
+ * and one for its values keeps the scales inside e4m3's range).  A row x is
+ * held as y = x * fl(1 / k_scale) in fp32; scale = max |y| of the 16 channels
+ * divided by 6, rounded to e4m3 (nearest even, at most 448); code = the
+ * nearest e2m1 to y / scale (ties to the even code, at most 6 in magnitude),
+ * 0 where the scale is 0.  code * scale has at most six significant bits, so
+ * it is exact in bf16: the MinMax metadata of a 4-bit page are the exact
+ * bounds of its keys over k_scale.  A positive factor common to a layer does
+ * not change which pages page_score_topk selects; its scores are then those
+ * over k_scale.
+ *
+ * kvmm_kv4_page_bytes: T * (D + D/8), 0 for an unsupported shape.
+ *
+ * kv4_append_rope -- kv_append_rope into the 4-bit cache.  The keys are held
+ * from their rotated fp32 values (not rounded to bf16 first); meta are the
+ * bounds of the keys as held, over k_scale.
+ */
+size_t kvmm_kv4_page_bytes(const kvmm_shape* shape);
+
+kvmm_status kv4_append_rope(const kvmm_shape* shape, int32_t layer, const kvmm_rows* q, const kvmm_rows* new_k,
+                            const kvmm_rows* new_v, int32_t n_new, const int32_t* tok_begin, const int32_t* tok_end,
+                            const kvmm_rope* rope, kvmm_bf16* q_out, uint8_t* kv4_pool, float k_scale,
+                            float v_scale, const int32_t* block_table, kvmm_bf16* meta, int32_t* err,
+                            kvmm_stream stream);
+
+/* kv4_gather -- tokens of the 4-bit cache as bf16 rows: for a prompt chunk's
+ * own attention over what is already held, or to take a sequence out.
+ * Token tok_begin[b] + j (tok_begin NULL: j) of every KV head of `layer`, for
+ * j < tok_end[b] - tok_begin[b] <= n_rows, goes to row j of k_out and v_out
+ * ([B][n_rows][Hkv][D] bf16, either may be NULL): code * scale * factor,
+ * rounded once (nearest even).  Rows behind a sequence's last are left as
+ * they were, as are those of pages whose table entry is null or out of range
+ * (which sets its error bit).  A range outside [0, Pmax*T], or one longer
+ * than n_rows, sets KVMM_ERR_OUT_OF_RANGE and is clamped.
+ */
+kvmm_status kv4_gather(const kvmm_shape* shape, int32_t layer, const uint8_t* kv4_pool, float k_scale, float v_scale,
+                       const int32_t* block_table, const int32_t* tok_begin, const int32_t* tok_end, int32_t n_rows,
+                       kvmm_bf16* k_out, kvmm_bf16* v_out, int32_t* err, kvmm_stream stream);
+
+/* sparse_paged_decode_attn_kv4 -- sparse_paged_decode_attn over the 4-bit
+ * cache: z_t = sm_scale * (q_g . k_t) and out = sum p_t v_t over the values
+ * the cache holds, accumulated in fp32, with the same results for empty units
+ * (out = 0, lse = -inf), invalid selections and table entries.  sel_idx and
+ * sel_cnt both NULL: every page of the sequence (Kmax is then not used).
+ * What a page holds behind its sequence's last token is not looked at.
+ * The pages of all units are dealt evenly to one CTA for each SM, whatever
+ * the sequences' lengths; partial results of a unit that falls on several
+ * CTAs pass through the workspace (kvmm_kv4_workspace_size(shape) bytes,
+ * 16-byte aligned; it needs no initialisation and holds nothing between
+ * calls) and are merged by a second launch.
+ * flags: 0, or KVMM_EARLY_READS: the caller guarantees that no kernel still
+ * running when this launch starts writes seq_len or the layer's block-table
+ * rows; the launch may then read them while that kernel drains.
+ */
+size_t kvmm_kv4_workspace_size(const kvmm_shape* shape);
+
+kvmm_status sparse_paged_decode_attn_kv4(const kvmm_shape* shape, int32_t layer, const kvmm_bf16* q,
+                                         const uint8_t* kv4_pool, float k_scale, float v_scale,
+                                         const int32_t* block_table, const int32_t* seq_len, const int32_t* sel_idx,
+                                         const int32_t* sel_cnt, float sm_scale, float* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, uint32_t flags, int32_t* err,
+                                         kvmm_stream stream);
+
 /* Workspace bytes that page_score_topk and page_score_topk_attn need
  * (sparse_paged_decode_attn needs none; num_splits is accepted for the
  * stable signature and ignored).  Returns 0 for an unsupported shape. */

@@ -850,4 +850,184 @@ kvmm_status topk_stability_rco(const kvmm_shape* shape, const int32_t* hist_idx,
     return launched(kvmm::launch_stability_rco(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// new rows: aligned, with strides that keep every row 16-byte aligned
+static bool rows_ok(const kvmm_rows* r)
+{
+    if (r == nullptr || !req(r->data)) return false;
+    for (const int64_t st : {r->batch_stride, r->token_stride, r->head_stride})
+        if (st < 0 || st % 8 != 0) return false;
+    return true;
+}
+
+static bool factor_ok(float f) { return std::isfinite(f) && f > 0.f && std::isfinite(1.0f / f); }
+
+// kv_append_rope and kv4_append_rope: the arguments they share
+static kvmm_status append_rope_params(const kvmm_shape* shape, int32_t layer, const kvmm_rows* q,
+                                      const kvmm_rows* new_k, const kvmm_rows* new_v, int32_t n_new,
+                                      const int32_t* tok_begin, const int32_t* tok_end, const kvmm_rope* rope,
+                                      kvmm_bf16* q_out, const int32_t* block_table, kvmm_bf16* meta, int32_t* err,
+                                      kvmm::AppendParams& p)
+{
+    kvmm_status st = check_shape(shape);
+    if (st != KVMM_OK) return st;
+    const kvmm_shape& s = *shape;
+    if (layer < 0 || layer >= s.L || n_new < 1) return KVMM_INVALID_ARG;
+    if (!rows_ok(new_k) || !rows_ok(new_v) || (q != nullptr && !rows_ok(q)) || !req4(tok_begin) || !req4(tok_end) ||
+        !req4(block_table) || !opt(meta) || !opt4(err))
+        return KVMM_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr) || !opt(q_out)) return KVMM_INVALID_ARG;
+    if (rope != nullptr) {
+        if (!req(rope->table) || rope->rows < 1 || !opt4(rope->positions) || rope->dim < 1 || rope->dim > s.D ||
+            (rope->interleaved != 0 && rope->interleaved != 1))
+            return KVMM_INVALID_ARG;
+        if (rope->dim % 32 != 0) return KVMM_UNSUPPORTED_SHAPE;
+    }
+    p.B = s.B;
+    p.L = s.L;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.D = s.D;
+    p.T = s.T;
+    p.Pmax = s.Pmax;
+    p.layer = layer;
+    p.n_new = n_new;
+    p.n_phys = s.n_phys;
+    if (q != nullptr) p.q = *q;
+    p.k = *new_k;
+    p.v = *new_v;
+    p.tok_begin = tok_begin;
+    p.tok_end = tok_end;
+    if (rope != nullptr) p.rope = *rope;
+    p.q_out = q_out;
+    p.block_table = block_table;
+    p.meta = meta;
+    p.err = err;
+    return KVMM_OK;
+}
+
+kvmm_status kv_append_rope(const kvmm_shape* shape, int32_t layer, const kvmm_rows* q, const kvmm_rows* new_k,
+                           const kvmm_rows* new_v, int32_t n_new, const int32_t* tok_begin, const int32_t* tok_end,
+                           const kvmm_rope* rope, kvmm_bf16* q_out, kvmm_bf16* k_pool, kvmm_bf16* v_pool,
+                           const int32_t* block_table, kvmm_bf16* meta, int32_t* err, kvmm_stream stream)
+{
+    kvmm::AppendParams p{};
+    const kvmm_status st = append_rope_params(shape, layer, q, new_k, new_v, n_new, tok_begin, tok_end, rope, q_out,
+                                              block_table, meta, err, p);
+    if (st != KVMM_OK) return st;
+    if (!req(k_pool) || !req(v_pool)) return KVMM_INVALID_ARG;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    return launched(kvmm::launch_append_rope(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kvmm_kv4_page_bytes(const kvmm_shape* shape)
+{
+    if (check_shape(shape) != KVMM_OK) return 0;
+    return static_cast<size_t>(shape->T) * (shape->D + shape->D / 8);
+}
+
+kvmm_status kv4_append_rope(const kvmm_shape* shape, int32_t layer, const kvmm_rows* q, const kvmm_rows* new_k,
+                            const kvmm_rows* new_v, int32_t n_new, const int32_t* tok_begin, const int32_t* tok_end,
+                            const kvmm_rope* rope, kvmm_bf16* q_out, uint8_t* kv4_pool, float k_scale,
+                            float v_scale, const int32_t* block_table, kvmm_bf16* meta, int32_t* err,
+                            kvmm_stream stream)
+{
+    kvmm::AppendParams p{};
+    const kvmm_status st = append_rope_params(shape, layer, q, new_k, new_v, n_new, tok_begin, tok_end, rope, q_out,
+                                              block_table, meta, err, p);
+    if (st != KVMM_OK) return st;
+    if (!req(kv4_pool) || !factor_ok(k_scale) || !factor_ok(v_scale)) return KVMM_INVALID_ARG;
+    p.kv4_pool = kv4_pool;
+    p.k_inv = 1.0f / k_scale;
+    p.v_inv = 1.0f / v_scale;
+    return launched(kvmm::launch_append_rope(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvmm_status kv4_gather(const kvmm_shape* shape, int32_t layer, const uint8_t* kv4_pool, float k_scale, float v_scale,
+                       const int32_t* block_table, const int32_t* tok_begin, const int32_t* tok_end, int32_t n_rows,
+                       kvmm_bf16* k_out, kvmm_bf16* v_out, int32_t* err, kvmm_stream stream)
+{
+    kvmm_status st = check_shape(shape);
+    if (st != KVMM_OK) return st;
+    const kvmm_shape& s = *shape;
+    if (layer < 0 || layer >= s.L || n_rows < 1) return KVMM_INVALID_ARG;
+    if (!req(kv4_pool) || !factor_ok(k_scale) || !factor_ok(v_scale) || !req4(block_table) || !opt4(tok_begin) ||
+        !req4(tok_end) || !opt(k_out) || !opt(v_out) || (k_out == nullptr && v_out == nullptr) || !opt4(err))
+        return KVMM_INVALID_ARG;
+    kvmm::GatherParams p{};
+    p.B = s.B;
+    p.L = s.L;
+    p.Hkv = s.Hkv;
+    p.D = s.D;
+    p.T = s.T;
+    p.Pmax = s.Pmax;
+    p.layer = layer;
+    p.n_rows = n_rows;
+    p.n_phys = s.n_phys;
+    p.kv4_pool = kv4_pool;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.tok_begin = tok_begin;
+    p.tok_end = tok_end;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.err = err;
+    return launched(kvmm::launch_kv4_gather(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kvmm_kv4_workspace_size(const kvmm_shape* shape)
+{
+    if (check_shape(shape) != KVMM_OK) return 0;
+    return kvmm::kv4_ws_bytes(shape->D);
+}
+
+kvmm_status sparse_paged_decode_attn_kv4(const kvmm_shape* shape, int32_t layer, const kvmm_bf16* q,
+                                         const uint8_t* kv4_pool, float k_scale, float v_scale,
+                                         const int32_t* block_table, const int32_t* seq_len, const int32_t* sel_idx,
+                                         const int32_t* sel_cnt, float sm_scale, float* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, uint32_t flags, int32_t* err,
+                                         kvmm_stream stream)
+{
+    kvmm_status st = check_shape(shape);
+    if (st != KVMM_OK) return st;
+    const kvmm_shape& s = *shape;
+    if (layer < 0 || layer >= s.L || !std::isfinite(sm_scale) || (flags & ~KVMM_EARLY_READS) != 0u)
+        return KVMM_INVALID_ARG;
+    if (!req(q) || !req(kv4_pool) || !factor_ok(k_scale) || !factor_ok(v_scale) || !req4(block_table) ||
+        !req4(seq_len) || !opt4(sel_idx) || !opt4(sel_cnt) || (sel_idx == nullptr) != (sel_cnt == nullptr) ||
+        !req4(out) || !opt4(lse) || !req(workspace) || !opt4(err))
+        return KVMM_INVALID_ARG;
+    if (workspace_bytes < kvmm::kv4_ws_bytes(s.D)) return KVMM_WORKSPACE_TOO_SMALL;
+    kvmm::Kv4AttnParams p{};
+    p.B = s.B;
+    p.L = s.L;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.G = s.Hq / s.Hkv;
+    p.D = s.D;
+    p.T = s.T;
+    p.Pmax = s.Pmax;
+    p.Kmax = s.Kmax;
+    p.layer = layer;
+    p.early = (flags & KVMM_EARLY_READS) != 0u ? 1 : 0;
+    p.n_phys = s.n_phys;
+    p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(s.D))) * 1.4426950408889634f *
+                   k_scale;
+    if (!std::isfinite(p.scale_log2)) return KVMM_INVALID_ARG;
+    p.v_scale = v_scale;
+    p.q = q;
+    p.kv4_pool = kv4_pool;
+    p.block_table = block_table;
+    p.seq_len = seq_len;
+    p.sel_idx = sel_idx;
+    p.sel_cnt = sel_cnt;
+    p.out = out;
+    p.lse = lse;
+    p.pre = static_cast<int32_t*>(workspace);
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kvmm::kKv4PreBytes);
+    p.err = err;
+    return launched(kvmm::launch_kv4_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -271,6 +271,68 @@ struct StabilityParams {
     int32_t* err;
 };
 
+// kv_append_rope / kv4_append_rope (append_rope.cu)
+struct AppendParams {
+    int32_t B, L, Hq, Hkv, D, T, Pmax, layer, n_new;
+    int64_t n_phys;
+    kvmm_rows q;  // data null: no queries
+    kvmm_rows k, v;
+    const int32_t* tok_begin;
+    const int32_t* tok_end;
+    kvmm_rope rope;  // table null: nothing turns
+    kvmm_bf16* q_out;
+    kvmm_bf16* k_pool;  // the bf16 cache, or
+    kvmm_bf16* v_pool;
+    uint8_t* kv4_pool;  // the 4-bit cache (k_pool null)
+    float k_inv, v_inv;  // 1 / k_scale, 1 / v_scale
+    const int32_t* block_table;
+    kvmm_bf16* meta;  // or null
+    int32_t* err;
+};
+
+// kv4_gather (kv4_gather.cu)
+struct GatherParams {
+    int32_t B, L, Hkv, D, T, Pmax, layer, n_rows;
+    int64_t n_phys;
+    const uint8_t* kv4_pool;
+    float k_scale, v_scale;
+    const int32_t* block_table;
+    const int32_t* tok_begin;  // or null: 0
+    const int32_t* tok_end;
+    kvmm_bf16* k_out;  // either may be null
+    kvmm_bf16* v_out;
+    int32_t* err;
+};
+
+// sparse_paged_decode_attn_kv4 (kv4_attn.cu)
+struct Kv4AttnParams {
+    int32_t B, L, Hq, Hkv, G, D, T, Pmax, Kmax, layer;
+    int32_t u0, nu;  // the (batch, KV head) units of this launch: u0 .. u0 + nu - 1
+    int32_t early;   // 1: seq_len and the table may be read before the preceding kernel has finished
+    int64_t n_phys;
+    float scale_log2;  // sm_scale * k_scale * log2(e)
+    float v_scale;
+    const kvmm_bf16* q;
+    const uint8_t* kv4_pool;
+    const int32_t* block_table;
+    const int32_t* seq_len;
+    const int32_t* sel_idx;  // null: every page
+    const int32_t* sel_cnt;
+    float* out;
+    float* lse;
+    float* partial;  // workspace: two partial results for each CTA
+    int32_t* pre;    // workspace: the units' first pages in the launch's page order, then their sum
+    int32_t* err;
+};
+constexpr int kKv4MaxUnits = 2048;  // units of one launch (their page counts are summed in shared memory)
+constexpr int kKv4MaxCtas = 256;    // CTAs of one launch
+constexpr size_t kKv4PreBytes = (kKv4MaxUnits + 1) * sizeof(int32_t) + 252;  // a multiple of 256
+__host__ __device__ constexpr size_t kv4_partial_floats(int D) { return size_t(8) * D + 16; }  // unnormalised output, then (m, l) of 8 heads
+inline size_t kv4_ws_bytes(int D) { return kKv4PreBytes + size_t(kKv4MaxCtas) * 2 * kv4_partial_floats(D) * sizeof(float); }
+
+cudaError_t launch_append_rope(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv4_gather(const GatherParams& p, cudaStream_t stream);
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, cudaStream_t stream);
 cudaError_t launch_minmax_update(const UpdateParams& p, cudaStream_t stream);
 cudaError_t launch_score_topk(const ScoreParams& p, int group_reduce, cudaStream_t stream);
 cudaError_t launch_sparse_attention(const AttnParams& p, cudaStream_t stream);

@@ -25,7 +25,9 @@ EXPORTS = ("kv_minmax_update", "page_score_topk", "sparse_paged_decode_attn", "t
            "kvmm_status_string",
            "kvmm_last_cuda_error", "page_score_topk_static_scratch", "page_score_topk_attn", "decode_layer", "topk_history_record",
            "topk_stability_rco", "promote_pages", "block_table_update", "kv_meankey_update",
-           "page_score_topk_mean", "kv_centroid_build", "page_score_topk_centroid")
+           "page_score_topk_mean", "kv_centroid_build", "page_score_topk_centroid", "kv_append_rope",
+           "kv4_append_rope", "kv4_gather", "sparse_paged_decode_attn_kv4", "kvmm_kv4_page_bytes",
+           "kvmm_kv4_workspace_size")
 
 
 class KvmmError(RuntimeError):
@@ -48,6 +50,34 @@ class Shape(ctypes.Structure):
 
     def __repr__(self) -> str:
         return ("Shape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")")
+
+
+class Rows(ctypes.Structure):
+    """``kvmm_rows``: bf16 rows [batch][token][head] by their strides (in elements)."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class RopeStruct(ctypes.Structure):
+    """``kvmm_rope``."""
+
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class Rope:
+    """The position rotation of kv_append_rope and kv4_append_rope: ``table`` [rows, 2, dim/2] float32 (cosines, then
+    sines, of each position), the first ``dim`` channels turned in pairs (i, i + dim/2), or (2i, 2i + 1) with
+    ``interleaved``.  ``positions`` [B, n_new] int32: the tokens' positions when they are not their indices."""
+
+    def __init__(self, table: torch.Tensor, dim: int, interleaved: bool = False, positions: torch.Tensor | None = None):
+        if table.dim() != 3 or table.shape[1] != 2 or table.shape[2] * 2 != dim:
+            raise ValueError(f"table must be [rows, 2, {dim // 2}], got {tuple(table.shape)}")
+        self.table, self.positions, self.dim = table, positions, dim
+        self.c = RopeStruct(_dev(table, "table", torch.float32),
+                            _dev(positions, "positions", torch.int32, optional=True), table.shape[0], dim,
+                            int(bool(interleaved)))
 
 
 def make_shape(B, L, Hq, Hkv, D, T, Pmax, Kmax, n_phys) -> Shape:
@@ -90,6 +120,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.page_score_topk_mean.argtypes = [SP, I32, P, P, P, P, I32, I32, P, P, P, P, SZ, P, P]
     lib.kv_centroid_build.argtypes = [SP, I32, P, P, I32, I32, P, P, P, P, P, P]
     lib.page_score_topk_centroid.argtypes = [SP, I32, P, P, P, I32, P, P, P, P, I32, I32, I32, P, P, P, P, P, P]
+    RP, TP = ctypes.POINTER(Rows), ctypes.POINTER(RopeStruct)
+    lib.kv_append_rope.argtypes = [SP, I32, RP, RP, RP, I32, P, P, TP, P, P, P, P, P, P, P]
+    lib.kv4_append_rope.argtypes = [SP, I32, RP, RP, RP, I32, P, P, TP, P, P, F32, F32, P, P, P, P]
+    lib.kv4_gather.argtypes = [SP, I32, P, F32, F32, P, P, P, I32, P, P, P, P]
+    lib.sparse_paged_decode_attn_kv4.argtypes = [SP, I32, P, P, F32, F32, P, P, P, P, F32, P, P, P, SZ, U32, P, P]
+    lib.kvmm_kv4_page_bytes.argtypes = [SP]
+    lib.kvmm_kv4_page_bytes.restype = SZ
+    lib.kvmm_kv4_workspace_size.argtypes = [SP]
+    lib.kvmm_kv4_workspace_size.restype = SZ
+    for f in ("kv_append_rope", "kv4_append_rope", "kv4_gather", "sparse_paged_decode_attn_kv4"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("kv_minmax_update", "page_score_topk", "sparse_paged_decode_attn", "topk_promotion_diff",
               "page_score_topk_static_scratch", "page_score_topk_attn", "decode_layer", "topk_history_record",
               "topk_stability_rco", "promote_pages", "block_table_update", "kv_meankey_update",
@@ -469,3 +510,154 @@ def page_score_topk_centroid(shape: Shape, layer: int, q, mean, seq_len, R: int,
             _dev(scores_out, "scores_out", torch.float32, s.B * s.Hkv * s.Pmax, optional=True),
             _dev(err, "err", torch.int32, 1, optional=True), _stream(stream))
     _check("page_score_topk_centroid", load().page_score_topk_centroid(*args))
+
+
+# --------------------------------------------------------------------------- #
+def kv4_page_bytes(shape: Shape) -> int:
+    """Bytes of one page of the 4-bit cache (keys and values, codes and scales)."""
+    return int(load().kvmm_kv4_page_bytes(ctypes.byref(shape)))
+
+
+def kv4_workspace_size(shape: Shape) -> int:
+    return int(load().kvmm_kv4_workspace_size(ctypes.byref(shape)))
+
+
+def alloc_kv4_pool(shape: Shape, device="cuda") -> torch.Tensor:
+    """A zero-filled pool [n_phys, page bytes] (uint8) of the 4-bit cache."""
+    n = kv4_page_bytes(shape)
+    if n == 0:
+        raise KvmmError("kvmm_kv4_page_bytes", UNSUPPORTED_SHAPE)
+    return torch.zeros(shape.n_phys, n, dtype=torch.uint8, device=device)
+
+
+def alloc_kv4_workspace(shape: Shape, device="cuda") -> torch.Tensor:
+    """A workspace (uint8) for sparse_paged_decode_attn_kv4."""
+    n = kv4_workspace_size(shape)
+    if n == 0:
+        raise KvmmError("kvmm_kv4_workspace_size", UNSUPPORTED_SHAPE)
+    return torch.empty((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def _one_device(*tensors) -> None:
+    """The call runs on the current device's stream: every tensor has to be there."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"a tensor on {t.device} given to a call on cuda:{here}")
+
+
+def _rows(t: torch.Tensor | None, name: str, B: int, n: int, H: int, D: int) -> Rows | None:
+    """A [B, n, H, D] bf16 view as kvmm_rows."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (B, n, H, D):
+        raise ValueError(f"{name} must be {(B, n, H, D)}, got {tuple(t.shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the channels of a row must be consecutive")
+    sb, st, sh = t.stride()[:3]
+    # an axis of one entry has no step: its stride may be anything
+    return Rows(t.data_ptr(), sb if B > 1 else 0, st if n > 1 else 0, sh if H > 1 else 0)
+
+
+def _append_rows(s: Shape, q, new_k, new_v, rope, q_out):
+    n = new_k.shape[1] if new_k.dim() == 4 else -1
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out are given together or not at all")
+    rows = [_rows(t, name, s.B, n, H, s.D) for t, name, H in ((q, "q", s.Hq), (new_k, "new_k", s.Hkv),
+                                                              (new_v, "new_v", s.Hkv))]
+    if rope is not None and rope.positions is not None and rope.positions.numel() < s.B * n:
+        raise ValueError(f"positions has {rope.positions.numel()} elements, needs {s.B * n}")
+    return n, [None if r is None else ctypes.byref(r) for r in rows], None if rope is None else ctypes.byref(rope.c)
+
+
+def kv_append_rope(shape: Shape, layer: int, q, new_k, new_v, tok_begin, tok_end, k_pool, v_pool, block_table, meta,
+                   rope: Rope | None = None, q_out=None, err=None, stream=None) -> None:
+    """Rotate the new tokens' queries and keys, append keys and values, refresh the MinMax of their pages.
+
+    new_k, new_v [B, n_new, Hkv, D] and q [B, n_new, Hq, D] (or None) are bf16 views of any strides whose channels are
+    consecutive; q_out [B, n_new, Hq, D] takes the rotated queries; meta may be None."""
+    s = shape
+    units = s.B * s.L * s.Hkv
+    n, (qr, kr, vr), rp = _append_rows(s, q, new_k, new_v, rope, q_out)
+    _one_device(q, new_k, new_v, tok_begin, tok_end, k_pool, v_pool, block_table, meta, q_out, err,
+                rope and rope.table, rope and rope.positions)
+    args = (ctypes.byref(s), layer, qr, kr, vr, n, _dev(tok_begin, "tok_begin", torch.int32, s.B),
+            _dev(tok_end, "tok_end", torch.int32, s.B), rp,
+            _dev(q_out, "q_out", torch.bfloat16, s.B * n * s.Hq * s.D, optional=True),
+            _dev(k_pool, "k_pool", torch.bfloat16, s.n_phys * s.T * s.D),
+            _dev(v_pool, "v_pool", torch.bfloat16, s.n_phys * s.T * s.D),
+            _dev(block_table, "block_table", torch.int32, units * s.Pmax),
+            _dev(meta, "meta", torch.bfloat16, units * s.Pmax * 2 * s.D, optional=True),
+            _dev(err, "err", torch.int32, 1, optional=True), _stream(stream))
+    _check("kv_append_rope", load().kv_append_rope(*args))
+
+
+def kv4_append_rope(shape: Shape, layer: int, q, new_k, new_v, tok_begin, tok_end, kv4_pool, block_table, meta,
+                    rope: Rope | None = None, q_out=None, k_scale: float = 1.0, v_scale: float = 1.0, err=None,
+                    stream=None) -> None:
+    """kv_append_rope into the 4-bit cache (kv4_pool [n_phys, kv4_page_bytes] uint8); meta are the bounds of the keys
+    as held, over k_scale."""
+    s = shape
+    units = s.B * s.L * s.Hkv
+    n, (qr, kr, vr), rp = _append_rows(s, q, new_k, new_v, rope, q_out)
+    _one_device(q, new_k, new_v, tok_begin, tok_end, kv4_pool, block_table, meta, q_out, err, rope and rope.table,
+                rope and rope.positions)
+    args = (ctypes.byref(s), layer, qr, kr, vr, n, _dev(tok_begin, "tok_begin", torch.int32, s.B),
+            _dev(tok_end, "tok_end", torch.int32, s.B), rp,
+            _dev(q_out, "q_out", torch.bfloat16, s.B * n * s.Hq * s.D, optional=True),
+            _dev(kv4_pool, "kv4_pool", torch.uint8, s.n_phys * s.T * (s.D + s.D // 8)), float(k_scale), float(v_scale),
+            _dev(block_table, "block_table", torch.int32, units * s.Pmax),
+            _dev(meta, "meta", torch.bfloat16, units * s.Pmax * 2 * s.D, optional=True),
+            _dev(err, "err", torch.int32, 1, optional=True), _stream(stream))
+    _check("kv4_append_rope", load().kv4_append_rope(*args))
+
+
+def kv4_gather(shape: Shape, layer: int, kv4_pool, block_table, tok_begin, tok_end, k_out, v_out, k_scale: float = 1.0,
+               v_scale: float = 1.0, err=None, stream=None) -> None:
+    """Tokens [tok_begin, tok_end) of every KV head (tok_begin None = 0) as bf16 rows of k_out and v_out
+    [B, n_rows, Hkv, D] (either may be None); rows behind a sequence's last are left as they were."""
+    s = shape
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        raise ValueError("k_out or v_out is required")
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and (t.dim() != 4 or t.shape[1] != some.shape[1] or
+                              (t.shape[0], t.shape[2], t.shape[3]) != (s.B, s.Hkv, s.D)):
+            raise ValueError(f"{name} must be [{s.B}, n_rows, {s.Hkv}, {s.D}], got {tuple(t.shape)}")
+    _one_device(kv4_pool, block_table, tok_begin, tok_end, k_out, v_out, err)
+    args = (ctypes.byref(s), layer, _dev(kv4_pool, "kv4_pool", torch.uint8, s.n_phys * s.T * (s.D + s.D // 8)),
+            float(k_scale), float(v_scale),
+            _dev(block_table, "block_table", torch.int32, s.B * s.L * s.Hkv * s.Pmax),
+            _dev(tok_begin, "tok_begin", torch.int32, s.B, optional=True), _dev(tok_end, "tok_end", torch.int32, s.B),
+            some.shape[1], _dev(k_out, "k_out", torch.bfloat16, optional=True),
+            _dev(v_out, "v_out", torch.bfloat16, optional=True), _dev(err, "err", torch.int32, 1, optional=True),
+            _stream(stream))
+    _check("kv4_gather", load().kv4_gather(*args))
+
+
+def sparse_paged_decode_attn_kv4(shape: Shape, layer: int, q, kv4_pool, block_table, seq_len, sel_idx, sel_cnt, out,
+                                 workspace, lse=None, err=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                                 sm_scale: float = 0.0, stream=None, early_reads: bool = False) -> None:
+    """Attention over the selected pages of the 4-bit cache, or, with sel_idx and sel_cnt None, over every page.
+    workspace: alloc_kv4_workspace.  ``early_reads``: no kernel still running when this launch starts writes seq_len
+    or the layer's block-table rows."""
+    s = shape
+    units = s.B * s.L * s.Hkv
+    if (sel_idx is None) != (sel_cnt is None):
+        raise ValueError("sel_idx and sel_cnt are given together or not at all")
+    _one_device(q, kv4_pool, block_table, seq_len, sel_idx, sel_cnt, out, workspace, lse, err)
+    args = (ctypes.byref(s), layer, _dev(q, "q", torch.bfloat16, s.B * s.Hq * s.D),
+            _dev(kv4_pool, "kv4_pool", torch.uint8, s.n_phys * s.T * (s.D + s.D // 8)), float(k_scale), float(v_scale),
+            _dev(block_table, "block_table", torch.int32, units * s.Pmax),
+            _dev(seq_len, "seq_len", torch.int32, s.B),
+            _dev(sel_idx, "sel_idx", torch.int32, units * s.Kmax, optional=True),
+            _dev(sel_cnt, "sel_cnt", torch.int32, units, optional=True), float(sm_scale),
+            _dev(out, "out", torch.float32, s.B * s.Hq * s.D),
+            _dev(lse, "lse", torch.float32, s.B * s.Hq, optional=True),
+            _dev(workspace, "workspace", torch.uint8), workspace.numel(), EARLY_READS if early_reads else 0,
+            _dev(err, "err", torch.int32, 1, optional=True), _stream(stream))
+    _check("sparse_paged_decode_attn_kv4", load().sparse_paged_decode_attn_kv4(*args))

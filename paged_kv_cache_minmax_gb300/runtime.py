@@ -11,6 +11,8 @@ layer and step, the calls in the method's order:
   4. ``sparse_paged_decode_attn``  attention over the selected pages
 
 or, with steps 2 and 4 in one launch, ``page_score_topk_attn`` then the diff.
+From a projection's unrotated rows, step 1 is ``kv_append_rope``.
+:class:`Kv4DecodeState` is the same over a cache held in 4 bits.
 
 (FlexiCache, "Core method", sections 1-3.)  Everything runs on one CUDA
 stream; nothing here synchronises.
@@ -22,14 +24,15 @@ import torch
 from . import kvmm
 
 
-class DecodeState:
-    def __init__(self, B, L, Hq, Hkv, D, T, Pmax, K, k_pool, v_pool, block_table, seq_len, num_splits=0,
-                 group_reduce=0, device="cuda"):
-        self.shape = kvmm.make_shape(B, L, Hq, Hkv, D, T, Pmax, K, k_pool.shape[0])
+class _StepState:
+    """The buffers and calls that do not depend on how the pages hold their keys and values."""
+
+    def __init__(self, B, L, Hq, Hkv, D, T, Pmax, K, n_phys, block_table, seq_len, num_splits, group_reduce, device):
+        self.shape = kvmm.make_shape(B, L, Hq, Hkv, D, T, Pmax, K, n_phys)
         self.K = K
         self.num_splits = num_splits
         self.group_reduce = group_reduce
-        self.k_pool, self.v_pool, self.block_table, self.seq_len = k_pool, v_pool, block_table, seq_len
+        self.block_table, self.seq_len = block_table, seq_len
         i32 = dict(dtype=torch.int32, device=device)
         self.meta = torch.zeros(B, L, Hkv, Pmax, 2, D, dtype=torch.bfloat16, device=device)
         self.sel_idx = torch.zeros(B, L, Hkv, K, **i32)
@@ -43,10 +46,38 @@ class DecodeState:
         self.total_promoted = torch.zeros(1, **i32)
         self.out = torch.zeros(L, B, Hq, D, dtype=torch.float32, device=device)
         self.lse = torch.zeros(L, B, Hq, dtype=torch.float32, device=device)
+        self.q_turned = torch.zeros(L, B, Hq, D, dtype=torch.bfloat16, device=device)
         self.err = torch.zeros(1, **i32)
         self.tok_begin = torch.zeros(B, **i32)
         self.tok_end = torch.zeros(B, **i32)
         self.workspace = kvmm.alloc_workspace(self.shape, num_splits, device=device)
+
+    def _step_rows(self, q, new_k, new_v):
+        """One token's rows [B, 1, H, D] from [B, H, D] or [B, 1, H, D] views; the token is at seq_len - 1 (a slot of
+        the batch with no sequence appends nothing)."""
+        torch.sub(self.seq_len, 1, out=self.tok_begin).clamp_(min=0)
+        return [t if t.dim() == 4 else t.unsqueeze(1) for t in (q, new_k, new_v)]
+
+    def select(self, layer, q, rescore_mask=None, scores_out=None) -> None:
+        kvmm.page_score_topk(self.shape, layer, q, self.meta, self.seq_len, rescore_mask, self.K, self.sel_idx,
+                             self.sel_cnt, self.workspace, self.err, scores_out=scores_out,
+                             group_reduce=self.group_reduce)
+
+    def diff(self, layer, rescore_mask=None, commit=True) -> None:
+        kvmm.topk_promotion_diff(self.shape, layer, rescore_mask, self.prev_idx, self.prev_cnt, self.sel_idx,
+                                 self.sel_cnt, self.promoted, self.promoted_cnt, self.evicted, self.evicted_cnt,
+                                 self.total_promoted, commit=commit, err=self.err)
+
+    def read_err(self) -> int:
+        return int(self.err.item())
+
+
+class DecodeState(_StepState):
+    def __init__(self, B, L, Hq, Hkv, D, T, Pmax, K, k_pool, v_pool, block_table, seq_len, num_splits=0,
+                 group_reduce=0, device="cuda"):
+        super().__init__(B, L, Hq, Hkv, D, T, Pmax, K, k_pool.shape[0], block_table, seq_len, num_splits, group_reduce,
+                         device)
+        self.k_pool, self.v_pool = k_pool, v_pool
 
     @classmethod
     def for_workload(cls, wl, K=None, **kw):
@@ -71,16 +102,6 @@ class DecodeState:
         torch.sub(self.seq_len, 1, out=self.tok_begin)
         kvmm.kv_minmax_update(self.shape, layer, new_k, new_v, 1, self.tok_begin, self.seq_len, self.k_pool,
                               self.v_pool, self.block_table, self.meta, self.err)
-
-    def select(self, layer, q, rescore_mask=None, scores_out=None) -> None:
-        kvmm.page_score_topk(self.shape, layer, q, self.meta, self.seq_len, rescore_mask, self.K, self.sel_idx,
-                             self.sel_cnt, self.workspace, self.err, scores_out=scores_out,
-                             group_reduce=self.group_reduce)
-
-    def diff(self, layer, rescore_mask=None, commit=True) -> None:
-        kvmm.topk_promotion_diff(self.shape, layer, rescore_mask, self.prev_idx, self.prev_cnt, self.sel_idx,
-                                 self.sel_cnt, self.promoted, self.promoted_cnt, self.evicted, self.evicted_cnt,
-                                 self.total_promoted, commit=commit, err=self.err)
 
     def attend(self, layer, q, sm_scale=0.0) -> None:
         kvmm.sparse_paged_decode_attn(self.shape, layer, q, self.k_pool, self.v_pool, self.block_table,
@@ -116,8 +137,60 @@ class DecodeState:
             self.diff(layer, rescore_mask)
             self.attend(layer, q)
 
-    def read_err(self) -> int:
-        return int(self.err.item())
+    def append_rope(self, layer, q, new_k, new_v, rope=None) -> None:
+        """One new token per batch entry at position seq_len - 1, its query and key rotated (``kvmm.Rope``):
+        q [B, Hq, D], new_k and new_v [B, Hkv, D] bf16 views; the turned query goes to ``q_turned[layer]``."""
+        q, new_k, new_v = self._step_rows(q, new_k, new_v)
+        kvmm.kv_append_rope(self.shape, layer, q, new_k, new_v, self.tok_begin, self.seq_len, self.k_pool, self.v_pool,
+                            self.block_table, self.meta, rope=rope, q_out=self.q_turned[layer], err=self.err)
+
+    def layer_step_rope(self, layer, q, new_k, new_v, rope=None, rescore_mask=None) -> None:
+        """One layer of one decode step from a projection's rows: rotate and append, select + attend, diff."""
+        self.append_rope(layer, q, new_k, new_v, rope)
+        self.select_attend(layer, self.q_turned[layer], rescore_mask)
+        self.diff(layer, rescore_mask)
+
+
+class Kv4DecodeState(_StepState):
+    """DecodeState over the 4-bit cache: ``kv4_pool`` [n_phys, page bytes] (``kvmm.alloc_kv4_pool``), one factor for
+    its keys and one for its values.  Prompts are appended with :meth:`append_prompt`, which also keeps the MinMax."""
+
+    def __init__(self, B, L, Hq, Hkv, D, T, Pmax, K, kv4_pool, block_table, seq_len, k_scale=1.0, v_scale=1.0,
+                 group_reduce=0, device="cuda"):
+        super().__init__(B, L, Hq, Hkv, D, T, Pmax, K, kv4_pool.shape[0], block_table, seq_len, 0, group_reduce, device)
+        self.kv4_pool, self.k_scale, self.v_scale = kv4_pool, k_scale, v_scale
+        self.kv4_workspace = kvmm.alloc_kv4_workspace(self.shape, device=device)
+
+    def append_prompt(self, layer, new_k, new_v, tok_begin, tok_end, rope=None, q=None, q_out=None) -> None:
+        """Tokens [tok_begin, tok_end) of every sequence from rows [B, n, H, D]."""
+        kvmm.kv4_append_rope(self.shape, layer, q, new_k, new_v, tok_begin, tok_end, self.kv4_pool, self.block_table,
+                             self.meta, rope=rope, q_out=q_out, k_scale=self.k_scale, v_scale=self.v_scale,
+                             err=self.err)
+
+    def gather(self, layer, k_out, v_out, tok_begin=None, tok_end=None) -> None:
+        """Tokens [tok_begin, tok_end) (default: the whole sequences) as bf16 rows [B, n_rows, Hkv, D]."""
+        kvmm.kv4_gather(self.shape, layer, self.kv4_pool, self.block_table, tok_begin,
+                        self.seq_len if tok_end is None else tok_end, k_out, v_out, k_scale=self.k_scale,
+                        v_scale=self.v_scale, err=self.err)
+
+    def append_rope(self, layer, q, new_k, new_v, rope=None) -> None:
+        """As DecodeState.append_rope."""
+        q, new_k, new_v = self._step_rows(q, new_k, new_v)
+        self.append_prompt(layer, new_k, new_v, self.tok_begin, self.seq_len, rope, q, self.q_turned[layer])
+
+    def attend(self, layer, q, sm_scale=0.0, every_page=False) -> None:
+        """Attention over the kept selections, or over every page."""
+        kvmm.sparse_paged_decode_attn_kv4(self.shape, layer, q, self.kv4_pool, self.block_table, self.seq_len,
+                                          None if every_page else self.sel_idx, None if every_page else self.sel_cnt,
+                                          self.out[layer], self.kv4_workspace, lse=self.lse[layer], err=self.err,
+                                          k_scale=self.k_scale, v_scale=self.v_scale, sm_scale=sm_scale)
+
+    def layer_step_rope(self, layer, q, new_k, new_v, rope=None, rescore_mask=None) -> None:
+        """One layer of one decode step: rotate and append, select, diff, attend."""
+        self.append_rope(layer, q, new_k, new_v, rope)
+        self.select(layer, self.q_turned[layer], rescore_mask)
+        self.diff(layer, rescore_mask)
+        self.attend(layer, self.q_turned[layer])
 
 
 class StabilityProfiler:
