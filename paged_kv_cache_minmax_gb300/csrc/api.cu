@@ -1024,8 +1024,8 @@ kvmm_status sparse_paged_decode_attn_kv4(const kvmm_shape* shape, int32_t layer,
     p.sel_cnt = sel_cnt;
     p.out = out;
     p.lse = lse;
-    p.pre = static_cast<int32_t*>(workspace);
-    p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kvmm::kKv4PreBytes);
+    p.counter = static_cast<int32_t*>(workspace);
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kvmm::kKv4CounterBytes);
     p.err = err;
     return launched(kvmm::launch_kv4_attention(p, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -307,7 +307,8 @@ struct GatherParams {
 // sparse_paged_decode_attn_kv4 (kv4_attn.cu)
 struct Kv4AttnParams {
     int32_t B, L, Hq, Hkv, G, D, T, Pmax, Kmax, layer;
-    int32_t u0, nu;  // the (batch, KV head) units of this launch: u0 .. u0 + nu - 1
+    int32_t b0, nb;  // the batch entries of this launch: b0 .. b0 + nb - 1
+    int32_t C;       // CTAs a unit (a cluster each); 0: the pages of all units are dealt evenly to the CTAs
     int32_t early;   // 1: seq_len and the table may be read before the preceding kernel has finished
     int64_t n_phys;
     float scale_log2;  // sm_scale * k_scale * log2(e)
@@ -320,15 +321,16 @@ struct Kv4AttnParams {
     const int32_t* sel_cnt;
     float* out;
     float* lse;
-    float* partial;  // workspace: two partial results for each CTA
-    int32_t* pre;    // workspace: the units' first pages in the launch's page order, then their sum
+    int32_t* counter;  // workspace: for each CTA, the parts stored of the unit that begins in it and goes on (zero between calls)
+    float* partial;    // workspace: two partial results for each CTA
     int32_t* err;
 };
-constexpr int kKv4MaxUnits = 2048;  // units of one launch (their page counts are summed in shared memory)
-constexpr int kKv4MaxCtas = 256;    // CTAs of one launch
-constexpr size_t kKv4PreBytes = (kKv4MaxUnits + 1) * sizeof(int32_t) + 252;  // a multiple of 256
+constexpr int kKv4MaxBatch = 1024;  // batch entries of one launch (their page counts are summed in shared memory)
+constexpr int kKv4MaxCtas = 256;    // CTAs of one launch that deals the pages evenly
+constexpr int kKv4MaxCluster = 16;  // CTAs of one unit
+constexpr size_t kKv4CounterBytes = kKv4MaxCtas * sizeof(int32_t);
 __host__ __device__ constexpr size_t kv4_partial_floats(int D) { return size_t(8) * D + 16; }  // unnormalised output, then (m, l) of 8 heads
-inline size_t kv4_ws_bytes(int D) { return kKv4PreBytes + size_t(kKv4MaxCtas) * 2 * kv4_partial_floats(D) * sizeof(float); }
+inline size_t kv4_ws_bytes(int D) { return kKv4CounterBytes + size_t(kKv4MaxCtas) * 2 * kv4_partial_floats(D) * sizeof(float); }
 
 cudaError_t launch_append_rope(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_gather(const GatherParams& p, cudaStream_t stream);

@@ -6,16 +6,19 @@
 // in one pass with a running reference m (sm_scale, k_scale and log2(e) are one
 // factor on z; v_scale is applied to the result).
 //
-// Work.  The pages of all units form one list; CTA c of the N launched (one for
-// each SM) takes the c-th of N equal pieces of it, whatever the sequences'
-// lengths, so there is no tail of long sequences and no more than one wave.
-// Every CTA sums the units' page counts itself to find its piece.  The warps
-// of a CTA take its pages in turn, each through a private ring of slots filled
-// by one bulk copy a page, and run ahead across unit boundaries.  Where a
-// unit ends (or the piece does), the warps' partial results are merged in
-// shared memory; a unit that lies in one CTA is written out at once, the
-// parts of others (two a CTA at most: its first and last unit) go through the
-// workspace to a second, small launch.
+// Work.  With selections and no more units than SMs, each unit has a cluster of
+// CTAs (as many as all run at once), which share its Kmax places and merge their
+// parts through distributed shared memory.  Else the pages of all units form one
+// list (with selections, Kmax places a unit) and CTA c of the N launched, one for
+// each SM, takes the c-th of N equal pieces of it, whatever the sequences'
+// lengths, so there is one wave without a tail.  Sixteen warps take a CTA's pages
+// in turn, two pages of 16 tokens or one of 32 a step, each through a private
+// ring of steps filled by one bulk copy a page (with the L2 policy of data read
+// once), running ahead across unit boundaries.  Where a unit ends (or the piece
+// does) the warps' partial results are merged in shared memory.  A unit that lies
+// in one CTA is written out at once; the parts of the others (two a CTA at most:
+// its first and its last unit) go to the workspace, and the CTA that stores a
+// unit's last part, as a counter tells it, combines them.
 //
 // A 16-token tile.  S^T[16 tok x 8 head] = K[16 x D] Q^T and O^T[D x 8] +=
 // V^T[D x 16] P^T on mma.sync m16n8k16 in fp16, fp32 accumulation: a group of
@@ -38,6 +41,7 @@
 //   - Tokens are visited in the order r ^ ((r >> 1) & 1) within eight, which
 //     lets the K rows of a load fall on different banks and leaves V two ways.
 // Launched with programmatic dependent launch.
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -50,22 +54,31 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-__host__ __device__ constexpr int ring_depth(int D, int T) { return D * T <= 64 * 16 ? 6 : D * T <= 128 * 16 ? 4 : 2; }
+constexpr int kStep = 32;                      // tokens of a step: two pages of 16, or one of 32
+constexpr uint64_t kWaitNs = 1000000000ull;    // far beyond any legitimate wait
+__host__ __device__ constexpr int ring_depth(int D) { return D == 64 ? 4 : 2; }  // steps in flight a warp
+__host__ __device__ constexpr int step_bytes(int D) { return kStep * (D + D / 8); }
 
 struct Shared {
-    uint64_t bar[kWarps][6];
-    float m[kWarps][8];
+    uint64_t full[kWarps][4];  // a step has landed
+    int2 meta[kWarps][4];      // per tile of the step: unit * 64 + valid tokens
+    float m[kWarps][8];        // each warp's (in the final merge: each group's) reference and sum per head
     float l[kWarps][8];
+    float f[kWarps][8];        // weight of each warp's partial
+    float ref[8], sum[8];      // the CTA's reference and sum per head
     int scan[kWarps];
+    int last[2];
+    float recv[8 * 128 + kKv4MaxCluster];  // received: every CTA's partial of this CTA's slice of the outputs
+    float rstat[kKv4MaxCluster][16];       // received: (reference, sum) per head of every CTA of the cluster
 };
 
-// dynamic shared memory: [rings][partials: kWarps x G x (D + 4) floats][pre: nu + 1 ints]
-__host__ __device__ inline size_t part_offset(int D, int T) { return size_t(kWarps) * ring_depth(D, T) * T * (D + D / 8); }
-__host__ __device__ inline size_t pre_offset(int D, int T, int G)
+// dynamic shared memory: [rings][partials: kWarps x G x (D + 4) floats][first pages and page counts of the batch]
+__host__ __device__ constexpr size_t part_offset(int D) { return size_t(kWarps) * ring_depth(D) * step_bytes(D); }
+__host__ __device__ inline size_t list_offset(int D, int G)
 {
-    return part_offset(D, T) + size_t(kWarps) * G * (D + 4) * sizeof(float);
+    return part_offset(D) + size_t(kWarps) * G * (D + 4) * sizeof(float);
 }
-inline size_t smem_bytes(int D, int T, int G, int nu) { return pre_offset(D, T, G) + size_t(nu + 1) * sizeof(int); }
+inline size_t smem_bytes(int D, int G, int nb) { return list_offset(D, G) + size_t(2 * nb + 1) * sizeof(int); }
 
 __device__ __forceinline__ float fast_exp2(float x)
 {
@@ -74,11 +87,17 @@ __device__ __forceinline__ float fast_exp2(float x)
     return y;
 }
 
-// first page of CTA c's piece of `total` pages dealt to n CTAs
-__host__ __device__ __forceinline__ int piece_start(int total, int c, int n)
-{
-    return static_cast<int>(static_cast<long long>(total) * c / n);
-}
+// `total` pages dealt to n CTAs: the first total % n take one more than the others
+struct Pieces {
+    int each, more;
+    __device__ __forceinline__ Pieces(int total, int n) : each(total / n), more(total % n) {}
+    __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int owner(int f) const  // the CTA that takes page f
+    {
+        const int long_pages = more * (each + 1);
+        return f < long_pages ? f / (each + 1) : more + (f - long_pages) / each;  // f < total: each > 0 there
+    }
+};
 
 __device__ __forceinline__ int clamped_seq(const Kv4AttnParams& p, int b, bool tell)
 {
@@ -91,169 +110,249 @@ __device__ __forceinline__ int clamped_seq(const Kv4AttnParams& p, int b, bool t
     return seq;
 }
 
+// The launch's page list: Kmax places a unit (selections), or the pages of every batch entry's sequence, head after
+// head.  Units count from the launch's first batch entry.
+struct List {
+    const int* first;  // every page: the first page of each batch entry, and the total
+    const int* count;  // ... and its pages
+    int per, Hkv, nb;  // selections: places a unit (0: every page)
+    __device__ __forceinline__ int batch_of(int f) const  // the last entry that starts at or before page f
+    {
+        int a = 0, z = nb - 1;
+        while (a < z) {
+            const int m = (a + z + 1) >> 1;
+            if (first[m] <= f) a = m;
+            else z = m - 1;
+        }
+        return a;
+    }
+    __device__ __forceinline__ int unit_of(int f) const
+    {
+        if (per) return f / per;
+        const int b = batch_of(f);
+        return b * Hkv + (f - first[b]) / count[b];
+    }
+    __device__ __forceinline__ void range(int u, int& beg, int& end) const
+    {
+        if (per) {
+            beg = u * per;
+            end = beg + per;
+        } else {
+            const int b = u / Hkv, n = count[b];
+            beg = first[b] + (u - b * Hkv) * n;
+            end = beg + n;
+        }
+    }
+};
+
 template <int D, int T, bool DUP>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnParams p)
 {
     using Page = Kv4Page<D, T>;
-    constexpr int kDepth = ring_depth(D, T);
-    constexpr int kWords = D / 32;   // code words of a lane's K row: its 4 * kWords * 2 channels
+    constexpr int kDepth = ring_depth(D);
+    constexpr int kPages = kStep / T;  // pages of a step
+    constexpr int kSlot = step_bytes(D);
+    static_assert(kSlot == kPages * Page::kBytes, "a slot holds whole pages");
+    constexpr int kWords = D / 32;   // code words of a lane's K row
     constexpr int kTiles = D / 16;   // m-tiles of O^T
     constexpr int kMine = D / 8;     // output channels of a lane's row group
     constexpr int kVWords = D / 64;  // code words of a lane's V token
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int gid = lane >> 2, tig = lane & 3;
     const int G = p.G;
     const int N = gridDim.x, rank = blockIdx.x;
-    uint8_t* ring = smem + static_cast<size_t>(warp) * kDepth * Page::kBytes;
-    float* part = reinterpret_cast<float*>(smem + part_offset(D, T));
-    int* pre = reinterpret_cast<int*>(smem + pre_offset(D, T, G));
+    float* part = reinterpret_cast<float*>(smem + part_offset(D));
+    int* first = reinterpret_cast<int*>(smem + list_offset(D, G));
+    int* count = first + p.nb + 1;
 
-    if (tid < kWarps * kDepth) mbar_init(&sh.bar[tid / kDepth][tid % kDepth], 1);
-    fence_barrier_init();
+    if (tid < kWarps * kDepth) {
+        mbar_init(&sh.full[tid / kDepth][tid % kDepth], kPages);
+        fence_barrier_init();
+    }
+    __syncwarp();  // converged for the aligned barrier
+    if (p.C > 1) cluster_arrive();  // passed before anything reaches another CTA
     pdl_wait_then_release();
 
-    // ---- the units' first pages in the launch's page list ----------------------------------------------------
-    int total = 0;
-    for (int base = 0; base < p.nu; base += kThreads) {
-        const int i = base + tid;
-        int n = 0;
-        if (i < p.nu) {
-            const int u = p.u0 + i, b = u / p.Hkv, h = u - b * p.Hkv;
-            if (p.sel_cnt != nullptr) {
-                n = p.sel_cnt[(static_cast<size_t>(b) * p.L + p.layer) * p.Hkv + h];
-                if (n < 0 || n > p.Kmax) {
-                    if (rank == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
-                    n = n < 0 ? 0 : p.Kmax;
-                }
-            } else {
-                n = (clamped_seq(p, b, rank == 0 && h == 0) + T - 1) / T;
-            }
-        }
-        int inc = n;
+    // ---- the page list and this CTA's piece of it ------------------------------------------------------------
+    int total;
+    if (p.sel_idx != nullptr) {
+        total = p.nb * p.Hkv * p.Kmax;
+        __syncthreads();  // the barriers exist
+    } else {
+        total = 0;
+        for (int base = 0; base < p.nb; base += kThreads) {
+            const int i = base + tid;
+            int n = 0, inc;
+            if (i < p.nb) n = (clamped_seq(p, p.b0 + i, rank == 0) + T - 1) / T;
+            inc = n * p.Hkv;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(kFullMask, inc, off);
-            if (lane >= off) inc += o;
-        }
-        if (lane == 31) sh.scan[warp] = inc;
-        __syncthreads();
-        int before = total, sum = 0;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(kFullMask, inc, off);
+                if (lane >= off) inc += o;
+            }
+            if (lane == 31) sh.scan[warp] = inc;
+            __syncthreads();
+            int before = total;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const int s = sh.scan[w];
-            if (w < warp) before += s;
-            sum += s;
+            for (int w = 0; w < kWarps; ++w) {
+                const int v = sh.scan[w];
+                if (w < warp) before += v;
+                total += v;
+            }
+            if (i < p.nb) {
+                first[i] = before + inc - n * p.Hkv;
+                count[i] = n;
+            }
+            if (p.nb > base + kThreads) __syncthreads();
         }
-        if (i < p.nu) pre[i] = before + inc - n;
-        total += sum;
+        if (tid == 0) first[p.nb] = total;
         __syncthreads();
+        // sequences without a token: their results are written here, spread over the CTAs
+        for (int b = rank; b < p.nb; b += N) {
+            if (count[b] != 0) continue;
+            float* o = p.out + static_cast<size_t>(p.b0 + b) * p.Hq * D;
+            for (int e = tid; e < p.Hq * D; e += kThreads) o[e] = 0.f;
+            if (p.lse)
+                for (int e = tid; e < p.Hq; e += kThreads) p.lse[static_cast<size_t>(p.b0 + b) * p.Hq + e] = -INFINITY;
+        }
     }
-    if (tid == 0) pre[p.nu] = total;
-    __syncthreads();
-    if (rank == 0)
-        for (int i = tid; i <= p.nu; i += kThreads) p.pre[i] = pre[i];
-    // units without a page: their results are written here, spread over the CTAs
-    for (int i = rank * kWarps + warp; i < p.nu; i += N * kWarps) {
-        if (pre[i + 1] != pre[i]) continue;
-        const int u = p.u0 + i;
-        float* o = p.out + static_cast<size_t>(u) * G * D;
-        for (int e = lane; e < G * D; e += 32) o[e] = 0.f;
-        if (p.lse && lane < G) p.lse[static_cast<size_t>(u) * G + lane] = -INFINITY;
+    const List list{first, count, p.sel_idx != nullptr ? p.Kmax : 0, p.Hkv, p.nb};
+    const Pieces pieces(total, N);
+    int lo, hi;
+    if (p.C > 0) {  // a unit's places dealt to its C CTAs
+        const int u = rank / p.C, c = rank - u * p.C;
+        lo = u * p.Kmax + p.Kmax * c / p.C;  // (Kmax <= 32768, C <= 16)
+        hi = u * p.Kmax + p.Kmax * (c + 1) / p.C;  // > lo: C <= Kmax
+    } else {
+        lo = pieces.start(rank);
+        hi = pieces.start(rank + 1);
+        if (lo >= hi) return;
     }
-    const int lo = piece_start(total, rank, N), hi = piece_start(total, rank + 1, N);
-    if (lo >= hi) return;
-    // the last unit that starts at or before a page of the list (empty units share their start with the next)
-    auto unit_of = [&](int f) {
-        int a = 0, z = p.nu - 1;
-        while (a < z) {
-            const int m = (a + z + 1) >> 1;
-            if (pre[m] <= f) a = m;
-            else z = m - 1;
-        }
-        return a;
-    };
 
-    // ---- this warp's pages: lo + warp, lo + warp + kWarps, ... ------------------------------------------------
-    int next = lo + warp;        // first page of the batch not looked up yet
-    unsigned mask = 0u;          // pages of the batch not issued yet; lane i holds the i-th one's entry
-    int e_phys = 0, e_nv = 0, e_u = 0;
-    int issued = 0, consumed = 0;
-    int s_nv = 0, s_u = 0;       // lane s: valid tokens and unit of the page in slot s
-    const uint64_t policy = l2_policy_evict_first();
-    auto look_up = [&]() {
-        const int f = next + kWarps * lane;
-        e_phys = -1;
-        if (f < hi) {
-            e_u = unit_of(f);
-            const int u = p.u0 + e_u, b = u / p.Hkv, h = u - b * p.Hkv;
-            const size_t unit = (static_cast<size_t>(b) * p.L + p.layer) * p.Hkv + h;
-            const int i = f - pre[e_u];
-            const int seq = clamped_seq(p, b, false);
-            const int lp = p.sel_idx != nullptr ? p.sel_idx[unit * p.Kmax + i] : i;
-            if (lp < 0 || lp >= (seq + T - 1) / T) {
-                report(p.err, KVMM_ERR_OUT_OF_RANGE);
-            } else {
-                const int32_t phys = p.block_table[unit * p.Pmax + lp];
-                if (phys < 0 || phys >= p.n_phys) report(p.err, phys < 0 ? KVMM_ERR_NULL_BLOCK : KVMM_ERR_OUT_OF_RANGE);
-                else e_phys = phys;
-                e_nv = min(T, seq - lp * T);
-            }
-        }
-        mask = __ballot_sync(kFullMask, e_phys >= 0);
-        next += kWarps * 32;
-    };
-    auto fill = [&]() {  // issue pages while slots are free
-        while (issued - consumed < kDepth) {
-            while (mask == 0u) {
-                if (next >= hi) return;
-                look_up();
-            }
-            const int src = __ffs(mask) - 1;
-            mask &= mask - 1u;
-            const int phys = __shfl_sync(kFullMask, e_phys, src);
-            const int nv = __shfl_sync(kFullMask, e_nv, src);
-            const int u = __shfl_sync(kFullMask, e_u, src);
-            const int slot = issued % kDepth;
-            if (lane == slot) {
-                s_nv = nv;
-                s_u = u;
-            }
-            if (lane == 0) {
-                uint64_t* bar = &sh.bar[warp][slot];
-                mbar_arrive_expect_tx(bar, Page::kBytes);
-                bulk_copy_g2s_hint(ring + slot * Page::kBytes, p.kv4_pool + static_cast<size_t>(phys) * Page::kBytes,
-                                   Page::kBytes, bar, policy);
-            }
-            ++issued;
-        }
-    };
-    fill();
-
-    const int head = DUP ? (gid & 3) : gid;  // the query head of this lane's column
-    const int col0 = DUP ? ((2 * tig) & 3) : 2 * tig;  // ... and of its two accumulator columns: col0, col0 + 1
+    const int gid = lane >> 2, tig = lane & 3;
+    const int head = DUP ? (gid & 3) : gid;            // the query head of this lane's column
+    const int col0 = DUP ? ((2 * tig) & 3) : 2 * tig;  // the heads of its accumulator columns: col0, col0 + 1
     const int ra = gid ^ ((gid >> 1) & 1);   // the tokens of this lane's K rows: ra and ra + 8
     const int t0 = (2 * tig) ^ (tig & 1), t1 = t0 ^ 1;  // ... and of its V pairs: (t0, t1) and (t0 + 8, t1 + 8)
-    bool dead = false;  // a copy never arrived: this warp takes no more pages
-    int dead_at = 0;
+    const float lo_lane = tig < 2 ? 0.f : -1.f;  // G <= 4: the lanes whose columns carry the lo parts
+    // the queries of the first unit are on their way while the pages are looked up
+    const int first_unit = list.unit_of(lo);
+    uint4 qv[D / 32];
+    auto load_queries = [&](int u) {
+        const kvmm_bf16* qh = p.q + ((static_cast<size_t>(p.b0) * p.Hkv + u) * G + head) * D + tig * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            qv[i] = head < G ? reinterpret_cast<const uint4*>(qh)[i] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    load_queries(first_unit);
 
-    for (int u = unit_of(lo); u < p.nu && pre[u] < hi; ++u) {
-        const int ubeg = pre[u], uend = pre[u + 1];
-        if (uend == ubeg) continue;
+    // ---- this warp's steps: round r is pages lo + r * kStride + kPages * warp .. + kPages - 1 --------------------
+    constexpr int kStride = kWarps * kPages;
+    constexpr int kBatch = 32 / kPages;  // rounds looked up at once, a page a lane
+    uint8_t* ring = smem + static_cast<size_t>(warp) * kDepth * kSlot;
+    const int my_first = lo + kPages * warp;
+    const int rounds = my_first < hi ? (hi - my_first + kStride - 1) / kStride : 0;
+    const uint64_t policy = l2_policy_evict_first();
+    // A page's entry takes two dependent loads (its place in the selection, its table entry): place() starts the
+    // first, entry() takes it and starts the second, and a batch's run one and two batches ahead of its copies.
+    int pl_lp, pl_cnt, pl_seq, pl_u, pl_i;  // place(): logical page, pages of the unit, tokens, unit, place in it
+    auto place = [&](int rb) {
+        const int f = my_first + (rb + lane / kPages) * kStride + lane % kPages;
+        pl_u = -1;
+        if (f >= hi || f < my_first) return;
+        int b, h;
+        if (p.sel_idx != nullptr) {
+            pl_u = f / p.Kmax;
+            pl_i = f - pl_u * p.Kmax;
+            b = pl_u / p.Hkv;
+            h = pl_u - b * p.Hkv;
+            const size_t unit = (static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + h;
+            pl_cnt = p.sel_cnt[unit];
+            pl_lp = p.sel_idx[unit * p.Kmax + pl_i];
+        } else {
+            b = list.batch_of(f);
+            pl_cnt = count[b];
+            h = (f - first[b]) / pl_cnt;
+            pl_i = pl_lp = f - first[b] - h * pl_cnt;
+            pl_u = b * p.Hkv + h;
+        }
+        pl_seq = p.seq_len[p.b0 + b];
+    };
+    int en_phys, en_meta;  // entry(): physical page, unit * 64 + valid tokens (none: nothing to copy)
+    auto entry = [&]() {
+        en_phys = 0;
+        en_meta = 0x7fffffc0;  // behind the piece: after every unit
+        if (pl_u < 0) return;
+        en_meta = pl_u * 64;
+        const int cap = p.Pmax * T;
+        if (p.sel_idx != nullptr && pl_i == 0 && (pl_cnt < 0 || pl_cnt > p.Kmax || pl_seq < 0 || pl_seq > cap))
+            report(p.err, KVMM_ERR_OUT_OF_RANGE);  // (the sum of the page counts has told the others)
+        const int seq = min(max(pl_seq, 0), cap);
+        if (pl_i >= pl_cnt) return;
+        if (pl_lp < 0 || pl_lp >= (seq + T - 1) / T) {
+            report(p.err, KVMM_ERR_OUT_OF_RANGE);
+            return;
+        }
+        en_meta += min(T, seq - pl_lp * T);
+        const int b = pl_u / p.Hkv;
+        en_phys = p.block_table[((static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + (pl_u - b * p.Hkv)) * p.Pmax + pl_lp];
+    };
+    int phys = 0, pmeta = 0;  // the batch being issued
+    auto issue = [&](int r) {  // start the copies of round r
+        if (r % kBatch == 0) {
+            phys = en_phys;
+            pmeta = en_meta;
+            if ((pmeta & 63) != 0 && (phys < 0 || phys >= p.n_phys)) {
+                report(p.err, phys < 0 ? KVMM_ERR_NULL_BLOCK : KVMM_ERR_OUT_OF_RANGE);
+                pmeta &= ~63;
+            }
+            entry();
+            place(r + 2 * kBatch);
+        }
+        if (lane / kPages == r % kBatch) {
+            const int slot = r % kDepth, tile = lane % kPages;
+            uint64_t* bar = &sh.full[warp][slot];
+            int* meta = reinterpret_cast<int*>(&sh.meta[warp][slot]);
+            const int nv = pmeta & 63;
+            if (kPages == 2) {
+                meta[tile] = pmeta;
+            } else {
+                meta[0] = pmeta - nv + min(nv, 16);
+                meta[1] = pmeta - nv + max(nv - 16, 0);
+            }
+            mbar_arrive_expect_tx(bar, nv > 0 ? Page::kBytes : 0);
+            if (nv > 0)
+                bulk_copy_g2s_hint(ring + slot * kSlot + tile * Page::kBytes,
+                                   p.kv4_pool + static_cast<size_t>(phys) * Page::kBytes, Page::kBytes, bar, policy);
+        }
+    };
+    place(0);
+    entry();
+    place(kBatch);
+#pragma unroll
+    for (int r = 0; r < kDepth; ++r)
+        if (r < rounds) issue(r);
+
+    int r = 0;
+    int seg_unit[2] = {-1, -1};  // units whose parts this CTA stores: the one that began before, the one that goes on
+
+    for (int u = first_unit;; ++u) {
+        int ubeg, uend;
+        list.range(u, ubeg, uend);
+        if (uend == ubeg) {  // an empty sequence
+            if (u + 1 >= p.nb * p.Hkv) break;
+            continue;
+        }
+        if (u != first_unit) load_queries(u);
         // queries: halves of the lane's channels of its head, scaled by a power of two
         uint32_t qf[2 * kTiles];
         float zf0, zf1;
         {
-            const kvmm_bf16* qh = p.q + (static_cast<size_t>(p.u0 + u) * G + head) * D + tig * (D / 4);
-            uint4 v[D / 32];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-                v[i] = head < G ? reinterpret_cast<const uint4*>(qh)[i] : make_uint4(0u, 0u, 0u, 0u);
             float mx = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
             }
@@ -266,129 +365,149 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * p.scale_log2;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) qf[4 * i + k] = pack_half2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
             }
-            zf0 = __shfl_sync(kFullMask, down, 4 * (col0));
-            zf1 = __shfl_sync(kFullMask, down, 4 * (col0 + 1));
+            // > 0: a masked score of -inf stays -inf under it
+            zf0 = fmaxf(__shfl_sync(kFullMask, down, 4 * col0), FLT_MIN);
+            zf1 = fmaxf(__shfl_sync(kFullMask, down, 4 * (col0 + 1)), FLT_MIN);
         }
 
         float o[kTiles][4];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-
-        while (issued > consumed && __shfl_sync(kFullMask, s_u, consumed % kDepth) == u) {
-            const int slot = consumed % kDepth;
-            const int nv = __shfl_sync(kFullMask, s_nv, slot);
-            const uint8_t* pg = ring + slot * Page::kBytes;
-            if (!dead) {
-                const bool ok = mbar_wait_bounded(&sh.bar[warp][slot], (consumed / kDepth) & 1);
-                if (__any_sync(kFullMask, !ok)) {  // warp-uniform; the remaining pages are dropped
-                    dead = true;
-                    dead_at = consumed;
-                    if (lane == 0) report(p.err, KVMM_ERR_TIMEOUT);
-                }
+        while (r < rounds) {
+            const int slot = r % kDepth;
+            if (__any_sync(kFullMask, !mbar_wait_bounded(&sh.full[warp][slot], (r / kDepth) & 1, kWaitNs))) {
+                if (lane == 0) report(p.err, KVMM_ERR_TIMEOUT);  // the remaining pages are dropped
+                for (int k = r; k < min(rounds, r + kDepth); ++k)  // what is in flight lands before the CTA leaves
+                    mbar_wait_bounded(&sh.full[warp][k % kDepth], (k / kDepth) & 1, 100000000ull);
+                __syncwarp();
+                r = rounds;
+                break;
             }
-            if (!dead) {
+            const int2 meta = sh.meta[warp][slot];
+            if ((meta.x >> 6) > u) break;  // of a later unit
+            int nv[2] = {(meta.x >> 6) == u ? meta.x & 63 : 0, (meta.y >> 6) == u ? meta.y & 63 : 0};
+            const uint8_t* pg = ring + slot * kSlot;
+            if (kPages == 2 && nv[0] == 0) {  // the first page is of the unit before, or could not be read
+                pg += Page::kBytes;
+                nv[0] = nv[1];
+                nv[1] = 0;
+            }
+            if (nv[0] > 0) {
+                // tile j: tokens 16j .. 16j + 15 of the step, in page j (or the second half of the page)
+                auto tile_at = [&](int j) { return kPages == 2 ? pg + j * Page::kBytes : pg; };
+                constexpr int kRow1 = kPages == 2 ? 0 : 16;  // the second tile's first row in its page
+                const bool two = nv[1] != 0;
+                const bool full = nv[0] + nv[1] == 32;
+                // ---- scores before their factor: x[j] = token ra of tile j with heads col0, col0 + 1, then token ra + 8
+                float x[2][4];
 #pragma unroll
-                for (int j = 0; j < T; j += 16) {
-                    if (j >= nv) break;
-                    const bool full = nv - j >= 16;
-                    // ---- scores ----------------------------------------------------------------------------
-                    float c[2][4] = {};
-                    {
-                        const uint8_t* ka = pg + (j + ra) * Page::kRow + tig * (D / 8);
-                        const uint8_t* kb = ka + 8 * Page::kRow;
-                        uint32_t wa[kWords], wb[kWords], sa[kWords], sb[kWords];
-                        if (D == 128) {
-                            const uint4 x = ld_shared_v4(ka), y = ld_shared_v4(kb);
-                            wa[0] = x.x, wa[1] = x.y, wa[kWords - 2] = x.z, wa[kWords - 1] = x.w;
-                            wb[0] = y.x, wb[1] = y.y, wb[kWords - 2] = y.z, wb[kWords - 1] = y.w;
-                            // scale groups 2 tig and 2 tig + 1
-                            const uint8_t* sc = pg + Page::kKeyScales + (j + ra) * Page::kGroups + 2 * tig;
-                            const uint32_t ha = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sc));
-                            const uint32_t hb = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sc + 8 * Page::kGroups));
-                            sa[0] = sa[1] = prmt(ha, ha, 0x1010);
-                            sa[kWords - 2] = sa[kWords - 1] = prmt(ha, ha, 0x3232);
-                            sb[0] = sb[1] = prmt(hb, hb, 0x1010);
-                            sb[kWords - 2] = sb[kWords - 1] = prmt(hb, hb, 0x3232);
-                        } else {
-                            const uint2 x = ld_shared_v2(ka), y = ld_shared_v2(kb);
-                            wa[0] = x.x, wa[1] = x.y, wb[0] = y.x, wb[1] = y.y;
-                            const uint8_t* sc = pg + Page::kKeyScales + (j + ra) * Page::kGroups + tig;
-                            const uint32_t h = e4m3x2_to_half2(sc[0] | (static_cast<uint32_t>(sc[8 * Page::kGroups]) << 8));
-                            sa[0] = sa[1] = prmt(h, h, 0x1010);
-                            sb[0] = sb[1] = prmt(h, h, 0x3232);
-                        }
-#pragma unroll
-                        for (int w = 0; w < kWords; ++w) {
-                            mma_f16_16816(c[0], half2_mul(e2m1x2_to_half2<0>(wa[w]), sa[w]),
-                                          half2_mul(e2m1x2_to_half2<0>(wb[w]), sb[w]),
-                                          half2_mul(e2m1x2_to_half2<1>(wa[w]), sa[w]),
-                                          half2_mul(e2m1x2_to_half2<1>(wb[w]), sb[w]), qf[4 * w], qf[4 * w + 1]);
-                            mma_f16_16816(c[1], half2_mul(e2m1x2_to_half2<2>(wa[w]), sa[w]),
-                                          half2_mul(e2m1x2_to_half2<2>(wb[w]), sb[w]),
-                                          half2_mul(e2m1x2_to_half2<3>(wa[w]), sa[w]),
-                                          half2_mul(e2m1x2_to_half2<3>(wb[w]), sb[w]), qf[4 * w + 2], qf[4 * w + 3]);
-                        }
+                for (int j = 0; j < 2; ++j) {
+                    if (j == 1 && !two) {
+                        x[1][0] = x[1][1] = x[1][2] = x[1][3] = -INFINITY;
+                        break;
                     }
-                    // x: token ra with heads col0, col0 + 1, then token ra + 8
-                    float x[4] = {(c[0][0] + c[1][0]) * zf0, (c[0][1] + c[1][1]) * zf1, (c[0][2] + c[1][2]) * zf0,
-                                  (c[0][3] + c[1][3]) * zf1};
+                    float c[4] = {};
+                    const uint8_t* base = tile_at(j);
+                    const int row = j * kRow1 + ra;
+                    const uint8_t* ka = base + row * Page::kRow + tig * (D / 8);
+                    const uint8_t* kb = ka + 8 * Page::kRow;
+                    uint32_t wa[kWords], wb[kWords], sa[kWords], sb[kWords];
+                    if (D == 128) {
+                        const uint4 y = ld_shared_v4(ka), z = ld_shared_v4(kb);
+                        wa[0] = y.x, wa[1] = y.y, wa[kWords - 2] = y.z, wa[kWords - 1] = y.w;
+                        wb[0] = z.x, wb[1] = z.y, wb[kWords - 2] = z.z, wb[kWords - 1] = z.w;
+                        // scale groups 2 tig and 2 tig + 1
+                        const uint8_t* sc = base + Page::kKeyScales + row * Page::kGroups + 2 * tig;
+                        const uint32_t ha = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sc));
+                        const uint32_t hb = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sc + 8 * Page::kGroups));
+                        sa[0] = sa[1] = prmt(ha, ha, 0x1010);
+                        sa[kWords - 2] = sa[kWords - 1] = prmt(ha, ha, 0x3232);
+                        sb[0] = sb[1] = prmt(hb, hb, 0x1010);
+                        sb[kWords - 2] = sb[kWords - 1] = prmt(hb, hb, 0x3232);
+                    } else {
+                        const uint2 y = ld_shared_v2(ka), z = ld_shared_v2(kb);
+                        wa[0] = y.x, wa[1] = y.y, wb[0] = z.x, wb[1] = z.y;
+                        const uint8_t* sc = base + Page::kKeyScales + row * Page::kGroups + tig;
+                        const uint32_t hs = e4m3x2_to_half2(sc[0] | (static_cast<uint32_t>(sc[8 * Page::kGroups]) << 8));
+                        sa[0] = sa[1] = prmt(hs, hs, 0x1010);
+                        sb[0] = sb[1] = prmt(hs, hs, 0x3232);
+                    }
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        mma_f16_16816(c, half2_mul(e2m1x2_to_half2<0>(wa[w]), sa[w]),
+                                      half2_mul(e2m1x2_to_half2<0>(wb[w]), sb[w]),
+                                      half2_mul(e2m1x2_to_half2<1>(wa[w]), sa[w]),
+                                      half2_mul(e2m1x2_to_half2<1>(wb[w]), sb[w]), qf[4 * w], qf[4 * w + 1]);
+                        mma_f16_16816(c, half2_mul(e2m1x2_to_half2<2>(wa[w]), sa[w]),
+                                      half2_mul(e2m1x2_to_half2<2>(wb[w]), sb[w]),
+                                      half2_mul(e2m1x2_to_half2<3>(wa[w]), sa[w]),
+                                      half2_mul(e2m1x2_to_half2<3>(wb[w]), sb[w]), qf[4 * w + 2], qf[4 * w + 3]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[j][i] = c[i];
                     if (!full) {  // selected, not multiplied: what the page holds there may be anything
-                        if (j + ra >= nv) x[0] = x[1] = -INFINITY;
-                        if (j + ra + 8 >= nv) x[2] = x[3] = -INFINITY;
+                        if (ra >= nv[j]) x[j][0] = x[j][1] = -INFINITY;
+                        if (ra + 8 >= nv[j]) x[j][2] = x[j][3] = -INFINITY;
                     }
-                    // ---- probabilities against a reference per head, raised only when a score exceeds it by
-                    // more than kSlack (one vote instead of a reduction a tile).  The reference lies kLift below
-                    // the maximum it was taken from, so a probability is at most 2^(kSlack + kLift) = 2^15, and
-                    // fp16 hi + lo holds it to 2^-22 of itself or 2^-25 * 2^-kLift of the largest.
-                    constexpr float kSlack = 8.f, kLift = 7.f;
-                    float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
-                    if (!__all_sync(kFullMask, mx0 - kLift <= m0 + kSlack && mx1 - kLift <= m1 + kSlack)) {
+                }
+                // ---- probabilities against a reference per head, raised only when a score exceeds it by more than
+                // kSlack (one vote instead of a reduction a step).  The reference lies kLift below the maximum it
+                // was taken from, so a probability is at most 2^(kSlack + kLift) = 2^15, and fp16 hi + lo holds it
+                // to 2^-22 of itself or 2^-25 * 2^-kLift of the largest.
+                constexpr float kSlack = 8.f, kLift = 7.f;
+                float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])) * zf0;
+                float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])) * zf1;
+                if (!__all_sync(kFullMask, mx0 <= m0 + (kSlack + kLift) && mx1 <= m1 + (kSlack + kLift))) {
 #pragma unroll
-                        for (int off = 4; off < 32; off <<= 1) {
-                            mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, off));
-                            mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, off));
-                        }
-                        const float n0 = fmaxf(m0, mx0 - kLift), n1 = fmaxf(m1, mx1 - kLift);
-                        const float a0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
-                        const float a1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
-                        l0 *= a0;
-                        l1 *= a1;
-#pragma unroll
-                        for (int i = 0; i < kTiles; ++i) {
-                            o[i][0] *= a0;
-                            o[i][1] *= a1;
-                            o[i][2] *= a0;
-                            o[i][3] *= a1;
-                        }
-                        m0 = n0;
-                        m1 = n1;
+                    for (int off = 4; off < 32; off <<= 1) {
+                        mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, off));
+                        mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, off));
                     }
-                    const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-                    const float p0 = fast_exp2(x[0] - r0), p1 = fast_exp2(x[1] - r1);
-                    const float p2 = fast_exp2(x[2] - r0), p3 = fast_exp2(x[3] - r1);
+                    // every step has a valid token, so the references are finite from the first one on
+                    const float n0 = fmaxf(m0, mx0 - kLift), n1 = fmaxf(m1, mx1 - kLift);
+                    const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
+                    l0 *= a0;
+                    l1 *= a1;
+#pragma unroll
+                    for (int i = 0; i < kTiles; ++i) {
+                        o[i][0] *= a0;
+                        o[i][1] *= a1;
+                        o[i][2] *= a0;
+                        o[i][3] *= a1;
+                    }
+                    m0 = n0;
+                    m1 = n1;
+                }
+                uint32_t bh[2][2], bl[2][2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float p0 = fast_exp2(fmaf(x[j][0], zf0, -m0)), p1 = fast_exp2(fmaf(x[j][1], zf1, -m1));
+                    const float p2 = fast_exp2(fmaf(x[j][2], zf0, -m0)), p3 = fast_exp2(fmaf(x[j][3], zf1, -m1));
                     l0 += p0 + p2;
                     l1 += p1 + p3;
                     const uint32_t h01 = pack_half2(p0, p1), h23 = pack_half2(p2, p3);
-                    const uint32_t d01 = pack_half2(p0 - half_lo(h01), p1 - half_hi(h01));
-                    const uint32_t d23 = pack_half2(p2 - half_lo(h23), p3 - half_hi(h23));
-                    uint32_t b0, b1, e0 = 0u, e1 = 0u;
-                    if (DUP) {  // columns 0-3 carry hi, 4-7 lo
-                        b0 = movmatrix_trans(tig < 2 ? h01 : d01);
-                        b1 = movmatrix_trans(tig < 2 ? h23 : d23);
+                    if (DUP) {  // columns 0-3 carry hi, 4-7 lo: p less its hi part in the latter's lanes
+                        bh[j][0] = movmatrix_trans(pack_half2(fmaf(half_lo(h01), lo_lane, p0), fmaf(half_hi(h01), lo_lane, p1)));
+                        bh[j][1] = movmatrix_trans(pack_half2(fmaf(half_lo(h23), lo_lane, p2), fmaf(half_hi(h23), lo_lane, p3)));
                     } else {
-                        b0 = movmatrix_trans(h01);
-                        b1 = movmatrix_trans(h23);
-                        e0 = movmatrix_trans(d01);
-                        e1 = movmatrix_trans(d23);
+                        bh[j][0] = movmatrix_trans(h01);
+                        bh[j][1] = movmatrix_trans(h23);
+                        bl[j][0] = movmatrix_trans(pack_half2(p0 - half_lo(h01), p1 - half_hi(h01)));
+                        bl[j][1] = movmatrix_trans(pack_half2(p2 - half_lo(h23), p3 - half_hi(h23)));
                     }
-                    // ---- values: channels gid * kMine .. + kMine - 1 of tokens t0, t1, t0 + 8, t1 + 8 -----------
-                    const uint8_t* vp = pg + Page::kValues + j * Page::kRow + gid * (D / 16);
-                    const uint8_t* vs = pg + Page::kValueScales + j * Page::kGroups + gid * kMine / 16;
+                }
+                // ---- values: channels gid * kMine .. + kMine - 1 of tokens t0, t1, t0 + 8, t1 + 8 of a tile -----------
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (j == 1 && !two) break;
+                    const uint8_t* base = tile_at(j);
+                    const uint8_t* vp = base + Page::kValues + j * kRow1 * Page::kRow + gid * (D / 16);
+                    const uint8_t* vs = base + Page::kValueScales + j * kRow1 * Page::kGroups + gid * kMine / 16;
                     uint32_t w[4][kVWords];
                     uint32_t sc[4];
 #pragma unroll
@@ -402,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                             w[k][0] = *reinterpret_cast<const uint32_t*>(vp + t * Page::kRow);
                         }
                         sc[k] = vs[t * Page::kGroups];
-                        if (!full && j + t >= nv) sc[k] = 0u;  // a scale of zero: codes are always finite
+                        if (!full && t >= nv[j]) sc[k] = 0u;  // a scale of zero: codes are always finite
                     }
                     const uint32_t s01 = e4m3x2_to_half2(sc[0] | (sc[1] << 8));
                     const uint32_t s23 = e4m3x2_to_half2(sc[2] | (sc[3] << 8));
@@ -424,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                         const uint32_t ya = (a & 1) ? od23[a / 8] : ev23[a / 8], yb = (b & 1) ? od23[b / 8] : ev23[b / 8];
                         const uint32_t a0 = half2_mul(e2m1x2_to_half2<ba>(xa), s01), a1 = half2_mul(e2m1x2_to_half2<bb>(xb), s01);
                         const uint32_t a2 = half2_mul(e2m1x2_to_half2<ba>(ya), s23), a3 = half2_mul(e2m1x2_to_half2<bb>(yb), s23);
-                        mma_f16_16816(o[i], a0, a1, a2, a3, b0, b1);
-                        if (!DUP) mma_f16_16816(o[i], a0, a1, a2, a3, e0, e1);
+                        mma_f16_16816(o[i], a0, a1, a2, a3, bh[j][0], bh[j][1]);
+                        if (!DUP) mma_f16_16816(o[i], a0, a1, a2, a3, bl[j][0], bl[j][1]);
                     };
                     tile(std::integral_constant<int, 0>{});
                     tile(std::integral_constant<int, 1>{});
@@ -439,10 +558,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                     }
                 }
             }
-            ++consumed;
+            if ((meta.y >> 6) > u && (meta.y & 63) != 0) break;  // the second page is of a later unit
+            ++r;
             __syncwarp();
-            fence_proxy_async_shared();  // this slot's reads before the copy that refills it
-            if (!dead) fill();
+            if (r + kDepth - 1 < rounds) {
+                fence_proxy_async_shared();  // this slot's reads before the copy that refills it
+                issue(r + kDepth - 1);
+            }
         }
 
         // ---- the unit ends here (or this CTA's piece of it): merge the warps ---------------------------------------
@@ -458,41 +580,107 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             sh.l[warp][col0 + 1] = l1;
         }
         float* mine = part + static_cast<size_t>(warp) * G * (D + 4);
+        if (m0 != -INFINITY) {  // this warp had a page of the unit
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            if (DUP) {  // hi + lo
+            for (int i = 0; i < (DUP ? kTiles / 2 : kTiles); ++i) {
+                float v[4];
+                int d = gid * kMine + i;
+                if (DUP) {  // hi + lo: the lanes with the hi columns take the first half of the tiles, the others the rest
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[i][k] += __shfl_xor_sync(kFullMask, o[i][k], 2);
-            }
-            if (!DUP || tig < 2) {
-                const int d = gid * kMine + i;
+                    for (int k = 0; k < 4; ++k) {
+                        const float give = tig < 2 ? o[i + kTiles / 2][k] : o[i][k];
+                        const float keep = tig < 2 ? o[i][k] : o[i + kTiles / 2][k];
+                        v[k] = keep + __shfl_xor_sync(kFullMask, give, 2);
+                    }
+                    if (tig >= 2) d += kTiles / 2;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = o[i][k];
+                }
                 if (col0 < G) {
-                    mine[col0 * (D + 4) + d] = o[i][0];
-                    mine[col0 * (D + 4) + d + kTiles] = o[i][2];
+                    mine[col0 * (D + 4) + d] = v[0];
+                    mine[col0 * (D + 4) + d + kTiles] = v[2];
                 }
                 if (col0 + 1 < G) {
-                    mine[(col0 + 1) * (D + 4) + d] = o[i][1];
-                    mine[(col0 + 1) * (D + 4) + d + kTiles] = o[i][3];
+                    mine[(col0 + 1) * (D + 4) + d] = v[1];
+                    mine[(col0 + 1) * (D + 4) + d + kTiles] = v[3];
                 }
             }
         }
         __syncthreads();
+        if (warp < G) {  // one warp a head, a lane a warp's partial
+            const float mw = lane < kWarps ? sh.m[lane][warp] : -INFINITY;
+            float M = mw;
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
+            M = __shfl_sync(kFullMask, M, 0);
+            const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+            float L = lane < kWarps && mw != -INFINITY ? sh.l[lane][warp] * f : 0.f;
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) L += __shfl_xor_sync(kFullMask, L, off);
+            if (lane < kWarps) sh.f[lane][warp] = f;
+            if (lane == 0) {
+                sh.ref[warp] = M;
+                sh.sum[warp] = L;
+            }
+        }
+        __syncthreads();
+        if (p.C > 1) {
+            // the unit's CTAs are a cluster: each stores, into every other, its references and sums and the slice of
+            // its outputs that the other owns; after one cluster barrier every CTA combines its slice
+            const int C = p.C, rc = static_cast<int>(cluster_ctarank());
+            const int slice = (G * D + C - 1) / C;
+            cluster_wait();
+            for (int e = tid; e < C * G; e += kThreads) {
+                const int c = e / G, g = e - c * G;
+                st_dsmem_f32(&sh.rstat[rc][g], c, sh.ref[g]);
+                st_dsmem_f32(&sh.rstat[rc][8 + g], c, sh.sum[g]);
+            }
+            for (int e = tid; e < G * D; e += kThreads) {
+                const int g = e / D, d = e - g * D, c = e / slice;
+                float O = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = sh.f[w][g];
+                    const float x = part[(static_cast<size_t>(w) * G + g) * (D + 4) + d];
+                    O = fmaf(f != 0.f ? x : 0.f, f, O);
+                }
+                st_dsmem_f32(&sh.recv[rc * slice + (e - c * slice)], c, O);
+            }
+            __syncwarp();
+            cluster_sync();
+            const size_t row0 = (static_cast<size_t>(p.b0) * p.Hkv + u) * G;
+            for (int i = tid; i < slice; i += kThreads) {
+                const int e = rc * slice + i, g = e / D;
+                if (e >= G * D) break;
+                float M = -INFINITY, L = 0.f, O = 0.f;
+                for (int c = 0; c < C; ++c) M = fmaxf(M, sh.rstat[c][g]);
+                if (M != -INFINITY)
+                    for (int c = 0; c < C; ++c) {
+                        const float f = exp2f(sh.rstat[c][g] - M);
+                        L = fmaf(sh.rstat[c][8 + g], f, L);
+                        O = fmaf(sh.recv[c * slice + i], f, O);
+                    }
+                p.out[row0 * D + e] = L > 0.f ? O * (p.v_scale / L) : 0.f;
+                if (p.lse && e == g * D) p.lse[row0 + g] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            }
+            return;
+        }
         const bool whole = ubeg >= lo && uend <= hi;
-        float* slotp = p.partial + (static_cast<size_t>(rank) * 2 + (ubeg < lo ? 0 : 1)) * kv4_partial_floats(D);
+        const int side = ubeg < lo ? 0 : 1;
+        if (!whole) seg_unit[side] = u;
+        float* slotp = p.partial + (static_cast<size_t>(rank) * 2 + side) * kv4_partial_floats(D);
         for (int e = tid; e < G * D; e += kThreads) {
             const int g = e / D, d = e - g * D;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][g]);
-            float L = 0.f, O = 0.f;
+            const float M = sh.ref[g], L = sh.sum[g];
+            float O = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float mw = sh.m[w][g];
-                const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-                L = fmaf(sh.l[w][g], f, L);
-                O = fmaf(part[(static_cast<size_t>(w) * G + g) * (D + 4) + d], f, O);
+                const float f = sh.f[w][g];
+                const float x = part[(static_cast<size_t>(w) * G + g) * (D + 4) + d];
+                O = fmaf(f != 0.f ? x : 0.f, f, O);  // (a warp without a page of the unit left nothing)
             }
-            const size_t row = static_cast<size_t>(p.u0 + u) * G + g;
+            const size_t row = (static_cast<size_t>(p.b0) * p.Hkv + u) * G + g;
             if (whole) {
                 p.out[row * D + d] = L > 0.f ? O * (p.v_scale / L) : 0.f;
                 if (d == 0 && p.lse) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
@@ -504,53 +692,123 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                 }
             }
         }
-        __syncthreads();  // the partials are free again
+        __syncthreads();  // the partials are free again (and stored, where another CTA has the rest of the unit)
+        if (uend >= hi) break;
     }
-    if (dead) {  // copies in flight land before the CTA leaves (bounded)
-        for (int k = dead_at; k < issued; ++k)
-            mbar_wait_bounded(&sh.bar[warp][k % kDepth], (k / kDepth) & 1, 100000000ull);
+
+    // ---- units that fell on several CTAs: whoever stored the last part combines them ---------------------------
+    // A unit's counter is that of the first CTA it lies in, which can be the first for one such unit only.
+    if (tid < 2) {
+        sh.last[tid] = 0;
+        const int u = seg_unit[tid];
+        if (u >= 0) {
+            int beg, end;
+            list.range(u, beg, end);
+            const int c0 = pieces.owner(beg), np = pieces.owner(end - 1) - c0 + 1;
+            // release: this CTA's parts, stored before the barrier above; acquire: the other CTAs'
+            int before;
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.counter + c0) : "memory");
+            if (before == np - 1) {
+                p.counter[c0] = 0;  // as the next call has to find it
+                sh.last[tid] = 1;
+            }
+        }
+    }
+    __syncthreads();
+    for (int side = 0; side < 2; ++side) {
+        if (!sh.last[side]) continue;
+        const int u = seg_unit[side];
+        int beg, end;
+        list.range(u, beg, end);
+        const int c0 = pieces.owner(beg), np = pieces.owner(end - 1) - c0 + 1;
+        const size_t stride = kv4_partial_floats(D);
+        // A thread takes four channels of one head from every ngrp-th part, eight at a time with a running reference;
+        // the groups' results are then combined in shared memory (where the warps' partials were, so ngrp <= kWarps).
+        // The first part is its CTA's last unit, the others are their CTAs' first.
+        const int nf4 = G * D / 4, ngrp = min(min(kThreads / nf4, kWarps), np);
+        const int grp = tid / nf4, e = tid - grp * nf4, g = 4 * e / D;
+        if (grp < ngrp) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            float M = -INFINITY, L = 0.f;
+            for (int k0 = grp; k0 < np; k0 += 8 * ngrp) {
+                float m[8], l[8];
+                float4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = k0 + i * ngrp;
+                    m[i] = -INFINITY;
+                    l[i] = 0.f;
+                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < np) {
+                        const float* slot = p.partial + (static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * stride;
+                        m[i] = __ldcg(slot + 8 * D + g);
+                        l[i] = __ldcg(slot + 8 * D + 8 + g);
+                        x[i] = __ldcg(reinterpret_cast<const float4*>(slot) + e);
+                    }
+                }
+                float top = M;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, m[i]);
+                if (top == -INFINITY) continue;  // no part has seen a token yet
+                const float old = exp2f(M - top);
+                L *= old;
+                a.x *= old, a.y *= old, a.z *= old, a.w *= old;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float f = exp2f(m[i] - top);
+                    L = fmaf(l[i], f, L);
+                    a.x = fmaf(x[i].x, f, a.x);
+                    a.y = fmaf(x[i].y, f, a.y);
+                    a.z = fmaf(x[i].z, f, a.z);
+                    a.w = fmaf(x[i].w, f, a.w);
+                }
+                M = top;
+            }
+            reinterpret_cast<float4*>(part)[tid] = a;
+            if (4 * e == g * D) {
+                sh.m[grp][g] = M;
+                sh.l[grp][g] = L;
+            }
+        }
+        __syncthreads();
+        const size_t row0 = (static_cast<size_t>(p.b0) * p.Hkv + u) * G;
+        for (int i = tid; i < G * D; i += kThreads) {
+            const int h = i / D;
+            float M = -INFINITY, L = 0.f, O = 0.f;
+            for (int k = 0; k < ngrp; ++k) M = fmaxf(M, sh.m[k][h]);
+            if (M != -INFINITY)
+                for (int k = 0; k < ngrp; ++k) {
+                    const float f = exp2f(sh.m[k][h] - M);
+                    L = fmaf(sh.l[k][h], f, L);
+                    O = fmaf(part[k * G * D + i], f, O);
+                }
+            p.out[row0 * D + i] = L > 0.f ? O * (p.v_scale / L) : 0.f;
+            if (p.lse && i == h * D) p.lse[row0 + h] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncthreads();
     }
 }
 
-// ---- units that fell on several CTAs: combine their parts ----------------------------------------------------
-__global__ void __launch_bounds__(128) kv4_merge_kernel(const Kv4AttnParams p, int N)
+// clusters of c CTAs of this kernel that the device holds at once
+int clusters_at_once(void (*kernel)(Kv4AttnParams), size_t smem, int c)
 {
-    pdl_wait_then_release();
-    const int i = blockIdx.x;
-    const int total = p.pre[p.nu], beg = p.pre[i], end = p.pre[i + 1];
-    if (beg == end) return;
-    auto owner = [&](int f) {  // the CTA whose piece holds page f
-        int c = static_cast<int>(static_cast<long long>(f) * N / total);
-        while (piece_start(total, c + 1, N) <= f) ++c;
-        while (piece_start(total, c, N) > f) --c;
-        return c;
-    };
-    const int c0 = owner(beg), c1 = owner(end - 1);
-    if (c0 == c1) return;  // written by that CTA
-    const int G = p.G, D = p.D;
-    const size_t stride = kv4_partial_floats(D);
-    for (int e = threadIdx.x; e < G * D; e += blockDim.x) {
-        const int g = e / D, d = e - g * D;
-        float M = -INFINITY;
-        for (int c = c0; c <= c1; ++c) {
-            const int s = piece_start(total, c, N);
-            if (s == piece_start(total, c + 1, N)) continue;  // an empty piece
-            M = fmaxf(M, p.partial[(static_cast<size_t>(c) * 2 + (beg < s ? 0 : 1)) * stride + 8 * D + g]);
-        }
-        float L = 0.f, O = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const int s = piece_start(total, c, N);
-            if (s == piece_start(total, c + 1, N)) continue;
-            const float* slot = p.partial + (static_cast<size_t>(c) * 2 + (beg < s ? 0 : 1)) * stride;
-            const float m = slot[8 * D + g];
-            const float f = m == -INFINITY ? 0.f : exp2f(m - M);
-            L = fmaf(slot[8 * D + 8 + g], f, L);
-            O = fmaf(slot[e], f, O);
-        }
-        const size_t row = static_cast<size_t>(p.u0 + i) * G + g;
-        p.out[row * D + d] = L > 0.f ? O * (p.v_scale / L) : 0.f;
-        if (d == 0 && p.lse) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c, 1, 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
     }
+    return n;
 }
 
 template <int D, int T>
@@ -559,33 +817,65 @@ cudaError_t launch(Kv4AttnParams p, cudaStream_t stream)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static thread_local int sm_dev = -1, sms = 0;
-    if (sm_dev != dev) {
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        sm_dev = dev;
-    }
     const bool dup = p.G <= 4;
     void (*kernel)(Kv4AttnParams) = dup ? kv4_attn_kernel<D, T, true> : kv4_attn_kernel<D, T, false>;
-    static thread_local int smem_dev[2] = {-1, -1};
-    static thread_local size_t smem_have[2] = {0, 0};
-    const int units = p.B * p.Hkv;
-    for (p.u0 = 0; p.u0 < units; p.u0 += kKv4MaxUnits) {
-        p.nu = units - p.u0 < kKv4MaxUnits ? units - p.u0 : kKv4MaxUnits;
-        const size_t smem = smem_bytes(D, T, p.G, p.nu);
-        e = allow_smem(kernel, smem, smem_dev[dup], smem_have[dup]);
+    // per thread and device: what the launches need to know of it
+    struct Device {
+        int dev = -1, sms = 0;
+        size_t smem[2] = {0, 0};
+        int held[9][kKv4MaxCluster + 1] = {};  // clusters of c CTAs held at once, by group size; 0: not asked yet
+    };
+    static thread_local Device known;
+    if (known.dev != dev) {
+        known = Device{};
+        e = cudaDeviceGetAttribute(&known.sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
-        // one CTA an SM, fewer when not every warp would get a page
-        const long long most = static_cast<long long>(p.nu) * (p.sel_idx ? p.Kmax : p.Pmax);
-        long long n = (most + kWarps - 1) / kWarps;
-        if (n > sms) n = sms;
-        if (n > kKv4MaxCtas) n = kKv4MaxCtas;
-        e = launch_pdl(kernel, dim3(static_cast<unsigned>(n)), dim3(kThreads), smem, stream, p);
-        if (e != cudaSuccess) return e;
-        if (n > 1) {
-            e = launch_pdl(kv4_merge_kernel, dim3(p.nu), dim3(128), 0, stream, p, static_cast<int>(n));
+        known.dev = dev;
+    }
+    // batch entries of one launch: their page counts are summed in shared memory, and the list's length is an int
+    const long long each = static_cast<long long>(p.Hkv) * (p.sel_idx ? p.Kmax : p.Pmax);  // <= 2^31
+    long long room = (1ll << 30) / each;
+    if (room > (1 << 24) / p.Hkv) room = (1 << 24) / p.Hkv;  // a unit's number and a count of tokens share a word
+    const int step = room < 1 ? 1 : room < kKv4MaxBatch ? static_cast<int>(room) : kKv4MaxBatch;
+    for (p.b0 = 0; p.b0 < p.B; p.b0 += step) {
+        p.nb = p.B - p.b0 < step ? p.B - p.b0 : step;
+        const size_t smem = smem_bytes(D, p.G, p.sel_idx ? 0 : p.nb);
+        if (known.smem[dup] < smem) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
             if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            known.smem[dup] = smem;
         }
+        const long long units = static_cast<long long>(p.nb) * p.Hkv;
+        p.C = 0;
+        if (p.sel_idx != nullptr && units <= known.sms) {
+            // selections of units that all run at once: a cluster a unit, as many CTAs as fit and have 16 pages each
+            const size_t bare = smem_bytes(D, p.G, 0);
+            int most = (p.Kmax + kWarps - 1) / kWarps;
+            if (most > kKv4MaxCluster) most = kKv4MaxCluster;
+            p.C = 1;
+            for (int c = 2; c <= most && units * c <= known.sms; ++c) {
+                int& held = known.held[p.G][c];
+                if (held == 0) {
+                    held = clusters_at_once(kernel, bare, c);
+                    if (held == 0) held = -1;
+                }
+                if (held >= units) p.C = c;
+            }
+        }
+        long long n = units * p.C;
+        if (p.C == 0) {  // one CTA an SM, fewer when not every warp would get a page
+            n = (each * p.nb + kWarps - 1) / kWarps;
+            if (n > known.sms) n = known.sms;
+            if (n > kKv4MaxCtas) n = kKv4MaxCtas;
+        }
+        if (p.C > 1)
+            e = launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(n)), dim3(kThreads), smem, stream,
+                                   static_cast<unsigned>(p.C), p);
+        else
+            e = launch_pdl(kernel, dim3(static_cast<unsigned>(n)), dim3(kThreads), smem, stream, p);
+        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -531,11 +531,11 @@ def alloc_kv4_pool(shape: Shape, device="cuda") -> torch.Tensor:
 
 
 def alloc_kv4_workspace(shape: Shape, device="cuda") -> torch.Tensor:
-    """A workspace (uint8) for sparse_paged_decode_attn_kv4."""
+    """A workspace (uint8, zero-filled as it has to be) for sparse_paged_decode_attn_kv4."""
     n = kv4_workspace_size(shape)
     if n == 0:
         raise KvmmError("kvmm_kv4_workspace_size", UNSUPPORTED_SHAPE)
-    return torch.empty((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
+    return torch.zeros((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
 def _one_device(*tensors) -> None:

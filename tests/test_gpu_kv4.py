@@ -52,7 +52,7 @@ class Cache:
         self.lse = torch.full((self.B, Hq), 7.0, device="cuda")
         self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.ws = kvmm.alloc_kv4_workspace(self.shape)
-        self.ws.fill_(0xFF)  # NaN: nothing of it may be read before it is written
+        self.ws[1024:] = 0xFF  # NaN behind the counters: nothing of it may be read before it is written
         self.sel = self.cnt = None
 
     def spoil_behind(self):
@@ -214,12 +214,37 @@ def test_one_long_sequence_falls_on_every_cta(G):
     torch.cuda.synchronize()
     assert int(c.err) == 0
     c.check()
-    # the same tokens selected one by one give the same bits: the list of pages is the same
-    out, lse = c.out.clone(), c.lse.clone()
+    # every page selected: the same values through a cluster a unit
+    c.out.zero_(), c.lse.zero_()
     c.select(c.Pmax)
     c.attend()
     torch.cuda.synchronize()
-    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    assert int(c.err) == 0
+    c.check()
+
+
+@pytest.mark.parametrize("K", [1, 16, 17, 47, 130, 300])
+@pytest.mark.parametrize("B,Hkv,G,D,T", [(1, 1, 8, 128, 16), (1, 3, 1, 64, 16), (3, 2, 5, 128, 32), (7, 5, 4, 64, 32)])
+def test_clusters_of_every_size(K, B, Hkv, G, D, T):
+    """Few units: the more places a unit has, the more CTAs share it; counts below Kmax leave some of them idle."""
+    c = Cache([4000 - 900 * (b % 4) for b in range(B)], Hq=Hkv * G, Hkv=Hkv, D=D, T=T, L=1, layer=0)
+    rng = np.random.default_rng(K)
+    c.select(K, cnt=[int(x) for x in rng.integers(0, K + 1, B * Hkv)])
+    c.attend()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    c.check()
+
+
+def test_selections_of_more_units_than_sms():
+    """320 units: the selected pages of all are dealt evenly."""
+    rng = np.random.default_rng(5)
+    c = Cache([int(x) for x in rng.integers(0, 700, 40)], Hq=24, Hkv=8, D=64, L=1, layer=0)
+    c.select(20, cnt=[int(x) for x in rng.integers(0, 21, 320)])
+    c.attend()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    c.check()
 
 
 def test_more_units_than_one_launch_takes():
