@@ -89,35 +89,6 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s)
     b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
-// rotate a lane's two pieces (channels 8*ca.. and 8*cb..) by table row `pos`
-__device__ __forceinline__ void rotate(const AppendParams& p, int pos, int ca, int cb, float (&a)[8], float (&b)[8])
-{
-    const float* cs = p.rope.table + static_cast<size_t>(pos) * p.rope.dim;
-    const float* sn = cs + p.rope.dim / 2;
-    if (p.rope.interleaved) {  // pairs inside a piece: angles 4c .. 4c+3
-        const float4 c0 = *reinterpret_cast<const float4*>(cs + 4 * ca), s0 = *reinterpret_cast<const float4*>(sn + 4 * ca);
-        const float4 c1 = *reinterpret_cast<const float4*>(cs + 4 * cb), s1 = *reinterpret_cast<const float4*>(sn + 4 * cb);
-        turn(a[0], a[1], c0.x, s0.x);
-        turn(a[2], a[3], c0.y, s0.y);
-        turn(a[4], a[5], c0.z, s0.z);
-        turn(a[6], a[7], c0.w, s0.w);
-        turn(b[0], b[1], c1.x, s1.x);
-        turn(b[2], b[3], c1.y, s1.y);
-        turn(b[4], b[5], c1.z, s1.z);
-        turn(b[6], b[7], c1.w, s1.w);
-    } else {  // channel i with i + dim/2: angles 8*ca .. 8*ca+7
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 c = reinterpret_cast<const float4*>(cs + 8 * ca)[i];
-            const float4 s = reinterpret_cast<const float4*>(sn + 8 * ca)[i];
-            turn(a[4 * i], b[4 * i], c.x, s.x);
-            turn(a[4 * i + 1], b[4 * i + 1], c.y, s.y);
-            turn(a[4 * i + 2], b[4 * i + 2], c.z, s.z);
-            turn(a[4 * i + 3], b[4 * i + 3], c.w, s.w);
-        }
-    }
-}
-
 // a lane's pieces: `sub` of the D/16 lanes of a row
 struct Pieces {
     int a, b;
@@ -132,8 +103,18 @@ __device__ __forceinline__ Pieces pieces(const AppendParams& p, int sub)
     return {2 * r + (sub - r), 2 * r + rest + (sub - r), false};
 }
 
+// x / d from r = 1/d (rounded): the product and one correction by its residual (Markstein 1990), x/d to within 2^-45
+// before the one rounding.  Where it is taken, what matters is that a quotient that is a border of the next, coarser
+// rounding comes out as that border and every other on its side of it: x has 24 significant bits and the product of d
+// and a border at most seven, so x/d is off a border by at least 1.01 half-steps of fp32 there, or not at all.
+__device__ __forceinline__ float quotient(float x, float d, float r)
+{
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+}
+
 // Hold a lane's two pieces in 4 bits: codes (eight nibbles a piece) and the
-// scales' bytes; `a`, `b` become code * scale.  Every lane of the warp calls.
+// scales' bytes; `a`, `b` become x / factor.  Every lane of the warp calls.
 __device__ __forceinline__ void hold4(float (&a)[8], float (&b)[8], float inv, uint32_t& code_a, uint32_t& code_b,
                                       uint32_t& scale_a, uint32_t& scale_b)
 {
@@ -147,23 +128,20 @@ __device__ __forceinline__ void hold4(float (&a)[8], float (&b)[8], float inv, u
     }
     ma = fmaxf(ma, __shfl_xor_sync(kFullMask, ma, 1));  // the other eight channels of the scale
     mb = fmaxf(mb, __shfl_xor_sync(kFullMask, mb, 1));
-    scale_a = float_to_e4m3(__fdiv_rn(ma, 6.f));
-    scale_b = float_to_e4m3(__fdiv_rn(mb, 6.f));
+    constexpr float kSixth = 1.f / 6.f;
+    scale_a = float_to_e4m3(quotient(ma, 6.f, kSixth));
+    scale_b = float_to_e4m3(quotient(mb, 6.f, kSixth));
     const uint32_t s2 = e4m3x2_to_half2(scale_a | (scale_b << 8));
     const float sa = half_lo(s2), sb = half_hi(s2);
+    const float ra = __frcp_rn(sa), rb = __frcp_rn(sb);
     code_a = code_b = 0u;
-    // A quotient is rounded to fp32, then to e2m1.  y has 24 significant bits and the scale 4, so a quotient
-    // that is not a border of e2m1 does not round to one: the code is the nearest to the true quotient.
-    if (scale_a != 0u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            code_a |= float2_to_e2m1x2(__fdiv_rn(a[2 * i], sa), __fdiv_rn(a[2 * i + 1], sa)) << (8 * i);
+    for (int i = 0; i < 4; ++i) {
+        code_a |= float2_to_e2m1x2(quotient(a[2 * i], sa, ra), quotient(a[2 * i + 1], sa, ra)) << (8 * i);
+        code_b |= float2_to_e2m1x2(quotient(b[2 * i], sb, rb), quotient(b[2 * i + 1], sb, rb)) << (8 * i);
     }
-    if (scale_b != 0u) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            code_b |= float2_to_e2m1x2(__fdiv_rn(b[2 * i], sb), __fdiv_rn(b[2 * i + 1], sb)) << (8 * i);
-    }
+    if (scale_a == 0u) code_a = 0u;
+    if (scale_b == 0u) code_b = 0u;
 }
 
 // eight codes and their scale -> four bf16 pairs (exact)
@@ -211,13 +189,55 @@ struct Bounds {
     }
 };
 
+// the angles of a lane's two pieces at one position
+struct Angles {
+    float4 c0, c1, s0, s1;
+};
+__device__ __forceinline__ Angles angles(const AppendParams& p, int pos, const Pieces& pc)
+{
+    const float* cs = p.rope.table + static_cast<size_t>(pos) * p.rope.dim;
+    const float* sn = cs + p.rope.dim / 2;
+    // pairs inside a piece: angles 4c .. 4c + 3 of either; channel i with i + dim/2: angles 8a .. 8a + 7
+    const int i0 = p.rope.interleaved ? pc.a : 2 * pc.a, i1 = p.rope.interleaved ? pc.b : 2 * pc.a + 1;
+    return {reinterpret_cast<const float4*>(cs)[i0], reinterpret_cast<const float4*>(cs)[i1],
+            reinterpret_cast<const float4*>(sn)[i0], reinterpret_cast<const float4*>(sn)[i1]};
+}
+__device__ __forceinline__ void rotate(const AppendParams& p, const Angles& g, float (&a)[8], float (&b)[8])
+{
+    if (p.rope.interleaved) {
+        turn(a[0], a[1], g.c0.x, g.s0.x);
+        turn(a[2], a[3], g.c0.y, g.s0.y);
+        turn(a[4], a[5], g.c0.z, g.s0.z);
+        turn(a[6], a[7], g.c0.w, g.s0.w);
+        turn(b[0], b[1], g.c1.x, g.s1.x);
+        turn(b[2], b[3], g.c1.y, g.s1.y);
+        turn(b[4], b[5], g.c1.z, g.s1.z);
+        turn(b[6], b[7], g.c1.w, g.s1.w);
+    } else {
+        turn(a[0], b[0], g.c0.x, g.s0.x);
+        turn(a[1], b[1], g.c0.y, g.s0.y);
+        turn(a[2], b[2], g.c0.z, g.s0.z);
+        turn(a[3], b[3], g.c0.w, g.s0.w);
+        turn(a[4], b[4], g.c1.x, g.s1.x);
+        turn(a[5], b[5], g.c1.y, g.s1.y);
+        turn(a[6], b[6], g.c1.z, g.s1.z);
+        turn(a[7], b[7], g.c1.w, g.s1.w);
+    }
+}
+
+constexpr int kQueryPasses = 4;  // rows of one token a lane turns: its loads in flight together
+
+// Loads come before the stores that follow them in each batch: the compiler may not move a load over a store that
+// could alias it, so the order written is the number of bytes in flight.
 template <int D, int T, bool KV4>
-__global__ void __launch_bounds__(kAppWarps * 32) append_rope_kernel(const AppendParams p, int page_slots,
-                                                                     unsigned kv_ctas, int q_passes)
+__global__ void __launch_bounds__(kAppWarps * 32, 2) append_rope_kernel(const AppendParams p, int page_slots,
+                                                                        unsigned kv_ctas, int head_blocks)
 {
     using Page = Kv4Page<D, T>;
-    constexpr int kLanes = D / 16;        // lanes of a row
-    constexpr int kRows = 32 / kLanes;    // rows a warp moves at once
+    constexpr int kLanes = D / 16;      // lanes of a row
+    constexpr int kRows = 32 / kLanes;  // rows a warp moves at once
+    constexpr int kBatch = 2;           // passes loaded together
+    static_assert(T % (kRows * kBatch) == 0, "whole batches");
     pdl_wait_then_release();  // the pools, table and metadata may be in use by the previous kernel
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
@@ -226,37 +246,49 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_rope_kernel(const Appen
     const Pieces pc = pieces<D>(p, sub);
 
     if (blockIdx.x >= kv_ctas) {
-        // ---- query rows: q_passes * kRows consecutive (batch, token, head) rows a warp --------------------
-        const int64_t rows = static_cast<int64_t>(p.B) * p.n_new * p.Hq;
-        const int64_t first = (static_cast<int64_t>(blockIdx.x - kv_ctas) * kAppWarps + warp) * q_passes * kRows;
-        for (int k = 0; k < q_passes; ++k) {
-            const int64_t row = first + k * kRows + rsub;
-            if (row >= rows) continue;
-            const int64_t bt = row / p.Hq;
-            const int h = static_cast<int>(row - bt * p.Hq);
-            const int b = static_cast<int>(bt / p.n_new);
-            const int j = static_cast<int>(bt - static_cast<int64_t>(b) * p.n_new);
-            int tb, te;
-            if (!token_range(p, b, tb, te, false) || j >= te - tb) continue;
-            const int pos = position(p, b, j, tb + j);
-            if (pos < 0) {
-                if (sub == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
-                continue;
+        // ---- queries: one token's kQueryPasses * kRows heads a warp; its angles are loaded once ---------------------
+        const int64_t item = static_cast<int64_t>(blockIdx.x - kv_ctas) * kAppWarps + warp;
+        const int64_t token = item / head_blocks;
+        const int h0 = static_cast<int>(item - token * head_blocks) * (kQueryPasses * kRows) + rsub;
+        const int b = static_cast<int>(token / p.n_new);
+        if (b >= p.B) return;
+        const int j = static_cast<int>(token - static_cast<int64_t>(b) * p.n_new);
+        int tb, te;
+        if (!token_range(p, b, tb, te, false) || j >= te - tb) return;
+        const int pos = position(p, b, j, tb + j);
+        if (pos < 0) {
+            if (lane == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
+            return;
+        }
+        const kvmm_bf16* src = p.q.data + b * p.q.batch_stride + j * p.q.token_stride;
+        kvmm_bf16* dst = p.q_out + token * p.Hq * D;
+        uint4 va[kQueryPasses], vb[kQueryPasses];
+#pragma unroll
+        for (int k = 0; k < kQueryPasses; ++k) {
+            const int h = h0 + k * kRows;
+            if (h < p.Hq) {
+                const uint4* row = reinterpret_cast<const uint4*>(src + h * p.q.head_stride);
+                va[k] = row[pc.a];
+                vb[k] = row[pc.b];
             }
-            const uint4* src = reinterpret_cast<const uint4*>(p.q.data + b * p.q.batch_stride +
-                                                              j * p.q.token_stride + h * p.q.head_stride);
-            uint4* dst = reinterpret_cast<uint4*>(p.q_out + row * D);
-            uint4 va = src[pc.a], vb = src[pc.b];
+        }
+        Angles g{};
+        if (pc.turns) g = angles(p, pos, pc);
+#pragma unroll
+        for (int k = 0; k < kQueryPasses; ++k) {
+            const int h = h0 + k * kRows;
+            if (h >= p.Hq) break;
             if (pc.turns) {
                 float a[8], c[8];
-                unpack8(va, a);
-                unpack8(vb, c);
-                rotate(p, pos, pc.a, pc.b, a, c);
-                va = pack8(a);
-                vb = pack8(c);
+                unpack8(va[k], a);
+                unpack8(vb[k], c);
+                rotate(p, g, a, c);
+                va[k] = pack8(a);
+                vb[k] = pack8(c);
             }
-            dst[pc.a] = va;
-            dst[pc.b] = vb;
+            uint4* row = reinterpret_cast<uint4*>(dst + static_cast<size_t>(h) * D);
+            row[pc.a] = va[k];
+            row[pc.b] = vb[k];
         }
         return;
     }
@@ -279,102 +311,125 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_rope_kernel(const Appen
         if (lane == 0) report(p.err, phys < 0 ? KVMM_ERR_NULL_BLOCK : KVMM_ERR_OUT_OF_RANGE);
         return;
     }
-    const int r0 = max(tb - first, 0);      // new rows of the page: [r0, r1); rows before r0 are there already
-    const int r1 = min(te - first, T);
-    const kvmm_bf16* k_src = p.k.data + b * p.k.batch_stride + h * p.k.head_stride;
-    const kvmm_bf16* v_src = p.v.data + b * p.v.batch_stride + h * p.v.head_stride;
+    // rows of the page this call writes (`fresh`), and those that stay and count for its MinMax (`held`); lane r < T
+    // has the position of row r
+    const int r0 = max(tb - first, 0), r1 = min(te - first, T);
+    int pos = -1;
+    if (lane >= r0 && lane < r1) {
+        pos = position(p, b, first + lane - tb, first + lane);
+        if (pos < 0 && h == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
+    }
+    const unsigned fresh = __ballot_sync(kFullMask, pos >= 0);
+    const unsigned held = p.meta != nullptr ? ((r1 < 32 ? (1u << r1) : 0u) - 1u) & ~fresh : 0u;
+    const kvmm_bf16* k_src = p.k.data + b * p.k.batch_stride + h * p.k.head_stride + (first - tb) * p.k.token_stride;
+    const kvmm_bf16* v_src = p.v.data + b * p.v.batch_stride + h * p.v.head_stride + (first - tb) * p.v.token_stride;
     uint8_t* page4 = KV4 ? p.kv4_pool + static_cast<size_t>(phys) * Page::kBytes : nullptr;
     kvmm_bf16* kpage = KV4 ? nullptr : p.k_pool + static_cast<size_t>(phys) * T * D;
     kvmm_bf16* vpage = KV4 ? nullptr : p.v_pool + static_cast<size_t>(phys) * T * D;
+    constexpr unsigned kBatchRows = kRows * kBatch == 32 ? ~0u : (1u << (kRows * kBatch)) - 1u;
 
     Bounds ba, bb;
     ba.clear();
     bb.clear();
-#pragma unroll 4
-    for (int i = 0; i < T / kRows; ++i) {
-        const int r = i * kRows + rsub;
-        const int j = first + r - tb;  // its row among the new ones
-        int pos = -1;
-        if (r >= r0 && r < r1) {
-            pos = position(p, b, j, first + r);
-            if (pos < 0 && sub == 0 && h == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
-        }
-        const bool fresh = pos >= 0;
-        const bool held = !fresh && r < r1 && p.meta != nullptr;  // read back for the MinMax
-        uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
-        if (fresh) {
-            const uint4* src = reinterpret_cast<const uint4*>(k_src + j * p.k.token_stride);
-            va = src[pc.a];
-            vb = src[pc.b];
-        } else if (held) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < T; i0 += kRows * kBatch) {
+        const unsigned here = kBatchRows << i0;
+        if ((held & here) != 0u) {
+            uint4 va[kBatch], vb[kBatch];
             if (KV4) {
-                const uint8_t* sc = page4 + Page::kKeyScales + r * Page::kGroups;
-                const uint32_t* cd = reinterpret_cast<const uint32_t*>(page4 + r * Page::kRow);
-                va = held8(cd[pc.a], sc[pc.a >> 1]);
-                vb = held8(cd[pc.b], sc[pc.b >> 1]);
+                uint32_t ca[kBatch], cb[kBatch], sa[kBatch], sb[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = i0 + i * kRows + rsub;
+                    const uint32_t* cd = reinterpret_cast<const uint32_t*>(page4 + r * Page::kRow);
+                    const uint8_t* sc = page4 + Page::kKeyScales + r * Page::kGroups;
+                    ca[i] = cd[pc.a], cb[i] = cd[pc.b], sa[i] = sc[pc.a >> 1], sb[i] = sc[pc.b >> 1];
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) va[i] = held8(ca[i], sa[i]), vb[i] = held8(cb[i], sb[i]);
             } else {
-                const uint4* src = reinterpret_cast<const uint4*>(kpage + static_cast<size_t>(r) * D);
-                va = src[pc.a];
-                vb = src[pc.b];
-            }
-        }
-        if (KV4) {
-            float a[8], c[8];
-            unpack8(va, a);
-            unpack8(vb, c);
-            if (fresh && pc.turns) rotate(p, pos, pc.a, pc.b, a, c);
-            uint32_t ca, cb, sa, sb;
-            hold4(a, c, p.k_inv, ca, cb, sa, sb);
-            if (fresh) {
-                uint32_t* cd = reinterpret_cast<uint32_t*>(page4 + r * Page::kRow);
-                cd[pc.a] = ca;
-                cd[pc.b] = cb;
-                if ((sub & 1) == 0) {
-                    uint8_t* sc = page4 + Page::kKeyScales + r * Page::kGroups;
-                    sc[pc.a >> 1] = static_cast<uint8_t>(sa);
-                    sc[pc.b >> 1] = static_cast<uint8_t>(sb);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const uint4* src = reinterpret_cast<const uint4*>(kpage + (i0 + i * kRows + rsub) * D);
+                    va[i] = src[pc.a];
+                    vb[i] = src[pc.b];
                 }
-                va = held8(ca, sa);
-                vb = held8(cb, sb);
             }
-        } else if (fresh) {
-            if (pc.turns) {
-                float a[8], c[8];
-                unpack8(va, a);
-                unpack8(vb, c);
-                rotate(p, pos, pc.a, pc.b, a, c);
-                va = pack8(a);
-                vb = pack8(c);
-            }
-            uint4* dst = reinterpret_cast<uint4*>(kpage + static_cast<size_t>(r) * D);
-            dst[pc.a] = va;
-            dst[pc.b] = vb;
-        }
-        if (fresh || held) {
-            ba.add(va);
-            bb.add(vb);
-        }
-        if (KV4) {
-            uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
-            if (fresh) {
-                const uint4* src = reinterpret_cast<const uint4*>(v_src + j * p.v.token_stride);
-                wa = src[pc.a];
-                wb = src[pc.b];
-            }
-            float a[8], c[8];
-            unpack8(wa, a);
-            unpack8(wb, c);
-            uint32_t ca, cb, sa, sb;
-            hold4(a, c, p.v_inv, ca, cb, sa, sb);
-            if (fresh) {
-                uint32_t* cd = reinterpret_cast<uint32_t*>(page4 + Page::kValues + r * Page::kRow);
-                cd[pc.a] = ca;
-                cd[pc.b] = cb;
-                if ((sub & 1) == 0) {
-                    uint8_t* sc = page4 + Page::kValueScales + r * Page::kGroups;
-                    sc[pc.a >> 1] = static_cast<uint8_t>(sa);
-                    sc[pc.b >> 1] = static_cast<uint8_t>(sb);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (held >> (i0 + i * kRows + rsub) & 1u) {
+                    ba.add(va[i]);
+                    bb.add(vb[i]);
                 }
+        }
+        if ((fresh & here) == 0u) continue;
+        uint4 va[kBatch], vb[kBatch], wa[KV4 ? kBatch : 1], wb[KV4 ? kBatch : 1];
+        Angles g[kBatch];
+        bool mine[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = i0 + i * kRows + rsub;
+            const int at = __shfl_sync(kFullMask, pos, r);
+            mine[i] = at >= 0;
+            va[i] = vb[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (KV4) wa[i] = wb[i] = va[i];
+            if (mine[i]) {
+                const uint4* src = reinterpret_cast<const uint4*>(k_src + r * p.k.token_stride);
+                va[i] = src[pc.a];
+                vb[i] = src[pc.b];
+                if (KV4) {
+                    src = reinterpret_cast<const uint4*>(v_src + r * p.v.token_stride);
+                    wa[i] = src[pc.a];
+                    wb[i] = src[pc.b];
+                }
+                if (pc.turns) g[i] = angles(p, at, pc);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = i0 + i * kRows + rsub;
+            float a[8], c[8];
+            unpack8(va[i], a);
+            unpack8(vb[i], c);
+            if (mine[i] && pc.turns) rotate(p, g[i], a, c);
+            if (KV4) {
+                uint32_t ca, cb, sa, sb;
+                hold4(a, c, p.k_inv, ca, cb, sa, sb);
+                float x[8], y[8];
+                unpack8(wa[i], x);
+                unpack8(wb[i], y);
+                uint32_t da, db, ta, tb4;
+                hold4(x, y, p.v_inv, da, db, ta, tb4);
+                if (mine[i]) {
+                    uint32_t* cd = reinterpret_cast<uint32_t*>(page4 + r * Page::kRow);
+                    cd[pc.a] = ca;
+                    cd[pc.b] = cb;
+                    cd = reinterpret_cast<uint32_t*>(page4 + Page::kValues + r * Page::kRow);
+                    cd[pc.a] = da;
+                    cd[pc.b] = db;
+                    if ((sub & 1) == 0) {
+                        uint8_t* sc = page4 + Page::kKeyScales + r * Page::kGroups;
+                        sc[pc.a >> 1] = static_cast<uint8_t>(sa);
+                        sc[pc.b >> 1] = static_cast<uint8_t>(sb);
+                        sc = page4 + Page::kValueScales + r * Page::kGroups;
+                        sc[pc.a >> 1] = static_cast<uint8_t>(ta);
+                        sc[pc.b >> 1] = static_cast<uint8_t>(tb4);
+                    }
+                    if (p.meta != nullptr) {
+                        ba.add(held8(ca, sa));
+                        bb.add(held8(cb, sb));
+                    }
+                }
+            } else if (mine[i]) {
+                if (pc.turns) {
+                    va[i] = pack8(a);
+                    vb[i] = pack8(c);
+                }
+                uint4* dst = reinterpret_cast<uint4*>(kpage + r * D);
+                dst[pc.a] = va[i];
+                dst[pc.b] = vb[i];
+                ba.add(va[i]);
+                bb.add(vb[i]);
             }
         }
     }
@@ -394,27 +449,20 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_rope_kernel(const Appen
     if (!KV4) {
         // values go dimension-major: a lane moves two channels of 16 tokens (coalesced 4-byte loads of the rows,
         // 32 bytes of one channel's tokens a store)
-#pragma unroll
+#pragma unroll 1
         for (int t0 = 0; t0 < T; t0 += 16) {
-            if (t0 >= r1 || t0 + 16 <= r0) continue;
-            const bool whole = t0 >= r0 && t0 + 16 <= r1;
+            const unsigned have = fresh >> t0 & 0xffffu;
+            if (have == 0u) continue;
 #pragma unroll
             for (int d0 = 0; d0 < D; d0 += 64) {
                 const int d = d0 + 2 * lane;
                 uint32_t w[16];
-                unsigned have = 0u;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = t0 + i, j = first + r - tb;
-                    w[i] = 0u;
-                    if (r >= r0 && r < r1 && position(p, b, j, first + r) >= 0) {
-                        w[i] = *reinterpret_cast<const uint32_t*>(v_src + j * p.v.token_stride + d);
-                        have |= 1u << i;
-                    }
-                }
-                kvmm_bf16* c0 = vpage + static_cast<size_t>(d) * T + t0;
+                for (int i = 0; i < 16; ++i)
+                    if (have >> i & 1u) w[i] = *reinterpret_cast<const uint32_t*>(v_src + (t0 + i) * p.v.token_stride + d);
+                kvmm_bf16* c0 = vpage + d * T + t0;
                 kvmm_bf16* c1 = c0 + T;
-                if (whole && have == 0xffffu) {
+                if (have == 0xffffu) {
                     uint32_t a[8], c[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -446,16 +494,15 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream)
     const int slots = static_cast<int>(span < p.Pmax ? span : p.Pmax);
     const long long items = static_cast<long long>(p.B) * slots * p.Hkv;
     const long long kv_ctas = (items + kAppWarps - 1) / kAppWarps;
-    constexpr int kRows = 32 / (D / 16);
-    const long long rows = p.q.data ? static_cast<long long>(p.B) * p.n_new * p.Hq : 0;
-    const int passes = rows >= 65536 ? 4 : 1;
-    const long long per_cta = static_cast<long long>(kAppWarps) * kRows * passes;
-    const long long ctas = kv_ctas + (rows + per_cta - 1) / per_cta;
+    constexpr int kHeads = kQueryPasses * 32 / (D / 16);  // heads a warp turns
+    const int head_blocks = (p.Hq + kHeads - 1) / kHeads;
+    const long long q_items = p.q.data ? static_cast<long long>(p.B) * p.n_new * head_blocks : 0;
+    const long long ctas = kv_ctas + (q_items + kAppWarps - 1) / kAppWarps;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     void (*kernel)(AppendParams, int, unsigned, int) =
         p.kv4_pool ? append_rope_kernel<D, T, true> : append_rope_kernel<D, T, false>;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kAppWarps * 32), 0, stream, p, slots,
-                      static_cast<unsigned>(kv_ctas), passes);
+                      static_cast<unsigned>(kv_ctas), head_blocks);
 }
 
 }  // namespace
