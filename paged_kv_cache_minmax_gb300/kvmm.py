@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -78,6 +79,7 @@ class Rope:
         self.c = RopeStruct(_dev(table, "table", torch.float32),
                             _dev(positions, "positions", torch.int32, optional=True), table.shape[0], dim,
                             int(bool(interleaved)))
+        self.ref = ctypes.byref(self.c)
 
 
 def make_shape(B, L, Hq, Hkv, D, T, Pmax, Kmax, n_phys) -> Shape:
@@ -120,9 +122,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.page_score_topk_mean.argtypes = [SP, I32, P, P, P, P, I32, I32, P, P, P, P, SZ, P, P]
     lib.kv_centroid_build.argtypes = [SP, I32, P, P, I32, I32, P, P, P, P, P, P]
     lib.page_score_topk_centroid.argtypes = [SP, I32, P, P, P, I32, P, P, P, P, I32, I32, I32, P, P, P, P, P, P]
-    RP, TP = ctypes.POINTER(Rows), ctypes.POINTER(RopeStruct)
-    lib.kv_append_rope.argtypes = [SP, I32, RP, RP, RP, I32, P, P, TP, P, P, P, P, P, P, P]
-    lib.kv4_append_rope.argtypes = [SP, I32, RP, RP, RP, I32, P, P, TP, P, P, F32, F32, P, P, P, P]
+    # kvmm_rows and kvmm_rope by address: packed bytes or a ctypes structure
+    lib.kv_append_rope.argtypes = [SP, I32, P, P, P, I32, P, P, P, P, P, P, P, P, P, P]
+    lib.kv4_append_rope.argtypes = [SP, I32, P, P, P, I32, P, P, P, P, P, F32, F32, P, P, P, P]
     lib.kv4_gather.argtypes = [SP, I32, P, F32, F32, P, P, P, I32, P, P, P, P]
     lib.sparse_paged_decode_attn_kv4.argtypes = [SP, I32, P, P, F32, F32, P, P, P, P, F32, P, P, P, SZ, U32, P, P]
     lib.kvmm_kv4_page_bytes.argtypes = [SP]
@@ -538,40 +540,60 @@ def alloc_kv4_workspace(shape: Shape, device="cuda") -> torch.Tensor:
     return torch.zeros((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
-def _one_device(*tensors) -> None:
-    """The call runs on the current device's stream: every tensor has to be there."""
+_fields = struct.Struct("8iq").unpack_from  # a Shape's fields at once: single ones cost a small call its time
+_pack_rows = struct.Struct("Pqqq").pack     # a kvmm_rows
+
+
+def _here(stream) -> tuple[int, int]:
+    """The current device and the stream of a call: every tensor of the call has to be on that device."""
     here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError(f"a tensor on {t.device} given to a call on cuda:{here}")
+    return here, torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
 
 
-def _rows(t: torch.Tensor | None, name: str, B: int, n: int, H: int, D: int) -> Rows | None:
-    """A [B, n, H, D] bf16 view as kvmm_rows."""
-    if t is None:
-        return None
+def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int, here: int) -> int:
+    """_dev, and the tensor is on the call's device."""
+    if t is None or t.get_device() != here or t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
+        _dev(t, name, dtype, numel)
+        raise ValueError(f"{name} is on {t.device}, the call on cuda:{here}")
+    return t.data_ptr()
+
+
+def _opt(t: torch.Tensor | None, name: str, dtype: torch.dtype, numel: int, here: int) -> int | None:
+    return None if t is None else _arg(t, name, dtype, numel, here)
+
+
+def _rows(t: torch.Tensor, name: str, B: int, n: int, H: int, D: int, here: int) -> bytes:
+    """A [B, n, H, D] bf16 view as a kvmm_rows."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on {t.device}, the call on cuda:{here}")
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (B, n, H, D):
+    if t.shape != (B, n, H, D):
         raise ValueError(f"{name} must be {(B, n, H, D)}, got {tuple(t.shape)}")
-    if t.stride(3) != 1:
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"{name}: the channels of a row must be consecutive")
-    sb, st, sh = t.stride()[:3]
     # an axis of one entry has no step: its stride may be anything
-    return Rows(t.data_ptr(), sb if B > 1 else 0, st if n > 1 else 0, sh if H > 1 else 0)
+    return _pack_rows(t.data_ptr(), sb if B > 1 else 0, st if n > 1 else 0, sh if H > 1 else 0)
 
 
-def _append_rows(s: Shape, q, new_k, new_v, rope, q_out):
+def _append_rows(f, q, new_k, new_v, tok_begin, tok_end, rope, q_out, here):
+    """The arguments kv_append_rope and kv4_append_rope share, from q to q_out."""
+    B, _, Hq, Hkv, D = f[:5]
     n = new_k.shape[1] if new_k.dim() == 4 else -1
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out are given together or not at all")
-    rows = [_rows(t, name, s.B, n, H, s.D) for t, name, H in ((q, "q", s.Hq), (new_k, "new_k", s.Hkv),
-                                                              (new_v, "new_v", s.Hkv))]
-    if rope is not None and rope.positions is not None and rope.positions.numel() < s.B * n:
-        raise ValueError(f"positions has {rope.positions.numel()} elements, needs {s.B * n}")
-    return n, [None if r is None else ctypes.byref(r) for r in rows], None if rope is None else ctypes.byref(rope.c)
+    if rope is not None:
+        if rope.table.get_device() != here:
+            raise ValueError(f"the rope's table is on {rope.table.device}, the call on cuda:{here}")
+        if rope.positions is not None and (rope.positions.numel() < B * n or rope.positions.get_device() != here):
+            raise ValueError(f"positions needs {B * n} elements on cuda:{here}")
+    return (None if q is None else _rows(q, "q", B, n, Hq, D, here), _rows(new_k, "new_k", B, n, Hkv, D, here),
+            _rows(new_v, "new_v", B, n, Hkv, D, here), n, _arg(tok_begin, "tok_begin", torch.int32, B, here),
+            _arg(tok_end, "tok_end", torch.int32, B, here), None if rope is None else rope.ref,
+            _opt(q_out, "q_out", torch.bfloat16, B * n * Hq * D, here))
 
 
 def kv_append_rope(shape: Shape, layer: int, q, new_k, new_v, tok_begin, tok_end, k_pool, v_pool, block_table, meta,
@@ -580,20 +602,17 @@ def kv_append_rope(shape: Shape, layer: int, q, new_k, new_v, tok_begin, tok_end
 
     new_k, new_v [B, n_new, Hkv, D] and q [B, n_new, Hq, D] (or None) are bf16 views of any strides whose channels are
     consecutive; q_out [B, n_new, Hq, D] takes the rotated queries; meta may be None."""
-    s = shape
-    units = s.B * s.L * s.Hkv
-    n, (qr, kr, vr), rp = _append_rows(s, q, new_k, new_v, rope, q_out)
-    _one_device(q, new_k, new_v, tok_begin, tok_end, k_pool, v_pool, block_table, meta, q_out, err,
-                rope and rope.table, rope and rope.positions)
-    args = (ctypes.byref(s), layer, qr, kr, vr, n, _dev(tok_begin, "tok_begin", torch.int32, s.B),
-            _dev(tok_end, "tok_end", torch.int32, s.B), rp,
-            _dev(q_out, "q_out", torch.bfloat16, s.B * n * s.Hq * s.D, optional=True),
-            _dev(k_pool, "k_pool", torch.bfloat16, s.n_phys * s.T * s.D),
-            _dev(v_pool, "v_pool", torch.bfloat16, s.n_phys * s.T * s.D),
-            _dev(block_table, "block_table", torch.int32, units * s.Pmax),
-            _dev(meta, "meta", torch.bfloat16, units * s.Pmax * 2 * s.D, optional=True),
-            _dev(err, "err", torch.int32, 1, optional=True), _stream(stream))
-    _check("kv_append_rope", load().kv_append_rope(*args))
+    f = _fields(shape)
+    B, L, _, Hkv, D, T, Pmax, _, n_phys = f
+    here, st = _here(stream)
+    pages = B * L * Hkv * Pmax
+    status = load().kv_append_rope(
+        ctypes.byref(shape), layer, *_append_rows(f, q, new_k, new_v, tok_begin, tok_end, rope, q_out, here),
+        _arg(k_pool, "k_pool", torch.bfloat16, n_phys * T * D, here),
+        _arg(v_pool, "v_pool", torch.bfloat16, n_phys * T * D, here),
+        _arg(block_table, "block_table", torch.int32, pages, here),
+        _opt(meta, "meta", torch.bfloat16, pages * 2 * D, here), _opt(err, "err", torch.int32, 1, here), st)
+    _check("kv_append_rope", status)
 
 
 def kv4_append_rope(shape: Shape, layer: int, q, new_k, new_v, tok_begin, tok_end, kv4_pool, block_table, meta,
@@ -601,42 +620,38 @@ def kv4_append_rope(shape: Shape, layer: int, q, new_k, new_v, tok_begin, tok_en
                     stream=None) -> None:
     """kv_append_rope into the 4-bit cache (kv4_pool [n_phys, kv4_page_bytes] uint8); meta are the bounds of the keys
     as held, over k_scale."""
-    s = shape
-    units = s.B * s.L * s.Hkv
-    n, (qr, kr, vr), rp = _append_rows(s, q, new_k, new_v, rope, q_out)
-    _one_device(q, new_k, new_v, tok_begin, tok_end, kv4_pool, block_table, meta, q_out, err, rope and rope.table,
-                rope and rope.positions)
-    args = (ctypes.byref(s), layer, qr, kr, vr, n, _dev(tok_begin, "tok_begin", torch.int32, s.B),
-            _dev(tok_end, "tok_end", torch.int32, s.B), rp,
-            _dev(q_out, "q_out", torch.bfloat16, s.B * n * s.Hq * s.D, optional=True),
-            _dev(kv4_pool, "kv4_pool", torch.uint8, s.n_phys * s.T * (s.D + s.D // 8)), float(k_scale), float(v_scale),
-            _dev(block_table, "block_table", torch.int32, units * s.Pmax),
-            _dev(meta, "meta", torch.bfloat16, units * s.Pmax * 2 * s.D, optional=True),
-            _dev(err, "err", torch.int32, 1, optional=True), _stream(stream))
-    _check("kv4_append_rope", load().kv4_append_rope(*args))
+    f = _fields(shape)
+    B, L, _, Hkv, D, T, Pmax, _, n_phys = f
+    here, st = _here(stream)
+    pages = B * L * Hkv * Pmax
+    status = load().kv4_append_rope(
+        ctypes.byref(shape), layer, *_append_rows(f, q, new_k, new_v, tok_begin, tok_end, rope, q_out, here),
+        _arg(kv4_pool, "kv4_pool", torch.uint8, n_phys * T * (D + D // 8), here), k_scale, v_scale,
+        _arg(block_table, "block_table", torch.int32, pages, here),
+        _opt(meta, "meta", torch.bfloat16, pages * 2 * D, here), _opt(err, "err", torch.int32, 1, here), st)
+    _check("kv4_append_rope", status)
 
 
 def kv4_gather(shape: Shape, layer: int, kv4_pool, block_table, tok_begin, tok_end, k_out, v_out, k_scale: float = 1.0,
                v_scale: float = 1.0, err=None, stream=None) -> None:
     """Tokens [tok_begin, tok_end) of every KV head (tok_begin None = 0) as bf16 rows of k_out and v_out
     [B, n_rows, Hkv, D] (either may be None); rows behind a sequence's last are left as they were."""
-    s = shape
+    B, L, _, Hkv, D, T, Pmax, _, n_phys = _fields(shape)
     some = k_out if k_out is not None else v_out
     if some is None:
         raise ValueError("k_out or v_out is required")
+    n = some.shape[1] if some.dim() == 4 else -1
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and (t.dim() != 4 or t.shape[1] != some.shape[1] or
-                              (t.shape[0], t.shape[2], t.shape[3]) != (s.B, s.Hkv, s.D)):
-            raise ValueError(f"{name} must be [{s.B}, n_rows, {s.Hkv}, {s.D}], got {tuple(t.shape)}")
-    _one_device(kv4_pool, block_table, tok_begin, tok_end, k_out, v_out, err)
-    args = (ctypes.byref(s), layer, _dev(kv4_pool, "kv4_pool", torch.uint8, s.n_phys * s.T * (s.D + s.D // 8)),
-            float(k_scale), float(v_scale),
-            _dev(block_table, "block_table", torch.int32, s.B * s.L * s.Hkv * s.Pmax),
-            _dev(tok_begin, "tok_begin", torch.int32, s.B, optional=True), _dev(tok_end, "tok_end", torch.int32, s.B),
-            some.shape[1], _dev(k_out, "k_out", torch.bfloat16, optional=True),
-            _dev(v_out, "v_out", torch.bfloat16, optional=True), _dev(err, "err", torch.int32, 1, optional=True),
-            _stream(stream))
-    _check("kv4_gather", load().kv4_gather(*args))
+        if t is not None and t.shape != (B, n, Hkv, D):
+            raise ValueError(f"{name} must be [{B}, n_rows, {Hkv}, {D}], got {tuple(t.shape)}")
+    here, st = _here(stream)
+    status = load().kv4_gather(
+        ctypes.byref(shape), layer, _arg(kv4_pool, "kv4_pool", torch.uint8, n_phys * T * (D + D // 8), here), k_scale,
+        v_scale, _arg(block_table, "block_table", torch.int32, B * L * Hkv * Pmax, here),
+        _opt(tok_begin, "tok_begin", torch.int32, B, here), _arg(tok_end, "tok_end", torch.int32, B, here), n,
+        _opt(k_out, "k_out", torch.bfloat16, 0, here), _opt(v_out, "v_out", torch.bfloat16, 0, here),
+        _opt(err, "err", torch.int32, 1, here), st)
+    _check("kv4_gather", status)
 
 
 def sparse_paged_decode_attn_kv4(shape: Shape, layer: int, q, kv4_pool, block_table, seq_len, sel_idx, sel_cnt, out,
@@ -645,19 +660,17 @@ def sparse_paged_decode_attn_kv4(shape: Shape, layer: int, q, kv4_pool, block_ta
     """Attention over the selected pages of the 4-bit cache, or, with sel_idx and sel_cnt None, over every page.
     workspace: alloc_kv4_workspace.  ``early_reads``: no kernel still running when this launch starts writes seq_len
     or the layer's block-table rows."""
-    s = shape
-    units = s.B * s.L * s.Hkv
+    B, L, Hq, Hkv, D, T, Pmax, Kmax, n_phys = _fields(shape)
     if (sel_idx is None) != (sel_cnt is None):
         raise ValueError("sel_idx and sel_cnt are given together or not at all")
-    _one_device(q, kv4_pool, block_table, seq_len, sel_idx, sel_cnt, out, workspace, lse, err)
-    args = (ctypes.byref(s), layer, _dev(q, "q", torch.bfloat16, s.B * s.Hq * s.D),
-            _dev(kv4_pool, "kv4_pool", torch.uint8, s.n_phys * s.T * (s.D + s.D // 8)), float(k_scale), float(v_scale),
-            _dev(block_table, "block_table", torch.int32, units * s.Pmax),
-            _dev(seq_len, "seq_len", torch.int32, s.B),
-            _dev(sel_idx, "sel_idx", torch.int32, units * s.Kmax, optional=True),
-            _dev(sel_cnt, "sel_cnt", torch.int32, units, optional=True), float(sm_scale),
-            _dev(out, "out", torch.float32, s.B * s.Hq * s.D),
-            _dev(lse, "lse", torch.float32, s.B * s.Hq, optional=True),
-            _dev(workspace, "workspace", torch.uint8), workspace.numel(), EARLY_READS if early_reads else 0,
-            _dev(err, "err", torch.int32, 1, optional=True), _stream(stream))
-    _check("sparse_paged_decode_attn_kv4", load().sparse_paged_decode_attn_kv4(*args))
+    here, st = _here(stream)
+    units = B * L * Hkv
+    status = load().sparse_paged_decode_attn_kv4(
+        ctypes.byref(shape), layer, _arg(q, "q", torch.bfloat16, B * Hq * D, here),
+        _arg(kv4_pool, "kv4_pool", torch.uint8, n_phys * T * (D + D // 8), here), k_scale, v_scale,
+        _arg(block_table, "block_table", torch.int32, units * Pmax, here),
+        _arg(seq_len, "seq_len", torch.int32, B, here), _opt(sel_idx, "sel_idx", torch.int32, units * Kmax, here),
+        _opt(sel_cnt, "sel_cnt", torch.int32, units, here), sm_scale, _arg(out, "out", torch.float32, B * Hq * D, here),
+        _opt(lse, "lse", torch.float32, B * Hq, here), _arg(workspace, "workspace", torch.uint8, 0, here),
+        workspace.numel(), EARLY_READS if early_reads else 0, _opt(err, "err", torch.int32, 1, here), st)
+    _check("sparse_paged_decode_attn_kv4", status)

@@ -161,7 +161,7 @@ def test_attention_refuses(lib):
 def test_binding_refuses_cpu_tensors_and_shapes():
     t = torch.zeros(2, 1, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
-        kvmm._rows(t, "new_k", 2, 1, 2, 64)
+        kvmm._rows(t, "new_k", 2, 1, 2, 64, 0)
     with pytest.raises(ValueError, match="dim|table"):
         kvmm.Rope(torch.zeros(4, 2, 16), 64)
     with pytest.raises(ValueError, match="CUDA"):
@@ -170,3 +170,7 @@ def test_binding_refuses_cpu_tensors_and_shapes():
         kvmm.sparse_paged_decode_attn_kv4(S, 0, t, t, t, t, t, None, t, t)
     with pytest.raises(ValueError, match="required"):
         kvmm.kv4_gather(S, 0, t, t, None, t, None, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        kvmm._arg(t, "q", torch.bfloat16, 1, 0)
+    with pytest.raises(ValueError, match="required"):
+        kvmm._arg(None, "q", torch.bfloat16, 1, 0)
