@@ -254,86 +254,81 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const int my_first = lo + kPages * warp;
     const int rounds = my_first < hi ? (hi - my_first + kStride - 1) / kStride : 0;
     const uint64_t policy = l2_policy_evict_first();
-    // A page's entry takes two dependent loads (its place in the selection, its table entry): place() starts the
-    // first, entry() takes it and starts the second, and a batch's run one and two batches ahead of its copies.
-    int pl_lp, pl_cnt, pl_seq, pl_u, pl_i;  // place(): logical page, pages of the unit, tokens, unit, place in it
-    auto place = [&](int rb) {
+    // A lane's page of the batch that starts with round rb: where it is held, and its word (unit * 64 + valid tokens;
+    // without tokens there is nothing to copy).  Two dependent loads (the place in the selection, the table entry)
+    // that a warp waits for once in kBatch steps, while the others go on (looking up a batch ahead took the same time
+    // and more registers).
+    const uint8_t* src = p.kv4_pool;
+    int pmeta = 0;
+    auto look_up = [&](int rb) {
         const int f = my_first + (rb + lane / kPages) * kStride + lane % kPages;
-        pl_u = -1;
+        pmeta = 0x7fffffc0;  // behind the piece: after every unit
         if (f >= hi || f < my_first) return;
-        int b, h;
+        int b, h, lp, n, u;
+        size_t unit;
         if (p.sel_idx != nullptr) {
-            pl_u = f / p.Kmax;
-            pl_i = f - pl_u * p.Kmax;
-            b = pl_u / p.Hkv;
-            h = pl_u - b * p.Hkv;
-            const size_t unit = (static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + h;
-            pl_cnt = p.sel_cnt[unit];
-            pl_lp = p.sel_idx[unit * p.Kmax + pl_i];
-        } else {
+            u = f / p.Kmax;
+            const int i = f - u * p.Kmax;
+            b = u / p.Hkv;
+            h = u - b * p.Hkv;
+            unit = (static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + h;
+            n = p.sel_cnt[unit];
+            lp = p.sel_idx[unit * p.Kmax + i];
+            const int seq = p.seq_len[p.b0 + b];
+            if (i == 0 && (n < 0 || n > p.Kmax || seq < 0 || seq > p.Pmax * T)) report(p.err, KVMM_ERR_OUT_OF_RANGE);
+            pmeta = u * 64;
+            if (i >= n) return;
+        } else {  // (the sum of the page counts has told of lengths out of range)
             b = list.batch_of(f);
-            pl_cnt = count[b];
-            h = (f - first[b]) / pl_cnt;
-            pl_i = pl_lp = f - first[b] - h * pl_cnt;
-            pl_u = b * p.Hkv + h;
+            h = (f - first[b]) / count[b];
+            lp = f - first[b] - h * count[b];
+            u = b * p.Hkv + h;
+            unit = (static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + h;
+            pmeta = u * 64;
         }
-        pl_seq = p.seq_len[p.b0 + b];
-    };
-    int en_phys, en_meta;  // entry(): physical page, unit * 64 + valid tokens (none: nothing to copy)
-    auto entry = [&]() {
-        en_phys = 0;
-        en_meta = 0x7fffffc0;  // behind the piece: after every unit
-        if (pl_u < 0) return;
-        en_meta = pl_u * 64;
-        const int cap = p.Pmax * T;
-        if (p.sel_idx != nullptr && pl_i == 0 && (pl_cnt < 0 || pl_cnt > p.Kmax || pl_seq < 0 || pl_seq > cap))
-            report(p.err, KVMM_ERR_OUT_OF_RANGE);  // (the sum of the page counts has told the others)
-        const int seq = min(max(pl_seq, 0), cap);
-        if (pl_i >= pl_cnt) return;
-        if (pl_lp < 0 || pl_lp >= (seq + T - 1) / T) {
+        const int seq = min(max(p.seq_len[p.b0 + b], 0), p.Pmax * T);
+        if (lp < 0 || lp >= (seq + T - 1) / T) {
             report(p.err, KVMM_ERR_OUT_OF_RANGE);
             return;
         }
-        en_meta += min(T, seq - pl_lp * T);
-        const int b = pl_u / p.Hkv;
-        en_phys = p.block_table[((static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + (pl_u - b * p.Hkv)) * p.Pmax + pl_lp];
-    };
-    int phys = 0, pmeta = 0;  // the batch being issued
-    auto issue = [&](int r) {  // start the copies of round r
-        if (r % kBatch == 0) {
-            phys = en_phys;
-            pmeta = en_meta;
-            if ((pmeta & 63) != 0 && (phys < 0 || phys >= p.n_phys)) {
-                report(p.err, phys < 0 ? KVMM_ERR_NULL_BLOCK : KVMM_ERR_OUT_OF_RANGE);
-                pmeta &= ~63;
-            }
-            entry();
-            place(r + 2 * kBatch);
+        const int32_t phys = p.block_table[unit * p.Pmax + lp];
+        if (phys < 0 || phys >= p.n_phys) {
+            report(p.err, phys < 0 ? KVMM_ERR_NULL_BLOCK : KVMM_ERR_OUT_OF_RANGE);
+            return;
         }
-        if (lane / kPages == r % kBatch) {
-            const int slot = r % kDepth, tile = lane % kPages;
-            uint64_t* bar = &sh.full[warp][slot];
-            int* meta = reinterpret_cast<int*>(&sh.meta[warp][slot]);
+        src = p.kv4_pool + static_cast<size_t>(phys) * Page::kBytes;
+        pmeta += min(T, seq - lp * T);
+    };
+    // this lane's copy of a step: the places its page and word go to, slot 0
+    const int my_round = lane / kPages, my_tile = lane % kPages;
+    const uint32_t bar_at = smem_addr(&sh.full[warp][0]);
+    const uint32_t meta_at = smem_addr(&sh.meta[warp][0]) + my_tile * 4;
+    const uint32_t copy_at = smem_addr(ring) + my_tile * Page::kBytes;
+    auto issue = [&](int r) {  // start the copies of round r
+        const int k = r % kBatch;
+        if (k == 0) look_up(r);
+        if (k == my_round) {
+            const uint32_t slot = r % kDepth;
             const int nv = pmeta & 63;
             if (kPages == 2) {
-                meta[tile] = pmeta;
+                sts_u32(meta_at + slot * 8, pmeta);
             } else {
-                meta[0] = pmeta - nv + min(nv, 16);
-                meta[1] = pmeta - nv + max(nv - 16, 0);
+                sts_u32(meta_at + slot * 8, pmeta - nv + min(nv, 16));
+                sts_u32(meta_at + slot * 8 + 4, pmeta - nv + max(nv - 16, 0));
             }
-            mbar_arrive_expect_tx(bar, nv > 0 ? Page::kBytes : 0);
-            if (nv > 0)
-                bulk_copy_g2s_hint(ring + slot * kSlot + tile * Page::kBytes,
-                                   p.kv4_pool + static_cast<size_t>(phys) * Page::kBytes, Page::kBytes, bar, policy);
+            mbar_arrive_expect_tx_at(bar_at + slot * 8, nv > 0 ? Page::kBytes : 0);
+            if (nv > 0) bulk_copy_g2s_hint_at(copy_at + slot * kSlot, src, Page::kBytes, bar_at + slot * 8, policy);
         }
     };
-    place(0);
-    entry();
-    place(kBatch);
 #pragma unroll
     for (int r = 0; r < kDepth; ++r)
         if (r < rounds) issue(r);
 
+    // this lane's places in a page: its K row and scales, its V pairs' rows and scales
+    const uint32_t ring_at = smem_addr(ring);
+    const uint32_t k_off = ra * Page::kRow + tig * (D / 8), ks_off = ra * Page::kGroups + (D == 128 ? 2 * tig : tig);
+    const uint32_t v0_off = t0 * Page::kRow + gid * (D / 16), v1_off = t1 * Page::kRow + gid * (D / 16);
+    const uint32_t vs0_off = t0 * Page::kGroups + gid * kMine / 16, vs1_off = t1 * Page::kGroups + gid * kMine / 16;
     int r = 0;
     int seg_unit[2] = {-1, -1};  // units whose parts this CTA stores: the one that began before, the one that goes on
 
@@ -378,6 +373,175 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        // One step.  FULL: both tiles are the unit's and have all their tokens (nearly every step: without its masks and
+        // branches, every page of 32 sequences up to 16K tokens takes 87 us, with them 95).
+        auto step = [&](auto whole_step, const uint32_t pg, const int nv0, const int nv1) {
+            constexpr bool full = decltype(whole_step)::value;
+            // tile j: tokens 16j .. 16j + 15 of the step, in page j (or the second half of the page)
+            constexpr int kTile = kPages == 2 ? Page::kBytes : 16 * Page::kRow;
+            constexpr int kTileScales = kPages == 2 ? Page::kBytes : 16 * Page::kGroups;
+            const bool two = full || nv1 != 0;
+            // ---- scores before their factor: x[j] = token ra of tile j with heads col0, col0 + 1, then token ra + 8
+            float x[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (j == 1 && !two) {
+                    x[1][0] = x[1][1] = x[1][2] = x[1][3] = -INFINITY;
+                    break;
+                }
+                float c[4] = {};
+                uint32_t wa[kWords], wb[kWords], sa[kWords], sb[kWords];
+                auto keys = [&](auto jc) {
+                    constexpr int kAt = decltype(jc)::value * kTile, kSc = Page::kKeyScales + decltype(jc)::value * kTileScales;
+                    if constexpr (D == 128) {
+                        const uint4 y = lds_v4<kAt>(pg + k_off), z = lds_v4<kAt + 8 * Page::kRow>(pg + k_off);
+                        wa[0] = y.x, wa[1] = y.y, wa[2] = y.z, wa[3] = y.w;
+                        wb[0] = z.x, wb[1] = z.y, wb[2] = z.z, wb[3] = z.w;
+                        // scale groups 2 tig and 2 tig + 1
+                        const uint32_t ha = e4m3x2_to_half2(lds_u16<kSc>(pg + ks_off));
+                        const uint32_t hb = e4m3x2_to_half2(lds_u16<kSc + 8 * Page::kGroups>(pg + ks_off));
+                        sa[0] = sa[1] = prmt(ha, ha, 0x1010);
+                        sa[2] = sa[3] = prmt(ha, ha, 0x3232);
+                        sb[0] = sb[1] = prmt(hb, hb, 0x1010);
+                        sb[2] = sb[3] = prmt(hb, hb, 0x3232);
+                    } else {
+                        const uint2 y = lds_v2<kAt>(pg + k_off), z = lds_v2<kAt + 8 * Page::kRow>(pg + k_off);
+                        wa[0] = y.x, wa[1] = y.y, wb[0] = z.x, wb[1] = z.y;
+                        const uint32_t hs = e4m3x2_to_half2(
+                            prmt(lds_u8<kSc>(pg + ks_off), lds_u8<kSc + 8 * Page::kGroups>(pg + ks_off), 0x0040));
+                        sa[0] = sa[1] = prmt(hs, hs, 0x1010);
+                        sb[0] = sb[1] = prmt(hs, hs, 0x3232);
+                    }
+                };
+                if (j == 0) keys(std::integral_constant<int, 0>{});
+                else keys(std::integral_constant<int, 1>{});
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    mma_f16_16816(c, half2_mul(e2m1x2_to_half2<0>(wa[w]), sa[w]),
+                                  half2_mul(e2m1x2_to_half2<0>(wb[w]), sb[w]),
+                                  half2_mul(e2m1x2_to_half2<1>(wa[w]), sa[w]),
+                                  half2_mul(e2m1x2_to_half2<1>(wb[w]), sb[w]), qf[4 * w], qf[4 * w + 1]);
+                    mma_f16_16816(c, half2_mul(e2m1x2_to_half2<2>(wa[w]), sa[w]),
+                                  half2_mul(e2m1x2_to_half2<2>(wb[w]), sb[w]),
+                                  half2_mul(e2m1x2_to_half2<3>(wa[w]), sa[w]),
+                                  half2_mul(e2m1x2_to_half2<3>(wb[w]), sb[w]), qf[4 * w + 2], qf[4 * w + 3]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[j][i] = c[i];
+                if (!full) {  // selected, not multiplied: what the page holds there may be anything
+                    if (ra >= (j == 0 ? nv0 : nv1)) x[j][0] = x[j][1] = -INFINITY;
+                    if (ra + 8 >= (j == 0 ? nv0 : nv1)) x[j][2] = x[j][3] = -INFINITY;
+                }
+            }
+            // ---- probabilities against a reference per head, raised only when a score exceeds it by more than
+            // kSlack (one vote instead of a reduction a step).  The reference lies kLift below the maximum it
+            // was taken from, so a probability is at most 2^(kSlack + kLift) = 2^15, and fp16 hi + lo holds it
+            // to 2^-22 of itself or 2^-25 * 2^-kLift of the largest.
+            constexpr float kSlack = 8.f, kLift = 7.f;
+            float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])) * zf0;
+            float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])) * zf1;
+            if (!__all_sync(kFullMask, mx0 <= m0 + (kSlack + kLift) && mx1 <= m1 + (kSlack + kLift))) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, off));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, off));
+                }
+                // every step has a valid token, so the references are finite from the first one on
+                const float n0 = fmaxf(m0, mx0 - kLift), n1 = fmaxf(m1, mx1 - kLift);
+                const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
+                l0 *= a0;
+                l1 *= a1;
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    o[i][0] *= a0;
+                    o[i][1] *= a1;
+                    o[i][2] *= a0;
+                    o[i][3] *= a1;
+                }
+                m0 = n0;
+                m1 = n1;
+            }
+            uint32_t bh[2][2], bl[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float p0 = fast_exp2(fmaf(x[j][0], zf0, -m0)), p1 = fast_exp2(fmaf(x[j][1], zf1, -m1));
+                const float p2 = fast_exp2(fmaf(x[j][2], zf0, -m0)), p3 = fast_exp2(fmaf(x[j][3], zf1, -m1));
+                l0 += p0 + p2;
+                l1 += p1 + p3;
+                const uint32_t h01 = pack_half2(p0, p1), h23 = pack_half2(p2, p3);
+                if (DUP) {  // columns 0-3 carry hi, 4-7 lo: p less its hi part in the latter's lanes
+                    bh[j][0] = movmatrix_trans(pack_half2(fmaf(half_lo(h01), lo_lane, p0), fmaf(half_hi(h01), lo_lane, p1)));
+                    bh[j][1] = movmatrix_trans(pack_half2(fmaf(half_lo(h23), lo_lane, p2), fmaf(half_hi(h23), lo_lane, p3)));
+                } else {
+                    bh[j][0] = movmatrix_trans(h01);
+                    bh[j][1] = movmatrix_trans(h23);
+                    bl[j][0] = movmatrix_trans(pack_half2(p0 - half_lo(h01), p1 - half_hi(h01)));
+                    bl[j][1] = movmatrix_trans(pack_half2(p2 - half_lo(h23), p3 - half_hi(h23)));
+                }
+            }
+            // ---- values: channels gid * kMine .. + kMine - 1 of tokens t0, t1, t0 + 8, t1 + 8 of a tile -----------
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (j == 1 && !two) break;
+                uint32_t w[4][kVWords];
+                uint32_t sc[4];
+                auto values = [&](auto jc) {
+                    constexpr int kAt = Page::kValues + decltype(jc)::value * kTile;
+                    constexpr int kSc = Page::kValueScales + decltype(jc)::value * kTileScales;
+                    if constexpr (D == 128) {
+                        const uint2 y0 = lds_v2<kAt>(pg + v0_off), y1 = lds_v2<kAt>(pg + v1_off);
+                        const uint2 y2 = lds_v2<kAt + 8 * Page::kRow>(pg + v0_off), y3 = lds_v2<kAt + 8 * Page::kRow>(pg + v1_off);
+                        w[0][0] = y0.x, w[0][1] = y0.y, w[1][0] = y1.x, w[1][1] = y1.y;
+                        w[2][0] = y2.x, w[2][1] = y2.y, w[3][0] = y3.x, w[3][1] = y3.y;
+                    } else {
+                        w[0][0] = lds_u32<kAt>(pg + v0_off), w[1][0] = lds_u32<kAt>(pg + v1_off);
+                        w[2][0] = lds_u32<kAt + 8 * Page::kRow>(pg + v0_off), w[3][0] = lds_u32<kAt + 8 * Page::kRow>(pg + v1_off);
+                    }
+                    sc[0] = lds_u8<kSc>(pg + vs0_off), sc[1] = lds_u8<kSc>(pg + vs1_off);
+                    sc[2] = lds_u8<kSc + 8 * Page::kGroups>(pg + vs0_off), sc[3] = lds_u8<kSc + 8 * Page::kGroups>(pg + vs1_off);
+                };
+                if (j == 0) values(std::integral_constant<int, 0>{});
+                else values(std::integral_constant<int, 1>{});
+                if (!full) {  // a scale of zero: codes are always finite
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (((k & 1) ? t1 : t0) + (k >> 1) * 8 >= (j == 0 ? nv0 : nv1)) sc[k] = 0u;
+                }
+                const uint32_t s01 = e4m3x2_to_half2(prmt(sc[0], sc[1], 0x0040));
+                const uint32_t s23 = e4m3x2_to_half2(prmt(sc[2], sc[3], 0x0040));
+                // byte i of an even / odd word: channel 2i / 2i + 1 of a token pair
+                uint32_t ev01[kVWords], od01[kVWords], ev23[kVWords], od23[kVWords];
+#pragma unroll
+                for (int i = 0; i < kVWords; ++i) {
+                    ev01[i] = (w[0][i] & 0x0f0f0f0fu) | ((w[1][i] << 4) & 0xf0f0f0f0u);
+                    od01[i] = ((w[0][i] >> 4) & 0x0f0f0f0fu) | (w[1][i] & 0xf0f0f0f0u);
+                    ev23[i] = (w[2][i] & 0x0f0f0f0fu) | ((w[3][i] << 4) & 0xf0f0f0f0u);
+                    od23[i] = ((w[2][i] >> 4) & 0x0f0f0f0fu) | (w[3][i] & 0xf0f0f0f0u);
+                }
+                // tile i: rows gid are channel i of the lane's, rows gid + 8 channel kTiles + i
+                auto tile = [&](auto ic) {
+                    constexpr int i = decltype(ic)::value;
+                    constexpr int a = i, b = kTiles + i;  // channels
+                    constexpr int ba = (a % 8) / 2, bb = (b % 8) / 2;
+                    const uint32_t xa = (a & 1) ? od01[a / 8] : ev01[a / 8], xb = (b & 1) ? od01[b / 8] : ev01[b / 8];
+                    const uint32_t ya = (a & 1) ? od23[a / 8] : ev23[a / 8], yb = (b & 1) ? od23[b / 8] : ev23[b / 8];
+                    const uint32_t a0 = half2_mul(e2m1x2_to_half2<ba>(xa), s01), a1 = half2_mul(e2m1x2_to_half2<bb>(xb), s01);
+                    const uint32_t a2 = half2_mul(e2m1x2_to_half2<ba>(ya), s23), a3 = half2_mul(e2m1x2_to_half2<bb>(yb), s23);
+                    mma_f16_16816(o[i], a0, a1, a2, a3, bh[j][0], bh[j][1]);
+                    if (!DUP) mma_f16_16816(o[i], a0, a1, a2, a3, bl[j][0], bl[j][1]);
+                };
+                tile(std::integral_constant<int, 0>{});
+                tile(std::integral_constant<int, 1>{});
+                tile(std::integral_constant<int, 2>{});
+                tile(std::integral_constant<int, 3>{});
+                if constexpr (kTiles == 8) {
+                    tile(std::integral_constant<int, 4>{});
+                    tile(std::integral_constant<int, 5>{});
+                    tile(std::integral_constant<int, 6>{});
+                    tile(std::integral_constant<int, 7>{});
+                }
+            }
+        };
         while (r < rounds) {
             const int slot = r % kDepth;
             if (__any_sync(kFullMask, !mbar_wait_bounded(&sh.full[warp][slot], (r / kDepth) & 1, kWaitNs))) {
@@ -389,176 +553,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                 break;
             }
             const int2 meta = sh.meta[warp][slot];
-            if ((meta.x >> 6) > u) break;  // of a later unit
-            int nv[2] = {(meta.x >> 6) == u ? meta.x & 63 : 0, (meta.y >> 6) == u ? meta.y & 63 : 0};
-            const uint8_t* pg = ring + slot * kSlot;
-            if (kPages == 2 && nv[0] == 0) {  // the first page is of the unit before, or could not be read
-                pg += Page::kBytes;
-                nv[0] = nv[1];
-                nv[1] = 0;
+            const uint32_t pg = ring_at + slot * kSlot;
+            if (meta.x == u * 64 + 16 && meta.y == u * 64 + 16) {
+                step(std::true_type{}, pg, 16, 16);
+            } else {
+                if ((meta.x >> 6) > u) break;  // the step is of a later unit
+                const int nv0 = (meta.x >> 6) == u ? meta.x & 63 : 0, nv1 = (meta.y >> 6) == u ? meta.y & 63 : 0;
+                if (nv0 > 0) step(std::false_type{}, pg, nv0, nv1);
+                // the first page is of the unit before, or could not be read
+                else if (kPages == 2 && nv1 > 0) step(std::false_type{}, pg + Page::kBytes, nv1, 0);
+                if ((meta.y >> 6) > u && (meta.y & 63) != 0) break;  // the second page is of a later unit
             }
-            if (nv[0] > 0) {
-                // tile j: tokens 16j .. 16j + 15 of the step, in page j (or the second half of the page)
-                auto tile_at = [&](int j) { return kPages == 2 ? pg + j * Page::kBytes : pg; };
-                constexpr int kRow1 = kPages == 2 ? 0 : 16;  // the second tile's first row in its page
-                const bool two = nv[1] != 0;
-                const bool full = nv[0] + nv[1] == 32;
-                // ---- scores before their factor: x[j] = token ra of tile j with heads col0, col0 + 1, then token ra + 8
-                float x[2][4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (j == 1 && !two) {
-                        x[1][0] = x[1][1] = x[1][2] = x[1][3] = -INFINITY;
-                        break;
-                    }
-                    float c[4] = {};
-                    const uint8_t* base = tile_at(j);
-                    const int row = j * kRow1 + ra;
-                    const uint8_t* ka = base + row * Page::kRow + tig * (D / 8);
-                    const uint8_t* kb = ka + 8 * Page::kRow;
-                    uint32_t wa[kWords], wb[kWords], sa[kWords], sb[kWords];
-                    if (D == 128) {
-                        const uint4 y = ld_shared_v4(ka), z = ld_shared_v4(kb);
-                        wa[0] = y.x, wa[1] = y.y, wa[kWords - 2] = y.z, wa[kWords - 1] = y.w;
-                        wb[0] = z.x, wb[1] = z.y, wb[kWords - 2] = z.z, wb[kWords - 1] = z.w;
-                        // scale groups 2 tig and 2 tig + 1
-                        const uint8_t* sc = base + Page::kKeyScales + row * Page::kGroups + 2 * tig;
-                        const uint32_t ha = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sc));
-                        const uint32_t hb = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sc + 8 * Page::kGroups));
-                        sa[0] = sa[1] = prmt(ha, ha, 0x1010);
-                        sa[kWords - 2] = sa[kWords - 1] = prmt(ha, ha, 0x3232);
-                        sb[0] = sb[1] = prmt(hb, hb, 0x1010);
-                        sb[kWords - 2] = sb[kWords - 1] = prmt(hb, hb, 0x3232);
-                    } else {
-                        const uint2 y = ld_shared_v2(ka), z = ld_shared_v2(kb);
-                        wa[0] = y.x, wa[1] = y.y, wb[0] = z.x, wb[1] = z.y;
-                        const uint8_t* sc = base + Page::kKeyScales + row * Page::kGroups + tig;
-                        const uint32_t hs = e4m3x2_to_half2(sc[0] | (static_cast<uint32_t>(sc[8 * Page::kGroups]) << 8));
-                        sa[0] = sa[1] = prmt(hs, hs, 0x1010);
-                        sb[0] = sb[1] = prmt(hs, hs, 0x3232);
-                    }
-#pragma unroll
-                    for (int w = 0; w < kWords; ++w) {
-                        mma_f16_16816(c, half2_mul(e2m1x2_to_half2<0>(wa[w]), sa[w]),
-                                      half2_mul(e2m1x2_to_half2<0>(wb[w]), sb[w]),
-                                      half2_mul(e2m1x2_to_half2<1>(wa[w]), sa[w]),
-                                      half2_mul(e2m1x2_to_half2<1>(wb[w]), sb[w]), qf[4 * w], qf[4 * w + 1]);
-                        mma_f16_16816(c, half2_mul(e2m1x2_to_half2<2>(wa[w]), sa[w]),
-                                      half2_mul(e2m1x2_to_half2<2>(wb[w]), sb[w]),
-                                      half2_mul(e2m1x2_to_half2<3>(wa[w]), sa[w]),
-                                      half2_mul(e2m1x2_to_half2<3>(wb[w]), sb[w]), qf[4 * w + 2], qf[4 * w + 3]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[j][i] = c[i];
-                    if (!full) {  // selected, not multiplied: what the page holds there may be anything
-                        if (ra >= nv[j]) x[j][0] = x[j][1] = -INFINITY;
-                        if (ra + 8 >= nv[j]) x[j][2] = x[j][3] = -INFINITY;
-                    }
-                }
-                // ---- probabilities against a reference per head, raised only when a score exceeds it by more than
-                // kSlack (one vote instead of a reduction a step).  The reference lies kLift below the maximum it
-                // was taken from, so a probability is at most 2^(kSlack + kLift) = 2^15, and fp16 hi + lo holds it
-                // to 2^-22 of itself or 2^-25 * 2^-kLift of the largest.
-                constexpr float kSlack = 8.f, kLift = 7.f;
-                float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])) * zf0;
-                float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])) * zf1;
-                if (!__all_sync(kFullMask, mx0 <= m0 + (kSlack + kLift) && mx1 <= m1 + (kSlack + kLift))) {
-#pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) {
-                        mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, off));
-                        mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, off));
-                    }
-                    // every step has a valid token, so the references are finite from the first one on
-                    const float n0 = fmaxf(m0, mx0 - kLift), n1 = fmaxf(m1, mx1 - kLift);
-                    const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
-                    l0 *= a0;
-                    l1 *= a1;
-#pragma unroll
-                    for (int i = 0; i < kTiles; ++i) {
-                        o[i][0] *= a0;
-                        o[i][1] *= a1;
-                        o[i][2] *= a0;
-                        o[i][3] *= a1;
-                    }
-                    m0 = n0;
-                    m1 = n1;
-                }
-                uint32_t bh[2][2], bl[2][2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float p0 = fast_exp2(fmaf(x[j][0], zf0, -m0)), p1 = fast_exp2(fmaf(x[j][1], zf1, -m1));
-                    const float p2 = fast_exp2(fmaf(x[j][2], zf0, -m0)), p3 = fast_exp2(fmaf(x[j][3], zf1, -m1));
-                    l0 += p0 + p2;
-                    l1 += p1 + p3;
-                    const uint32_t h01 = pack_half2(p0, p1), h23 = pack_half2(p2, p3);
-                    if (DUP) {  // columns 0-3 carry hi, 4-7 lo: p less its hi part in the latter's lanes
-                        bh[j][0] = movmatrix_trans(pack_half2(fmaf(half_lo(h01), lo_lane, p0), fmaf(half_hi(h01), lo_lane, p1)));
-                        bh[j][1] = movmatrix_trans(pack_half2(fmaf(half_lo(h23), lo_lane, p2), fmaf(half_hi(h23), lo_lane, p3)));
-                    } else {
-                        bh[j][0] = movmatrix_trans(h01);
-                        bh[j][1] = movmatrix_trans(h23);
-                        bl[j][0] = movmatrix_trans(pack_half2(p0 - half_lo(h01), p1 - half_hi(h01)));
-                        bl[j][1] = movmatrix_trans(pack_half2(p2 - half_lo(h23), p3 - half_hi(h23)));
-                    }
-                }
-                // ---- values: channels gid * kMine .. + kMine - 1 of tokens t0, t1, t0 + 8, t1 + 8 of a tile -----------
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (j == 1 && !two) break;
-                    const uint8_t* base = tile_at(j);
-                    const uint8_t* vp = base + Page::kValues + j * kRow1 * Page::kRow + gid * (D / 16);
-                    const uint8_t* vs = base + Page::kValueScales + j * kRow1 * Page::kGroups + gid * kMine / 16;
-                    uint32_t w[4][kVWords];
-                    uint32_t sc[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int t = ((k & 1) ? t1 : t0) + (k >> 1) * 8;
-                        if (D == 128) {
-                            const uint2 y = ld_shared_v2(vp + t * Page::kRow);
-                            w[k][0] = y.x;
-                            w[k][kVWords - 1] = y.y;
-                        } else {
-                            w[k][0] = *reinterpret_cast<const uint32_t*>(vp + t * Page::kRow);
-                        }
-                        sc[k] = vs[t * Page::kGroups];
-                        if (!full && t >= nv[j]) sc[k] = 0u;  // a scale of zero: codes are always finite
-                    }
-                    const uint32_t s01 = e4m3x2_to_half2(sc[0] | (sc[1] << 8));
-                    const uint32_t s23 = e4m3x2_to_half2(sc[2] | (sc[3] << 8));
-                    // byte i of an even / odd word: channel 2i / 2i + 1 of a token pair
-                    uint32_t ev01[kVWords], od01[kVWords], ev23[kVWords], od23[kVWords];
-#pragma unroll
-                    for (int i = 0; i < kVWords; ++i) {
-                        ev01[i] = (w[0][i] & 0x0f0f0f0fu) | ((w[1][i] << 4) & 0xf0f0f0f0u);
-                        od01[i] = ((w[0][i] >> 4) & 0x0f0f0f0fu) | (w[1][i] & 0xf0f0f0f0u);
-                        ev23[i] = (w[2][i] & 0x0f0f0f0fu) | ((w[3][i] << 4) & 0xf0f0f0f0u);
-                        od23[i] = ((w[2][i] >> 4) & 0x0f0f0f0fu) | (w[3][i] & 0xf0f0f0f0u);
-                    }
-                    // tile i: rows gid are channel i of the lane's, rows gid + 8 channel kTiles + i
-                    auto tile = [&](auto ic) {
-                        constexpr int i = decltype(ic)::value;
-                        constexpr int a = i, b = kTiles + i;  // channels
-                        constexpr int ba = (a % 8) / 2, bb = (b % 8) / 2;
-                        const uint32_t xa = (a & 1) ? od01[a / 8] : ev01[a / 8], xb = (b & 1) ? od01[b / 8] : ev01[b / 8];
-                        const uint32_t ya = (a & 1) ? od23[a / 8] : ev23[a / 8], yb = (b & 1) ? od23[b / 8] : ev23[b / 8];
-                        const uint32_t a0 = half2_mul(e2m1x2_to_half2<ba>(xa), s01), a1 = half2_mul(e2m1x2_to_half2<bb>(xb), s01);
-                        const uint32_t a2 = half2_mul(e2m1x2_to_half2<ba>(ya), s23), a3 = half2_mul(e2m1x2_to_half2<bb>(yb), s23);
-                        mma_f16_16816(o[i], a0, a1, a2, a3, bh[j][0], bh[j][1]);
-                        if (!DUP) mma_f16_16816(o[i], a0, a1, a2, a3, bl[j][0], bl[j][1]);
-                    };
-                    tile(std::integral_constant<int, 0>{});
-                    tile(std::integral_constant<int, 1>{});
-                    tile(std::integral_constant<int, 2>{});
-                    tile(std::integral_constant<int, 3>{});
-                    if constexpr (kTiles == 8) {
-                        tile(std::integral_constant<int, 4>{});
-                        tile(std::integral_constant<int, 5>{});
-                        tile(std::integral_constant<int, 6>{});
-                        tile(std::integral_constant<int, 7>{});
-                    }
-                }
-            }
-            if ((meta.y >> 6) > u && (meta.y & 63) != 0) break;  // the second page is of a later unit
             ++r;
             __syncwarp();
             if (r + kDepth - 1 < rounds) {
