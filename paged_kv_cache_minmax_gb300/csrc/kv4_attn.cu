@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     constexpr int kBatch = 32 / kPages;  // rounds looked up at once, a page a lane
     uint8_t* ring = smem + static_cast<size_t>(warp) * kDepth * kSlot;
     const int my_first = lo + kPages * warp;
-    const int rounds = my_first < hi ? (hi - my_first + kStride - 1) / kStride : 0;
+    const unsigned rounds = my_first < hi ? static_cast<unsigned>(hi - my_first + kStride - 1) / kStride : 0u;
     const uint64_t policy = l2_policy_evict_first();
     // A lane's page of the batch that starts with round rb: where it is held, and its word (unit * 64 + valid tokens;
     // without tokens there is nothing to copy).  Two dependent loads (the place in the selection, the table entry)
@@ -300,13 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         pmeta += min(T, seq - lp * T);
     };
     // this lane's copy of a step: the places its page and word go to, slot 0
-    const int my_round = lane / kPages, my_tile = lane % kPages;
+    const unsigned my_round = static_cast<unsigned>(lane) / kPages, my_tile = static_cast<unsigned>(lane) % kPages;
     const uint32_t bar_at = smem_addr(&sh.full[warp][0]);
     const uint32_t meta_at = smem_addr(&sh.meta[warp][0]) + my_tile * 4;
     const uint32_t copy_at = smem_addr(ring) + my_tile * Page::kBytes;
-    auto issue = [&](int r) {  // start the copies of round r
-        const int k = r % kBatch;
-        if (k == 0) look_up(r);
+    auto issue = [&](unsigned r) {  // start the copies of round r
+        const unsigned k = r % kBatch;
+        if (k == 0) look_up(static_cast<int>(r));
         if (k == my_round) {
             const uint32_t slot = r % kDepth;
             const int nv = pmeta & 63;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const uint32_t k_off = ra * Page::kRow + tig * (D / 8), ks_off = ra * Page::kGroups + (D == 128 ? 2 * tig : tig);
     const uint32_t v0_off = t0 * Page::kRow + gid * (D / 16), v1_off = t1 * Page::kRow + gid * (D / 16);
     const uint32_t vs0_off = t0 * Page::kGroups + gid * kMine / 16, vs1_off = t1 * Page::kGroups + gid * kMine / 16;
-    int r = 0;
+    unsigned r = 0;
     int seg_unit[2] = {-1, -1};  // units whose parts this CTA stores: the one that began before, the one that goes on
 
     for (int u = first_unit;; ++u) {
@@ -543,10 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             }
         };
         while (r < rounds) {
-            const int slot = r % kDepth;
+            const uint32_t slot = r % kDepth;
             if (__any_sync(kFullMask, !mbar_wait_bounded(&sh.full[warp][slot], (r / kDepth) & 1, kWaitNs))) {
                 if (lane == 0) report(p.err, KVMM_ERR_TIMEOUT);  // the remaining pages are dropped
-                for (int k = r; k < min(rounds, r + kDepth); ++k)  // what is in flight lands before the CTA leaves
+                for (unsigned k = r; k < min(rounds, r + kDepth); ++k)  // what is in flight lands before the CTA leaves
                     mbar_wait_bounded(&sh.full[warp][k % kDepth], (k / kDepth) & 1, 100000000ull);
                 __syncwarp();
                 r = rounds;
