@@ -147,6 +147,14 @@ __device__ __forceinline__ uint32_t cluster_ctarank()
     return r;
 }
 
+// the cluster's number in a one-dimensional grid
+__device__ __forceinline__ uint32_t cluster_id()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+
 // every thread of every CTA of the cluster arrives and waits; release/acquire
 // make each CTA's earlier shared-memory writes visible to the others
 __device__ __forceinline__ void cluster_sync()

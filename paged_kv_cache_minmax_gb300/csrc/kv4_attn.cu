@@ -67,6 +67,7 @@ struct Shared {
     float f[kWarps][8];        // weight of each warp's partial
     float ref[8], sum[8];      // the CTA's reference and sum per head
     int scan[kWarps];
+    int total;                 // pages of the list
     int last[2];
     float recv[8 * 128 + kKv4MaxCluster];  // received: every CTA's partial of this CTA's slice of the outputs
     float rstat[kKv4MaxCluster][16];       // received: (reference, sum) per head of every CTA of the cluster
@@ -87,15 +88,18 @@ __device__ __forceinline__ float fast_exp2(float x)
     return y;
 }
 
-// `total` pages dealt to n CTAs: the first total % n take one more than the others
+// `total` pages dealt to n CTAs: CTA c's piece starts at floor(c * total / n), so that units of one length of which
+// each fills the same number of CTAs begin where a piece does
 struct Pieces {
-    int each, more;
-    __device__ __forceinline__ Pieces(int total, int n) : each(total / n), more(total % n) {}
-    __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
-    __device__ __forceinline__ int owner(int f) const  // the CTA that takes page f
+    int total, n, each, more;
+    __device__ __forceinline__ Pieces(int total_, int n_) : total(total_), n(n_), each(total_ / n_), more(total_ % n_) {}
+    __device__ __forceinline__ int start(int c) const { return c * each + c * more / n; }  // c, more < n <= 256
+    __device__ __forceinline__ int owner(int f) const  // the CTA that takes page f < total
     {
-        const int long_pages = more * (each + 1);
-        return f < long_pages ? f / (each + 1) : more + (f - long_pages) / each;  // f < total: each > 0 there
+        int c = min(static_cast<int>(static_cast<float>(f) * n / total), n - 1);  // at most one off
+        while (start(c) > f) --c;
+        while (start(c + 1) <= f) ++c;
+        return c;
     }
 };
 
@@ -218,16 +222,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         }
     }
     const List list{first, count, p.sel_idx != nullptr ? p.Kmax : 0, p.Hkv, p.nb};
-    const Pieces pieces(total, N);
-    int lo, hi;
+    // (integer divisions are a large part of what comes before the first copy: a cluster's CTA makes two)
+    int lo, hi, first_unit;
     if (p.C > 0) {  // a unit's places dealt to its C CTAs
-        const int u = rank / p.C, c = rank - u * p.C;
-        lo = u * p.Kmax + p.Kmax * c / p.C;  // (Kmax <= 32768, C <= 16)
-        hi = u * p.Kmax + p.Kmax * (c + 1) / p.C;  // > lo: C <= Kmax
+        const int c = p.C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+        first_unit = p.C > 1 ? static_cast<int>(cluster_id()) : rank;
+        lo = first_unit * p.Kmax + p.Kmax * c / p.C;  // (Kmax <= 32768, C <= 16)
+        hi = first_unit * p.Kmax + p.Kmax * (c + 1) / p.C;  // > lo: C <= Kmax
     } else {
+        if (total == 0) return;
+        const Pieces pieces(total, min(N, total));  // no piece is empty: the CTAs behind have none
+        if (rank >= pieces.n) return;
+        if (tid == 0) sh.total = total;
         lo = pieces.start(rank);
         hi = pieces.start(rank + 1);
-        if (lo >= hi) return;
+        first_unit = list.unit_of(lo);
     }
 
     const int gid = lane >> 2, tig = lane & 3;
@@ -237,7 +246,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const int t0 = (2 * tig) ^ (tig & 1), t1 = t0 ^ 1;  // ... and of its V pairs: (t0, t1) and (t0 + 8, t1 + 8)
     const float lo_lane = tig < 2 ? 0.f : -1.f;  // G <= 4: the lanes whose columns carry the lo parts
     // the queries of the first unit are on their way while the pages are looked up
-    const int first_unit = list.unit_of(lo);
     uint4 qv[D / 32];
     auto load_queries = [&](int u) {
         const kvmm_bf16* qh = p.q + ((static_cast<size_t>(p.b0) * p.Hkv + u) * G + head) * D + tig * (D / 4);
@@ -267,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         int b, h, lp, n, u;
         size_t unit;
         if (p.sel_idx != nullptr) {
-            u = f / p.Kmax;
+            u = p.C > 0 ? first_unit : f / p.Kmax;
             const int i = f - u * p.Kmax;
             b = u / p.Hkv;
             h = u - b * p.Hkv;
@@ -339,7 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             if (u + 1 >= p.nb * p.Hkv) break;
             continue;
         }
-        if (u != first_unit) load_queries(u);
         // queries: halves of the lane's channels of its head, scaled by a power of two
         uint32_t qf[2 * kTiles];
         float zf0, zf1;
@@ -572,6 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             }
         }
 
+        if (uend < hi) {  // the next unit's queries are on their way during the merge
+            int nu = u + 1, b0, b1;
+            for (list.range(nu, b0, b1); b0 == b1; list.range(nu, b0, b1)) ++nu;  // (a unit with pages follows: hi is beyond)
+            load_queries(nu);
+        }
         // ---- the unit ends here (or this CTA's piece of it): merge the warps ---------------------------------------
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
@@ -703,6 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
 
     // ---- units that fell on several CTAs: whoever stored the last part combines them ---------------------------
     // A unit's counter is that of the first CTA it lies in, which can be the first for one such unit only.
+    if (p.C > 0) return;
+    const Pieces pieces(sh.total, min(N, sh.total));
     if (tid < 2) {
         sh.last[tid] = 0;
         const int u = seg_unit[tid];

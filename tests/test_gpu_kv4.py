@@ -236,6 +236,23 @@ def test_clusters_of_every_size(K, B, Hkv, G, D, T):
     c.check()
 
 
+@pytest.mark.parametrize("Pmax", [40, 1000, 32768])
+def test_short_sequences_in_a_long_table(Pmax):
+    """Far fewer pages than the table has room for: fewer than the CTAs launched, too."""
+    c = Cache([70, 1, 0, 150], Hkv=2, Hq=8, D=64, L=1, layer=0, Pmax=Pmax)
+    for _ in range(2):  # the counters are back at zero
+        c.out.fill_(5.0)
+        c.attend()
+        torch.cuda.synchronize()
+        assert int(c.err) == 0
+        c.check()
+    assert int(c.ws[:1024].max()) == 0
+    d = Cache([17], Hkv=1, Hq=8, D=128, L=1, layer=0, Pmax=Pmax)
+    d.attend()
+    torch.cuda.synchronize()
+    d.check()
+
+
 def test_selections_of_more_units_than_sms():
     """320 units: the selected pages of all are dealt evenly."""
     rng = np.random.default_rng(5)
