@@ -176,7 +176,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     }
     __syncwarp();  // converged for the aligned barrier
     if (p.C > 1) cluster_arrive();  // passed before anything reaches another CTA
-    pdl_wait_then_release();
+    // Every input may come from the preceding kernels.  Where the caller vouches for seq_len and the table, a launch
+    // over every page sums the lengths and looks its first pages up while the preceding kernel drains, and waits for
+    // it before it reads a query or a page or stores anything but error bits (selections come from that kernel: with
+    // them there is nothing to read early).
+    const bool early = p.early != 0 && p.sel_idx == nullptr;
+    if (!early) pdl_wait_then_release();
 
     // ---- the page list and this CTA's piece of it ------------------------------------------------------------
     int total;
@@ -212,14 +217,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         }
         if (tid == 0) first[p.nb] = total;
         __syncthreads();
-        // sequences without a token: their results are written here, spread over the CTAs
-        for (int b = rank; b < p.nb; b += N) {
-            if (count[b] != 0) continue;
-            float* o = p.out + static_cast<size_t>(p.b0 + b) * p.Hq * D;
-            for (int e = tid; e < p.Hq * D; e += kThreads) o[e] = 0.f;
-            if (p.lse)
-                for (int e = tid; e < p.Hq; e += kThreads) p.lse[static_cast<size_t>(p.b0 + b) * p.Hq + e] = -INFINITY;
-        }
     }
     const List list{first, count, p.sel_idx != nullptr ? p.Kmax : 0, p.Hkv, p.nb};
     // (integer divisions are a large part of what comes before the first copy: a cluster's CTA makes two)
@@ -230,13 +227,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         lo = first_unit * p.Kmax + p.Kmax * c / p.C;  // (Kmax <= 32768, C <= 16)
         hi = first_unit * p.Kmax + p.Kmax * (c + 1) / p.C;  // > lo: C <= Kmax
     } else {
-        if (total == 0) return;
-        const Pieces pieces(total, min(N, total));  // no piece is empty: the CTAs behind have none
-        if (rank >= pieces.n) return;
-        if (tid == 0) sh.total = total;
-        lo = pieces.start(rank);
-        hi = pieces.start(rank + 1);
-        first_unit = list.unit_of(lo);
+        lo = hi = first_unit = 0;
+        if (total > 0) {
+            const Pieces pieces(total, min(N, total));  // no piece is empty: the CTAs behind have none
+            if (tid == 0) sh.total = total;
+            if (rank < pieces.n) {
+                lo = pieces.start(rank);
+                hi = pieces.start(rank + 1);
+                first_unit = list.unit_of(lo);
+            }
+        }
     }
 
     const int gid = lane >> 2, tig = lane & 3;
@@ -245,7 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const int ra = gid ^ ((gid >> 1) & 1);   // the tokens of this lane's K rows: ra and ra + 8
     const int t0 = (2 * tig) ^ (tig & 1), t1 = t0 ^ 1;  // ... and of its V pairs: (t0, t1) and (t0 + 8, t1 + 8)
     const float lo_lane = tig < 2 ? 0.f : -1.f;  // G <= 4: the lanes whose columns carry the lo parts
-    // the queries of the first unit are on their way while the pages are looked up
     uint4 qv[D / 32];
     auto load_queries = [&](int u) {
         const kvmm_bf16* qh = p.q + ((static_cast<size_t>(p.b0) * p.Hkv + u) * G + head) * D + tig * (D / 4);
@@ -253,7 +252,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         for (int i = 0; i < D / 32; ++i)
             qv[i] = head < G ? reinterpret_cast<const uint4*>(qh)[i] : make_uint4(0u, 0u, 0u, 0u);
     };
-    load_queries(first_unit);
 
     // ---- this warp's steps: round r is pages lo + r * kStride + kPages * warp .. + kPages - 1 --------------------
     constexpr int kStride = kWarps * kPages;
@@ -314,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const uint32_t copy_at = smem_addr(ring) + my_tile * Page::kBytes;
     auto issue = [&](unsigned r) {  // start the copies of round r
         const unsigned k = r % kBatch;
-        if (k == 0) look_up(static_cast<int>(r));
+        if (k == 0 && r != 0) look_up(static_cast<int>(r));
         if (k == my_round) {
             const uint32_t slot = r % kDepth;
             const int nv = pmeta & 63;
@@ -328,8 +326,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             if (nv > 0) bulk_copy_g2s_hint_at(copy_at + slot * kSlot, src, Page::kBytes, bar_at + slot * 8, policy);
         }
     };
+    if (!early && lo < hi) load_queries(first_unit);  // on their way while the pages are looked up
+    look_up(0);
+    if (early) pdl_wait_then_release();
+    if (p.sel_idx == nullptr) {
+        // sequences without a token: their results are written here, spread over the CTAs
+        for (int b = rank; b < p.nb; b += N) {
+            if (count[b] != 0) continue;
+            float* o = p.out + static_cast<size_t>(p.b0 + b) * p.Hq * D;
+            for (int e = tid; e < p.Hq * D; e += kThreads) o[e] = 0.f;
+            if (p.lse)
+                for (int e = tid; e < p.Hq; e += kThreads) p.lse[static_cast<size_t>(p.b0 + b) * p.Hq + e] = -INFINITY;
+        }
+    }
+    if (lo >= hi) return;
+    if (early) load_queries(first_unit);
 #pragma unroll
-    for (int r = 0; r < kDepth; ++r)
+    for (unsigned r = 0; r < kDepth; ++r)
         if (r < rounds) issue(r);
 
     // this lane's places in a page: its K row and scales, its V pairs' rows and scales

@@ -424,6 +424,28 @@ def test_early_reads_give_the_same_bits():
         assert torch.equal(c.out, want)
 
 
+def test_early_reads_behind_an_append():
+    """The append writes the pool, not the lengths or the table: the attention behind it may read those early."""
+    D, T, Hkv, B = 128, 16, 2, 3
+    c = Cache([900, 333, 17], D=D, T=T, Hq=8, Hkv=Hkv, L=1, layer=0, Pmax=60)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rows = torch.randn(20, 2, B, 1, Hkv, D, generator=g, device="cuda").to(torch.bfloat16)
+    begin = c.seq_len - 1
+    outs = []
+    for early in (False, True):
+        got = []
+        for i in range(20):
+            kvmm.kv4_append_rope(c.shape, 0, None, rows[i, 0], rows[i, 1], begin, c.seq_len, c.pool, c.table, None,
+                                 err=c.err)
+            c.attend(early_reads=early)
+            got.append(c.out.clone())
+        outs.append(torch.stack(got))
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    assert torch.equal(outs[0], outs[1])
+    c.check()
+
+
 # ---- the operators together -----------------------------------------------------------------------------------
 def rope_table(rows, dim):
     ang = torch.arange(rows, dtype=torch.float64)[:, None] * 10000.0 ** (
