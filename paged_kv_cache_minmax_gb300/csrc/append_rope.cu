@@ -230,13 +230,13 @@ constexpr int kQueryPasses = 4;  // rows of one token a lane turns: its loads in
 // Loads come before the stores that follow them in each batch: the compiler may not move a load over a store that
 // could alias it, so the order written is the number of bytes in flight.
 template <int D, int T, bool KV4>
-__global__ void __launch_bounds__(kAppWarps * 32, 2) append_rope_kernel(const AppendParams p, int page_slots,
+__global__ void __launch_bounds__(kAppWarps * 32, 3) append_rope_kernel(const AppendParams p, int page_slots,
                                                                         unsigned kv_ctas, int head_blocks)
 {
     using Page = Kv4Page<D, T>;
     constexpr int kLanes = D / 16;      // lanes of a row
     constexpr int kRows = 32 / kLanes;  // rows a warp moves at once
-    constexpr int kBatch = 2;           // passes loaded together
+    constexpr int kBatch = 1;           // passes loaded together (2 took 143 us for a 32K prompt: 16 warps an SM instead of 24)
     static_assert(T % (kRows * kBatch) == 0, "whole batches");
     pdl_wait_then_release();  // the pools, table and metadata may be in use by the previous kernel
     const int lane = threadIdx.x & 31;
@@ -247,12 +247,12 @@ __global__ void __launch_bounds__(kAppWarps * 32, 2) append_rope_kernel(const Ap
 
     if (blockIdx.x >= kv_ctas) {
         // ---- queries: one token's kQueryPasses * kRows heads a warp; its angles are loaded once ---------------------
-        const int64_t item = static_cast<int64_t>(blockIdx.x - kv_ctas) * kAppWarps + warp;
-        const int64_t token = item / head_blocks;
+        const unsigned item = (blockIdx.x - kv_ctas) * kAppWarps + warp;  // fewer than 2^31
+        const unsigned token = item / static_cast<unsigned>(head_blocks);
         const int h0 = static_cast<int>(item - token * head_blocks) * (kQueryPasses * kRows) + rsub;
-        const int b = static_cast<int>(token / p.n_new);
+        const int b = static_cast<int>(token / static_cast<unsigned>(p.n_new));
         if (b >= p.B) return;
-        const int j = static_cast<int>(token - static_cast<int64_t>(b) * p.n_new);
+        const int j = static_cast<int>(token - static_cast<unsigned>(b) * p.n_new);
         int tb, te;
         if (!token_range(p, b, tb, te, false) || j >= te - tb) return;
         const int pos = position(p, b, j, tb + j);
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, 2) append_rope_kernel(const Ap
             return;
         }
         const kvmm_bf16* src = p.q.data + b * p.q.batch_stride + j * p.q.token_stride;
-        kvmm_bf16* dst = p.q_out + token * p.Hq * D;
+        kvmm_bf16* dst = p.q_out + static_cast<size_t>(token) * p.Hq * D;
         uint4 va[kQueryPasses], vb[kQueryPasses];
 #pragma unroll
         for (int k = 0; k < kQueryPasses; ++k) {
@@ -294,12 +294,12 @@ __global__ void __launch_bounds__(kAppWarps * 32, 2) append_rope_kernel(const Ap
     }
 
     // ---- keys and values: one page of one (batch, KV head) a warp, the heads of a page side by side -----------
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kAppWarps + warp;
-    const int64_t pages = item / p.Hkv;
+    const unsigned item = blockIdx.x * kAppWarps + warp;  // fewer than 2^31
+    const unsigned pages = item / static_cast<unsigned>(p.Hkv);
     const int h = static_cast<int>(item - pages * p.Hkv);
-    const int b = static_cast<int>(pages / page_slots);
+    const int b = static_cast<int>(pages / static_cast<unsigned>(page_slots));
     if (b >= p.B) return;
-    const int slot = static_cast<int>(pages - static_cast<int64_t>(b) * page_slots);
+    const int slot = static_cast<int>(pages - static_cast<unsigned>(b) * page_slots);
     int tb, te;
     if (!token_range(p, b, tb, te, slot == 0 && h == 0 && lane == 0)) return;
     const int page = tb / T + slot;
@@ -498,7 +498,7 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream)
     const int head_blocks = (p.Hq + kHeads - 1) / kHeads;
     const long long q_items = p.q.data ? static_cast<long long>(p.B) * p.n_new * head_blocks : 0;
     const long long ctas = kv_ctas + (q_items + kAppWarps - 1) / kAppWarps;
-    if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    if (ctas > 0x7fffffffll / kAppWarps) return cudaErrorInvalidConfiguration;  // (terabytes of rows)
     void (*kernel)(AppendParams, int, unsigned, int) =
         p.kv4_pool ? append_rope_kernel<D, T, true> : append_rope_kernel<D, T, false>;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kAppWarps * 32), 0, stream, p, slots,

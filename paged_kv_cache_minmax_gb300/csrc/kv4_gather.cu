@@ -34,12 +34,12 @@ __global__ void __launch_bounds__(kGatWarps * 32) kv4_gather_kernel(const Gather
     constexpr int kBatch = T / kRows < 8 ? T / kRows : 8;  // loads in flight a lane
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kGatWarps + (threadIdx.x >> 5);
-    const int64_t pages = item / p.Hkv;
+    const unsigned item = blockIdx.x * kGatWarps + (threadIdx.x >> 5);  // fewer than 2^31
+    const unsigned pages = item / static_cast<unsigned>(p.Hkv);
     const int h = static_cast<int>(item - pages * p.Hkv);
-    const int b = static_cast<int>(pages / page_slots);
+    const int b = static_cast<int>(pages / static_cast<unsigned>(page_slots));
     if (b >= p.B) return;
-    const int slot = static_cast<int>(pages - static_cast<int64_t>(b) * page_slots);
+    const int slot = static_cast<int>(pages - static_cast<unsigned>(b) * page_slots);
     const bool tell = slot == 0 && h == 0 && lane == 0;
     const int cap = p.Pmax * T;
     int tb = p.tok_begin ? p.tok_begin[b] : 0, te = p.tok_end[b];
@@ -97,7 +97,7 @@ cudaError_t launch(const GatherParams& p, cudaStream_t stream)
     const long long span = (static_cast<long long>(p.n_rows) + T - 1) / T + 1;  // pages one range can reach
     const int slots = static_cast<int>(span < p.Pmax ? span : p.Pmax);
     const long long ctas = (static_cast<long long>(p.B) * slots * p.Hkv + kGatWarps - 1) / kGatWarps;
-    if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    if (ctas > 0x7fffffffll / kGatWarps) return cudaErrorInvalidConfiguration;  // (terabytes of rows)
     return launch_pdl(kv4_gather_kernel<D, T>, dim3(static_cast<unsigned>(ctas)), dim3(kGatWarps * 32), 0, stream, p,
                       slots);
 }
