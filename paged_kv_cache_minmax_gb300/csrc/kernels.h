@@ -325,7 +325,7 @@ struct Kv4AttnParams {
     float* partial;    // workspace: two partial results for each CTA
     int32_t* err;
 };
-constexpr int kKv4MaxBatch = 1024;  // batch entries of one launch (their page counts are summed in shared memory)
+constexpr int kKv4MaxBatch = 512;  // batch entries of one launch (their page counts are summed in shared memory)
 constexpr int kKv4MaxCtas = 256;    // CTAs of one launch that deals the pages evenly
 constexpr int kKv4MaxCluster = 16;  // CTAs of one unit
 constexpr size_t kKv4CounterBytes = kKv4MaxCtas * sizeof(int32_t);

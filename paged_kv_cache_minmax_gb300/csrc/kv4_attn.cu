@@ -62,10 +62,9 @@ __host__ __device__ constexpr int step_bytes(int D) { return kStep * (D + D / 8)
 struct Shared {
     uint64_t full[kWarps][4];  // a step has landed
     int2 meta[kWarps][4];      // per tile of the step: unit * 64 + valid tokens
-    float m[kWarps][8];        // each warp's (in the final merge: each group's) reference and sum per head
-    float l[kWarps][8];
-    float f[kWarps][8];        // weight of each warp's partial
-    float ref[8], sum[8];      // the CTA's reference and sum per head
+    uint64_t done[2], clear[2];  // a unit's partials are all stored; ... are merged (the buffers of G <= 4)
+    float m[2][kWarps][8];     // each warp's (in the final merge: each group's) reference and sum per head
+    float l[2][kWarps][8];
     int scan[kWarps];
     int total;                 // pages of the list
     int last[2];
@@ -73,11 +72,16 @@ struct Shared {
     float rstat[kKv4MaxCluster][16];       // received: (reference, sum) per head of every CTA of the cluster
 };
 
-// dynamic shared memory: [rings][partials: kWarps x G x (D + 4) floats][first pages and page counts of the batch]
+// A warp's partial: a row of D + 8 floats a head, the D/8 channels of a row group one float apart from the next group's
+// (the lanes of a store then fall on different banks).  G <= 4: two buffers, so that a warp goes on to the next unit
+// without waiting for the slowest.
+__host__ __device__ constexpr int part_row(int D) { return D + 8; }
+__host__ __device__ constexpr int part_buffers(int G) { return G <= 4 ? 2 : 1; }
+// dynamic shared memory: [rings][partials][first pages and page counts of the batch]
 __host__ __device__ constexpr size_t part_offset(int D) { return size_t(kWarps) * ring_depth(D) * step_bytes(D); }
 __host__ __device__ inline size_t list_offset(int D, int G)
 {
-    return part_offset(D) + size_t(kWarps) * G * (D + 4) * sizeof(float);
+    return part_offset(D) + size_t(part_buffers(G)) * kWarps * G * part_row(D) * sizeof(float);
 }
 inline size_t smem_bytes(int D, int G, int nb) { return list_offset(D, G) + size_t(2 * nb + 1) * sizeof(int); }
 
@@ -161,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     constexpr int kTiles = D / 16;   // m-tiles of O^T
     constexpr int kMine = D / 8;     // output channels of a lane's row group
     constexpr int kVWords = D / 64;  // code words of a lane's V token
+    constexpr int kPartRow = part_row(D);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -172,6 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
 
     if (tid < kWarps * kDepth) {
         mbar_init(&sh.full[tid / kDepth][tid % kDepth], kPages);
+        if (tid < 2) {
+            mbar_init(&sh.done[tid], kWarps);
+            mbar_init(&sh.clear[tid], kWarps);
+        }
         fence_barrier_init();
     }
     __syncwarp();  // converged for the aligned barrier
@@ -352,6 +361,61 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const uint32_t vs0_off = t0 * Page::kGroups + gid * kMine / 16, vs1_off = t1 * Page::kGroups + gid * kMine / 16;
     unsigned r = 0;
     int seg_unit[2] = {-1, -1};  // units whose parts this CTA stores: the one that began before, the one that goes on
+
+    // one output channel of one head over the warps' partials: unnormalised, with the reference and the sum
+    auto combine = [&](int e, int buf, float& M, float& L) {
+        const int g = e / D, d = e % D;
+        const float* x = part + (static_cast<size_t>(buf) * kWarps * G + g) * kPartRow + (d / kMine) * (kMine + 1) + d % kMine;
+        float m[kWarps];
+        M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            m[w] = sh.m[buf][w][g];
+            M = fmaxf(M, m[w]);
+        }
+        L = 0.f;
+        if (M == -INFINITY) return 0.f;
+        float O = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = fast_exp2(m[w] - M);
+            const float y = x[w * G * kPartRow];
+            L = fmaf(sh.l[buf][w][g], f, L);
+            O = fmaf(m[w] == -INFINITY ? 0.f : y, f, O);  // (a warp without a page of the unit left nothing)
+        }
+        return O;
+    };
+    // a unit's results, or this CTA's part of them
+    auto finish = [&](int u, int buf) {
+        int ubeg, uend;
+        list.range(u, ubeg, uend);
+        const bool whole = p.C > 0 || (ubeg >= lo && uend <= hi);
+        const int side = ubeg < lo ? 0 : 1;
+        if (!whole) seg_unit[side] = u;
+        float* slotp = p.partial + (static_cast<size_t>(rank) * 2 + side) * kv4_partial_floats(D);
+        for (int e = tid; e < G * D; e += kThreads) {
+            const int g = e / D;
+            float M, L;
+            const float O = combine(e, buf, M, L);
+            const size_t row = (static_cast<size_t>(p.b0) * p.Hkv + u) * G;
+            if (whole) {
+                p.out[row * D + e] = L > 0.f ? O * (p.v_scale / L) : 0.f;
+                if (e == g * D && p.lse) p.lse[row + g] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            } else {
+                slotp[e] = O;
+                if (e == g * D) {
+                    slotp[8 * D + g] = M;
+                    slotp[8 * D + 8 + g] = L;
+                }
+            }
+        }
+    };
+    // the k-th time (from 0) that every warp has arrived
+    auto wait_warps = [&](uint64_t* bar, int k) {
+        if (!mbar_wait_bounded(bar, k & 1, 4 * kWaitNs) && lane == 0) report(p.err, KVMM_ERR_TIMEOUT);
+        __syncwarp();
+    };
+    int seg = 0, before = 0;  // units this CTA has finished with; the last one, whose partials wait to be merged
 
     for (int u = first_unit;; ++u) {
         int ubeg, uend;
@@ -603,18 +667,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             l0 += __shfl_xor_sync(kFullMask, l0, off);
             l1 += __shfl_xor_sync(kFullMask, l1, off);
         }
+        const int buf = DUP ? seg & 1 : 0;
+        if (DUP && seg >= 2) wait_warps(&sh.clear[buf], (seg >> 1) - 1);
         if (gid == 0 && (!DUP || tig < 2)) {
-            sh.m[warp][col0] = m0;
-            sh.m[warp][col0 + 1] = m1;
-            sh.l[warp][col0] = l0;
-            sh.l[warp][col0 + 1] = l1;
+            sh.m[buf][warp][col0] = m0;
+            sh.m[buf][warp][col0 + 1] = m1;
+            sh.l[buf][warp][col0] = l0;
+            sh.l[buf][warp][col0 + 1] = l1;
         }
-        float* mine = part + static_cast<size_t>(warp) * G * (D + 4);
         if (m0 != -INFINITY) {  // this warp had a page of the unit
+            float* mine = part + static_cast<size_t>(buf * kWarps + warp) * G * kPartRow + gid * (kMine + 1);
 #pragma unroll
             for (int i = 0; i < (DUP ? kTiles / 2 : kTiles); ++i) {
                 float v[4];
-                int d = gid * kMine + i;
+                int d = i;
                 if (DUP) {  // hi + lo: the lanes with the hi columns take the first half of the tiles, the others the rest
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -628,54 +694,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                     for (int k = 0; k < 4; ++k) v[k] = o[i][k];
                 }
                 if (col0 < G) {
-                    mine[col0 * (D + 4) + d] = v[0];
-                    mine[col0 * (D + 4) + d + kTiles] = v[2];
+                    mine[col0 * kPartRow + d] = v[0];
+                    mine[col0 * kPartRow + d + kTiles] = v[2];
                 }
                 if (col0 + 1 < G) {
-                    mine[(col0 + 1) * (D + 4) + d] = v[1];
-                    mine[(col0 + 1) * (D + 4) + d + kTiles] = v[3];
+                    mine[(col0 + 1) * kPartRow + d] = v[1];
+                    mine[(col0 + 1) * kPartRow + d + kTiles] = v[3];
                 }
             }
         }
-        __syncthreads();
-        if (warp < G) {  // one warp a head, a lane a warp's partial
-            const float mw = lane < kWarps ? sh.m[lane][warp] : -INFINITY;
-            float M = mw;
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
-            M = __shfl_sync(kFullMask, M, 0);
-            const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-            float L = lane < kWarps && mw != -INFINITY ? sh.l[lane][warp] * f : 0.f;
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) L += __shfl_xor_sync(kFullMask, L, off);
-            if (lane < kWarps) sh.f[lane][warp] = f;
-            if (lane == 0) {
-                sh.ref[warp] = M;
-                sh.sum[warp] = L;
-            }
-        }
-        __syncthreads();
         if (p.C > 1) {
             // the unit's CTAs are a cluster: each stores, into every other, its references and sums and the slice of
             // its outputs that the other owns; after one cluster barrier every CTA combines its slice
             const int C = p.C, rc = static_cast<int>(cluster_ctarank());
             const int slice = (G * D + C - 1) / C;
+            __syncthreads();
             cluster_wait();
-            for (int e = tid; e < C * G; e += kThreads) {
-                const int c = e / G, g = e - c * G;
-                st_dsmem_f32(&sh.rstat[rc][g], c, sh.ref[g]);
-                st_dsmem_f32(&sh.rstat[rc][8 + g], c, sh.sum[g]);
-            }
             for (int e = tid; e < G * D; e += kThreads) {
-                const int g = e / D, d = e - g * D, c = e / slice;
-                float O = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = sh.f[w][g];
-                    const float x = part[(static_cast<size_t>(w) * G + g) * (D + 4) + d];
-                    O = fmaf(f != 0.f ? x : 0.f, f, O);
-                }
+                const int c = e / slice;
+                float M, L;
+                const float O = combine(e, buf, M, L);
                 st_dsmem_f32(&sh.recv[rc * slice + (e - c * slice)], c, O);
+                if (e % D == 0)
+                    for (int k = 0; k < C; ++k) {
+                        st_dsmem_f32(&sh.rstat[rc][e / D], k, M);
+                        st_dsmem_f32(&sh.rstat[rc][8 + e / D], k, L);
+                    }
             }
             __syncwarp();
             cluster_sync();
@@ -696,39 +740,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             }
             return;
         }
-        const bool whole = ubeg >= lo && uend <= hi;
-        const int side = ubeg < lo ? 0 : 1;
-        if (!whole) seg_unit[side] = u;
-        float* slotp = p.partial + (static_cast<size_t>(rank) * 2 + side) * kv4_partial_floats(D);
-        for (int e = tid; e < G * D; e += kThreads) {
-            const int g = e / D, d = e - g * D;
-            const float M = sh.ref[g], L = sh.sum[g];
-            float O = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = sh.f[w][g];
-                const float x = part[(static_cast<size_t>(w) * G + g) * (D + 4) + d];
-                O = fmaf(f != 0.f ? x : 0.f, f, O);  // (a warp without a page of the unit left nothing)
+        if (DUP) {  // the unit before this one has been left by every warp by now, or soon
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.done[buf]);
+            if (seg >= 1) {
+                wait_warps(&sh.done[buf ^ 1], (seg - 1) >> 1);
+                finish(before, buf ^ 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.clear[buf ^ 1]);
             }
-            const size_t row = (static_cast<size_t>(p.b0) * p.Hkv + u) * G + g;
-            if (whole) {
-                p.out[row * D + d] = L > 0.f ? O * (p.v_scale / L) : 0.f;
-                if (d == 0 && p.lse) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-            } else {
-                slotp[e] = O;
-                if (d == 0) {
-                    slotp[8 * D + g] = M;
-                    slotp[8 * D + 8 + g] = L;
-                }
-            }
+            before = u;
+        } else {
+            __syncthreads();
+            finish(u, 0);
+            __syncthreads();  // the partials are free again
         }
-        __syncthreads();  // the partials are free again (and stored, where another CTA has the rest of the unit)
+        ++seg;
         if (uend >= hi) break;
     }
+    if (DUP) {
+        wait_warps(&sh.done[(seg - 1) & 1], (seg - 1) >> 1);
+        finish(before, (seg - 1) & 1);
+    }
+    if (p.C > 0) return;
+    __syncthreads();  // this CTA's parts are stored
 
     // ---- units that fell on several CTAs: whoever stored the last part combines them ---------------------------
     // A unit's counter is that of the first CTA it lies in, which can be the first for one such unit only.
-    if (p.C > 0) return;
     const Pieces pieces(sh.total, min(N, sh.total));
     if (tid < 2) {
         sh.last[tid] = 0;
@@ -798,8 +836,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             }
             reinterpret_cast<float4*>(part)[tid] = a;
             if (4 * e == g * D) {
-                sh.m[grp][g] = M;
-                sh.l[grp][g] = L;
+                sh.m[0][grp][g] = M;
+                sh.l[0][grp][g] = L;
             }
         }
         __syncthreads();
@@ -807,11 +845,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         for (int i = tid; i < G * D; i += kThreads) {
             const int h = i / D;
             float M = -INFINITY, L = 0.f, O = 0.f;
-            for (int k = 0; k < ngrp; ++k) M = fmaxf(M, sh.m[k][h]);
+            for (int k = 0; k < ngrp; ++k) M = fmaxf(M, sh.m[0][k][h]);
             if (M != -INFINITY)
                 for (int k = 0; k < ngrp; ++k) {
-                    const float f = exp2f(sh.m[k][h] - M);
-                    L = fmaf(sh.l[k][h], f, L);
+                    const float f = exp2f(sh.m[0][k][h] - M);
+                    L = fmaf(sh.l[0][k][h], f, L);
                     O = fmaf(part[k * G * D + i], f, O);
                 }
             p.out[row0 * D + i] = L > 0.f ? O * (p.v_scale / L) : 0.f;
