@@ -41,6 +41,23 @@
 //   - Tokens are visited in the order r ^ ((r >> 1) & 1) within eight, which
 //     lets the K rows of a load fall on different banks and leaves V two ways.
 // Launched with programmatic dependent launch.
+//
+// Bound and measured (one GB300, us a launch in a graph of launches over three
+// inputs; the bytes are what the tokens hold, against the 6.78 TB/s of a copy).
+//   every page, one 128K sequence, 8 KV heads (151 MB)          34.3  0.65
+//   every page, 32 ragged sequences up to 16K tokens (449 MB)   88.4  0.75
+//   128 selected pages a head, 32K context, batch 8 (19 MB)     10.1  0.28
+//   64 pages of 32 tokens, five heads a KV head, batch 16 (36 MB) 13.4  0.39
+// Inside the long calls a tile takes 99 clocks an SM at 128K, the rate of the
+// memory; 237 of its 312 instructions are the tile's own (68 conversions, 64
+// products with scales, 16 MMAs).  What is left is latency: lengths, table and
+// first pages (3 us), the merge of warps, then of CTAs (4 us), the next launch
+// (2 us).  Short calls are that and the tiles' 95 clocks, on the 128 SMs that
+// whole clusters fill.
+// Measured and not kept: a second launch for the merge (6 us of 20 at 32K), a
+// producer warp for all rings (the copies of one warp's lanes go out one after
+// another, 70 clocks each: 111 us against 97 for the ragged batch then), 8 or 12
+// warps with longer rings (124 and 112 against 106 then).
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -276,9 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const uint8_t* src = p.kv4_pool;
     int pmeta = 0;
     auto look_up = [&](int rb) {
-        const int f = my_first + (rb + lane / kPages) * kStride + lane % kPages;
+        // (unsigned: a place behind the last may pass 2^31)
+        const unsigned at = static_cast<unsigned>(my_first) + static_cast<unsigned>(rb + lane / kPages) * kStride + lane % kPages;
         pmeta = 0x7fffffc0;  // behind the piece: after every unit
-        if (f >= hi || f < my_first) return;
+        if (at >= static_cast<unsigned>(hi)) return;
+        const int f = static_cast<int>(at);
         int b, h, lp, n, u;
         size_t unit;
         if (p.sel_idx != nullptr) {

@@ -4,7 +4,10 @@
 // fp16, so one fp32 multiplication and one rounding to bf16 follow it.
 // One warp takes one page of one (batch, KV head): a lane turns eight codes (4
 // bytes) and their scale into 16 bytes of a row, so both sides of the copy are
-// coalesced.  Bound by the bytes written (2 of them for 0.56 read).
+// coalesced.  Bound by the bytes written (2 of them for 0.56 read): 72K tokens
+// of 8 heads (265 MB) take 45.8 us, 0.85 of a copy's rate; more or fewer loads
+// in flight, both sides' loads first, 4 or 16 warps a CTA and streaming stores
+// were all within 1% of it.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
