@@ -47,6 +47,14 @@ __device__ __forceinline__ uint32_t from_key2(uint32_t k)
     return k ^ ((neg * 0xffffu) | 0x80008000u);
 }
 
+// tokens of [tb, te) this call appends, 0 for a range that is refused
+__device__ __forceinline__ int token_count(const AppendParams& p, int tb, int te)
+{
+    const int cap = p.Pmax * p.T;
+    if (tb < 0 || te < tb || tb > cap) return 0;
+    return min(min(te, cap) - tb, p.n_new);
+}
+
 // the tokens of batch b this call appends: [tb, te), clamped as kv_minmax_update clamps
 __device__ __forceinline__ bool token_range(const AppendParams& p, int b, int& tb, int& te, bool tell)
 {
@@ -232,18 +240,29 @@ __device__ __forceinline__ void rotate(const AppendParams& p, const Angles& g, f
     }
 }
 
+// ... of bf16 rows
+__device__ __forceinline__ void turn_row(const AppendParams& p, const Angles& g, uint4& va, uint4& vb)
+{
+    float a[8], c[8];
+    unpack8(va, a);
+    unpack8(vb, c);
+    rotate(p, g, a, c);
+    va = pack8(a);
+    vb = pack8(c);
+}
+
 constexpr int kQueryPasses = 4;  // rows of one token a lane turns: its loads in flight together
 
 // Loads come before the stores that follow them in each batch: the compiler may not move a load over a store that
 // could alias it, so the order written is the number of bytes in flight.
 template <int D, int T, bool KV4>
-__global__ void __launch_bounds__(kAppWarps * 32, 3) append_rope_kernel(const AppendParams p, int page_slots,
+__global__ void __launch_bounds__(kAppWarps * 32, T == 16 ? 3 : 2) append_rope_kernel(const AppendParams p, int page_slots,
                                                                         unsigned kv_ctas, int head_blocks)
 {
     using Page = Kv4Page<D, T>;
     constexpr int kLanes = D / 16;      // lanes of a row
     constexpr int kRows = 32 / kLanes;  // rows a warp moves at once
-    constexpr int kBatch = 1;           // passes loaded together (2 took 143 us for a 32K prompt: 16 warps an SM instead of 24)
+    constexpr int kBatch = T == 16 ? 1 : 2;  // passes loaded together
     static_assert(T % (kRows * kBatch) == 0, "whole batches");
     pdl_wait_then_release();  // the pools, table and metadata may be in use by the previous kernel
     const int lane = threadIdx.x & 31;
@@ -253,50 +272,80 @@ __global__ void __launch_bounds__(kAppWarps * 32, 3) append_rope_kernel(const Ap
     const Pieces pc = pieces<D>(p, sub);
 
     if (blockIdx.x >= kv_ctas) {
-        // ---- queries: one token's kQueryPasses * kRows heads a warp; its angles are loaded once ---------------------
+        // ---- queries: kQueryPasses * kRows rows a warp, their loads in flight together ------------------------------
         const unsigned item = (blockIdx.x - kv_ctas) * kAppWarps + warp;  // fewer than 2^31
-        const unsigned token = item / static_cast<unsigned>(head_blocks);
-        const int h0 = static_cast<int>(item - token * head_blocks) * (kQueryPasses * kRows) + rsub;
-        const int b = static_cast<int>(token / static_cast<unsigned>(p.n_new));
-        if (b >= p.B) return;
-        const int j = static_cast<int>(token - static_cast<unsigned>(b) * p.n_new);
-        int tb, te;
-        if (!token_range(p, b, tb, te, false) || j >= te - tb) return;
-        const int pos = position(p, b, j, tb + j);
-        if (pos < 0) {
-            if (lane == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
-            return;
-        }
-        const kvmm_bf16* src = p.q.data + b * p.q.batch_stride + j * p.q.token_stride;
-        kvmm_bf16* dst = p.q_out + static_cast<size_t>(token) * p.Hq * D;
         uint4 va[kQueryPasses], vb[kQueryPasses];
+        if (head_blocks > 0) {  // whole blocks of one token's heads: its range, position and angles are taken once
+            const unsigned token = item / static_cast<unsigned>(head_blocks);
+            const int h0 = static_cast<int>(item - token * head_blocks) * (kQueryPasses * kRows) + rsub;
+            const int b = static_cast<int>(token / static_cast<unsigned>(p.n_new));
+            if (b >= p.B) return;
+            const int j = static_cast<int>(token - static_cast<unsigned>(b) * p.n_new);
+            int tb, te;
+            if (!token_range(p, b, tb, te, false) || j >= te - tb) return;
+            const int pos = position(p, b, j, tb + j);
+            if (pos < 0) {
+                if (lane == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
+                return;
+            }
+            const kvmm_bf16* src = p.q.data + b * p.q.batch_stride + j * p.q.token_stride;
+            uint4* dst = reinterpret_cast<uint4*>(p.q_out + (static_cast<size_t>(token) * p.Hq + h0) * D);
 #pragma unroll
-        for (int k = 0; k < kQueryPasses; ++k) {
-            const int h = h0 + k * kRows;
-            if (h < p.Hq) {
-                const uint4* row = reinterpret_cast<const uint4*>(src + h * p.q.head_stride);
+            for (int k = 0; k < kQueryPasses; ++k) {
+                const uint4* row = reinterpret_cast<const uint4*>(src + (h0 + k * kRows) * p.q.head_stride);
                 va[k] = row[pc.a];
                 vb[k] = row[pc.b];
             }
+            Angles g{};
+            if (pc.turns) g = angles(p, pos, pc);
+#pragma unroll
+            for (int k = 0; k < kQueryPasses; ++k) {
+                if (pc.turns) turn_row(p, g, va[k], vb[k]);
+                dst[k * kRows * (D / 8) + pc.a] = va[k];
+                dst[k * kRows * (D / 8) + pc.b] = vb[k];
+            }
+            return;
         }
-        Angles g{};
-        if (pc.turns) g = angles(p, pos, pc);
+        // other head counts: consecutive (batch, token, head) rows, each with its own range, position and angles
+        const unsigned rows = static_cast<unsigned>(p.B) * p.n_new * p.Hq;  // fewer than 2^32
+        const unsigned row0 = item * (kQueryPasses * kRows) + rsub;
+        int b[kQueryPasses], j[kQueryPasses], h[kQueryPasses], tb[kQueryPasses], te[kQueryPasses];
 #pragma unroll
         for (int k = 0; k < kQueryPasses; ++k) {
-            const int h = h0 + k * kRows;
-            if (h >= p.Hq) break;
-            if (pc.turns) {
-                float a[8], c[8];
-                unpack8(va[k], a);
-                unpack8(vb[k], c);
-                rotate(p, g, a, c);
-                va[k] = pack8(a);
-                vb[k] = pack8(c);
-            }
-            uint4* row = reinterpret_cast<uint4*>(dst + static_cast<size_t>(h) * D);
-            row[pc.a] = va[k];
-            row[pc.b] = vb[k];
+            const unsigned row = min(row0 + k * kRows, rows - 1);
+            const unsigned token = row / static_cast<unsigned>(p.Hq);
+            h[k] = static_cast<int>(row - token * p.Hq);
+            b[k] = static_cast<int>(token / static_cast<unsigned>(p.n_new));
+            j[k] = static_cast<int>(token - static_cast<unsigned>(b[k]) * p.n_new);
+            tb[k] = p.tok_begin[b[k]];
+            te[k] = p.tok_end[b[k]];
         }
+        int at[kQueryPasses];  // its position, -1: no row
+#pragma unroll
+        for (int k = 0; k < kQueryPasses; ++k) {
+            const int n = token_count(p, tb[k], te[k]);
+            at[k] = -1;
+            if (row0 + k * kRows < rows && j[k] < n) {
+                at[k] = position(p, b[k], j[k], tb[k] + j[k]);
+                if (at[k] < 0 && sub == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kQueryPasses; ++k)
+            if (at[k] >= 0) {
+                const uint4* row = reinterpret_cast<const uint4*>(p.q.data + b[k] * p.q.batch_stride +
+                                                                  j[k] * p.q.token_stride + h[k] * p.q.head_stride);
+                va[k] = row[pc.a];
+                vb[k] = row[pc.b];
+            }
+#pragma unroll
+        for (int k = 0; k < kQueryPasses; ++k)
+            if (at[k] >= 0) {
+                if (pc.turns) turn_row(p, angles(p, at[k], pc), va[k], vb[k]);
+                uint4* dst = reinterpret_cast<uint4*>(p.q_out + static_cast<size_t>(row0 + k * kRows) * D);
+                dst[pc.a] = va[k];
+                dst[pc.b] = vb[k];
+            }
         return;
     }
 
@@ -480,6 +529,26 @@ __global__ void __launch_bounds__(kAppWarps * 32, 3) append_rope_kernel(const Ap
                     reinterpret_cast<uint4*>(c0)[1] = make_uint4(a[4], a[5], a[6], a[7]);
                     reinterpret_cast<uint4*>(c1)[0] = make_uint4(c[0], c[1], c[2], c[3]);
                     reinterpret_cast<uint4*>(c1)[1] = make_uint4(c[4], c[5], c[6], c[7]);
+                } else if (__popc(have) > 2) {
+                    // some of the 16 tokens: put among those that are there and stored back whole (2-byte stores of 31
+                    // of a page's 32 tokens took ten times as long as the whole page)
+                    uint32_t a[8], c[8];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 x = reinterpret_cast<const uint4*>(c0)[i], y = reinterpret_cast<const uint4*>(c1)[i];
+                        a[4 * i] = x.x, a[4 * i + 1] = x.y, a[4 * i + 2] = x.z, a[4 * i + 3] = x.w;
+                        c[4 * i] = y.x, c[4 * i + 1] = y.y, c[4 * i + 2] = y.z, c[4 * i + 3] = y.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (have >> i & 1u) {  // (i even: the low half of the word)
+                            a[i / 2] = i % 2 ? prmt(a[i / 2], w[i], 0x5410) : prmt(a[i / 2], w[i], 0x3254);
+                            c[i / 2] = i % 2 ? prmt(c[i / 2], w[i], 0x7610) : prmt(c[i / 2], w[i], 0x3276);
+                        }
+                    reinterpret_cast<uint4*>(c0)[0] = make_uint4(a[0], a[1], a[2], a[3]);
+                    reinterpret_cast<uint4*>(c0)[1] = make_uint4(a[4], a[5], a[6], a[7]);
+                    reinterpret_cast<uint4*>(c1)[0] = make_uint4(c[0], c[1], c[2], c[3]);
+                    reinterpret_cast<uint4*>(c1)[1] = make_uint4(c[4], c[5], c[6], c[7]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -501,9 +570,12 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream)
     const int slots = static_cast<int>(span < p.Pmax ? span : p.Pmax);
     const long long items = static_cast<long long>(p.B) * slots * p.Hkv;
     const long long kv_ctas = (items + kAppWarps - 1) / kAppWarps;
-    constexpr int kHeads = kQueryPasses * 32 / (D / 16);  // heads a warp turns
-    const int head_blocks = (p.Hq + kHeads - 1) / kHeads;
-    const long long q_items = p.q.data ? static_cast<long long>(p.B) * p.n_new * head_blocks : 0;
+    // queries: a warp takes kQueryPasses * 32 / (D/16) rows, whole blocks of a token's heads where these divide them
+    constexpr int kHeads = kQueryPasses * 32 / (D / 16);
+    const int head_blocks = p.Hq % kHeads == 0 ? p.Hq / kHeads : 0;
+    const long long rows = p.q.data ? static_cast<long long>(p.B) * p.n_new * p.Hq : 0;
+    const long long q_items = (rows + kHeads - 1) / kHeads;
+    if (rows > 0xffffffffll - kHeads) return cudaErrorInvalidConfiguration;  // (terabytes of rows)
     const long long ctas = kv_ctas + (q_items + kAppWarps - 1) / kAppWarps;
     if (ctas > 0x7fffffffll / kAppWarps) return cudaErrorInvalidConfiguration;  // (terabytes of rows)
     void (*kernel)(AppendParams, int, unsigned, int) =

@@ -71,6 +71,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
+constexpr int kShortTiles = 256;               // tiles of 16 tokens a CTA may have for a cluster a unit over every page
 constexpr int kStep = 32;                      // tokens of a step: two pages of 16, or one of 32
 constexpr uint64_t kWaitNs = 1000000000ull;    // far beyond any legitimate wait
 __host__ __device__ constexpr int ring_depth(int D) { return D == 64 ? 4 : 2; }  // steps in flight a warp
@@ -210,12 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     if (!early) pdl_wait_then_release();
 
     // ---- the page list and this CTA's piece of it ------------------------------------------------------------
-    int total;
-    if (p.sel_idx != nullptr) {
-        total = p.nb * p.Hkv * p.Kmax;
+    int total = 0;
+    if (p.C > 0 || p.sel_idx != nullptr) {
+        if (p.C == 0) total = p.nb * p.Hkv * p.Kmax;
         __syncthreads();  // the barriers exist
     } else {
-        total = 0;
         for (int base = 0; base < p.nb; base += kThreads) {
             const int i = base + tid;
             int n = 0, inc;
@@ -244,14 +244,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         if (tid == 0) first[p.nb] = total;
         __syncthreads();
     }
-    const List list{first, count, p.sel_idx != nullptr ? p.Kmax : 0, p.Hkv, p.nb};
-    // (integer divisions are a large part of what comes before the first copy: a cluster's CTA makes two)
+    // places a unit has in the list: Kmax, or, with a cluster a unit, Pmax; 0: its pages, summed above
+    const List list{first, count, p.sel_idx != nullptr ? p.Kmax : p.C > 0 ? p.Pmax : 0, p.Hkv, p.nb};
+    // (integer divisions are a large part of what comes before the first copy: a cluster's CTA makes few)
     int lo, hi, first_unit;
-    if (p.C > 0) {  // a unit's places dealt to its C CTAs
+    if (p.C > 0) {  // a unit's places (every page: those its sequence fills) dealt to its C CTAs
         const int c = p.C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
         first_unit = p.C > 1 ? static_cast<int>(cluster_id()) : rank;
-        lo = first_unit * p.Kmax + p.Kmax * c / p.C;  // (Kmax <= 32768, C <= 16)
-        hi = first_unit * p.Kmax + p.Kmax * (c + 1) / p.C;  // > lo: C <= Kmax
+        int n = p.Kmax;
+        if (p.sel_idx == nullptr) n = (clamped_seq(p, p.b0 + first_unit / p.Hkv, c == 0 && first_unit % p.Hkv == 0) + T - 1) / T;
+        lo = first_unit * list.per + n * c / p.C;  // (n <= 32768, C <= 16)
+        hi = first_unit * list.per + n * (c + 1) / p.C;
     } else {
         lo = hi = first_unit = 0;
         if (total > 0) {
@@ -300,7 +303,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         const int f = static_cast<int>(at);
         int b, h, lp, n, u;
         size_t unit;
-        if (p.sel_idx != nullptr) {
+        if (p.C > 0 && p.sel_idx == nullptr) {
+            u = first_unit;
+            b = u / p.Hkv;
+            h = u - b * p.Hkv;
+            lp = f - u * p.Pmax;
+            unit = (static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + h;
+            pmeta = u * 64;
+        } else if (p.sel_idx != nullptr) {
             u = p.C > 0 ? first_unit : f / p.Kmax;
             const int i = f - u * p.Kmax;
             b = u / p.Hkv;
@@ -354,10 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             if (nv > 0) bulk_copy_g2s_hint_at(copy_at + slot * kSlot, src, Page::kBytes, bar_at + slot * 8, policy);
         }
     };
-    if (!early && lo < hi) load_queries(first_unit);  // on their way while the pages are looked up
+    if (!early && (p.C > 0 || lo < hi)) load_queries(first_unit);  // on their way while the pages are looked up
     look_up(0);
     if (early) pdl_wait_then_release();
-    if (p.sel_idx == nullptr) {
+    if (p.C == 0 && p.sel_idx == nullptr) {
         // sequences without a token: their results are written here, spread over the CTAs
         for (int b = rank; b < p.nb; b += N) {
             if (count[b] != 0) continue;
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                 for (int e = tid; e < p.Hq; e += kThreads) p.lse[static_cast<size_t>(p.b0 + b) * p.Hq + e] = -INFINITY;
         }
     }
-    if (lo >= hi) return;
+    if (p.C == 0 && lo >= hi) return;  // (a cluster's CTA without a page takes part in its merge)
     if (early) load_queries(first_unit);
 #pragma unroll
     for (unsigned r = 0; r < kDepth; ++r)
@@ -439,10 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     for (int u = first_unit;; ++u) {
         int ubeg, uend;
         list.range(u, ubeg, uend);
-        if (uend == ubeg) {  // an empty sequence
-            if (u + 1 >= p.nb * p.Hkv) break;
-            continue;
-        }
+        if (uend == ubeg) continue;  // an empty sequence (a page of another follows: hi is beyond)
         // queries: halves of the lane's channels of its head, scaled by a power of two
         uint32_t qf[2 * kTiles];
         float zf0, zf1;
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             }
         }
 
-        if (uend < hi) {  // the next unit's queries are on their way during the merge
+        if (p.C == 0 && uend < hi) {  // the next unit's queries are on their way during the merge
             int nu = u + 1, b0, b1;
             for (list.range(nu, b0, b1); b0 == b1; list.range(nu, b0, b1)) ++nu;  // (a unit with pages follows: hi is beyond)
             load_queries(nu);
@@ -775,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             __syncthreads();  // the partials are free again
         }
         ++seg;
-        if (uend >= hi) break;
+        if (p.C > 0 || uend >= hi) break;
     }
     if (DUP) {
         wait_warps(&sh.done[(seg - 1) & 1], (seg - 1) >> 1);
@@ -911,7 +918,7 @@ cudaError_t launch(Kv4AttnParams p, cudaStream_t stream)
     // per thread and device: what the launches need to know of it
     struct Device {
         int dev = -1, sms = 0;
-        size_t smem[2] = {0, 0};
+        bool ready[2] = {};  // by kernel
         int held[9][kKv4MaxCluster + 1] = {};  // clusters of c CTAs held at once, by group size; 0: not asked yet
     };
     static thread_local Device known;
@@ -921,6 +928,14 @@ cudaError_t launch(Kv4AttnParams p, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         known.dev = dev;
     }
+    if (!known.ready[dup]) {  // the most any launch of this kernel takes, so that clusters can be asked for first
+        const size_t most = smem_bytes(D, dup ? 4 : 8, kKv4MaxBatch);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        known.ready[dup] = true;
+    }
     // batch entries of one launch: their page counts are summed in shared memory, and the list's length is an int
     const long long each = static_cast<long long>(p.Hkv) * (p.sel_idx ? p.Kmax : p.Pmax);  // <= 2^31
     long long room = (1ll << 30) / each;
@@ -928,20 +943,17 @@ cudaError_t launch(Kv4AttnParams p, cudaStream_t stream)
     const int step = room < 1 ? 1 : room < kKv4MaxBatch ? static_cast<int>(room) : kKv4MaxBatch;
     for (p.b0 = 0; p.b0 < p.B; p.b0 += step) {
         p.nb = p.B - p.b0 < step ? p.B - p.b0 : step;
-        const size_t smem = smem_bytes(D, p.G, p.sel_idx ? 0 : p.nb);
-        if (known.smem[dup] < smem) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-            known.smem[dup] = smem;
-        }
         const long long units = static_cast<long long>(p.nb) * p.Hkv;
+        // A cluster a unit, as many CTAs as all run at once and have 16 pages each, where the units are no more than
+        // the SMs: with selections, or when a CTA's share of the longest sequence is short (kShortTiles).  What an
+        // uneven batch then loses to its longest sequence is less than what dealing its pages evenly costs: the sum of
+        // the lengths, the units that end inside a CTA and the merge through memory.  Six sequences of up to 1,914
+        // tokens, 8 KV heads: @@a us against @@b; at the border, @@c.
+        const int places = p.sel_idx ? p.Kmax : p.Pmax;
         p.C = 0;
-        if (p.sel_idx != nullptr && units <= known.sms) {
-            // selections of units that all run at once: a cluster a unit, as many CTAs as fit and have 16 pages each
+        if (units <= known.sms) {
             const size_t bare = smem_bytes(D, p.G, 0);
-            int most = (p.Kmax + kWarps - 1) / kWarps;
+            int most = (places + kWarps - 1) / kWarps;
             if (most > kKv4MaxCluster) most = kKv4MaxCluster;
             p.C = 1;
             for (int c = 2; c <= most && units * c <= known.sms; ++c) {
@@ -952,7 +964,9 @@ cudaError_t launch(Kv4AttnParams p, cudaStream_t stream)
                 }
                 if (held >= units) p.C = c;
             }
+            if (p.sel_idx == nullptr && (places + p.C - 1) / p.C * (T / 16) > kShortTiles) p.C = 0;
         }
+        const size_t smem = smem_bytes(D, p.G, p.C == 0 && !p.sel_idx ? p.nb : 0);
         long long n = units * p.C;
         if (p.C == 0) {  // one CTA an SM, fewer when not every warp would get a page
             n = (each * p.nb + kWarps - 1) / kWarps;
