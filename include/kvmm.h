@@ -670,11 +670,13 @@ kvmm_status kv4_gather(const kvmm_shape* shape, int32_t layer, const uint8_t* kv
  * (out = 0, lse = -inf), invalid selections and table entries.  sel_idx and
  * sel_cnt both NULL: every page of the sequence (Kmax is then not used).
  * What a page holds behind its sequence's last token is not looked at.
- * The pages of all units are dealt evenly to one CTA for each SM, whatever
- * the sequences' lengths (with selections: Kmax places a unit, so a Kmax far
- * above the counts leaves CTAs idle); the parts of a unit that falls on
- * several CTAs pass through the workspace (kvmm_kv4_workspace_size(shape)
- * bytes, 16-byte aligned), and the CTA that stores the last part merges them.
+ * With no more units (batch entries x KV heads) than SMs, and selections or a
+ * short table (Pmax), a cluster of CTAs shares a unit's Kmax places or its
+ * pages.  Else the pages of all units are dealt evenly to one CTA for each
+ * SM, whatever the sequences' lengths.  (A Kmax far above the counts leaves
+ * CTAs idle either way.)  The parts of a unit that falls on several CTAs
+ * then pass through the workspace (kvmm_kv4_workspace_size(shape) bytes,
+ * 16-byte aligned), and the CTA that stores the last part merges them.
  * The workspace must be zero when it is first used; every call leaves its
  * counters zero again and nothing else in it matters to the next.
  * flags: 0, or KVMM_EARLY_READS: the caller guarantees that no kernel still

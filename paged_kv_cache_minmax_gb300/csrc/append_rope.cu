@@ -15,16 +15,20 @@
 // both members of every pair are in one lane whichever way channels are
 // paired, and the 16 channels of a 4-bit scale are in two neighbouring lanes.
 // Rows of the page that were there before are read back (for the MinMax
-// alone).  Further warps rotate the query rows, sixteen heads of a token (D =
-// 64: 32) each, whose angles are loaded once.
+// alone); where more than two of a block of 16 value rows are new, the block's
+// other rows are read and it is stored whole.  Further warps rotate the query
+// rows, 16 (D = 64: 32) each with their loads in flight together: the heads of
+// one token where its heads are whole blocks, so that its range, position and
+// angles are looked up once, else rows of the whole list (32K prompt, 32 heads:
+// 133 us by blocks, 137 by rows; two 8K prompts, pages of 32: 71 and 77).
 //
 // Bound and measured (one GB300): prompts by the bytes they move, single tokens
 // by the chain of dependent loads (range, table entry, rows).  A 32K prompt, 32
 // query and 8 KV heads of 128 channels (830 MB): 133 us, 0.92 of a copy's rate;
 // the first version, with a store between every two rows' loads and angles for
-// every head, took 240.  One token a sequence, batch 32: 4.8 us on the device.
-// Two prompts' 8K tokens into 4 bits (282 MB): 63 us; the first version, with
-// a division a channel besides, took 142.
+// every head, took 240.  One token a sequence, batch 32: 5.2 us on the device.
+// Two prompts' 8K tokens into 4 bits (453 MB): 81 us, 0.82; the first version,
+// with a division a channel besides, took 151.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -255,14 +259,21 @@ constexpr int kQueryPasses = 4;  // rows of one token a lane turns: its loads in
 
 // Loads come before the stores that follow them in each batch: the compiler may not move a load over a store that
 // could alias it, so the order written is the number of bytes in flight.
+// Rows in flight: one pass a warp with 24 warps an SM, or two with 16.  The first is as fast or faster where the work
+// between load and store is long or a page is two passes (32K prompt, pages of 16: 133 us against 143; 336 tokens of 45
+// sequences into pages of 32 in 4 bits: 39 against 46); bf16 pages of 32 have four passes in a chain and little else
+// (short prompts: 8.4 us with two at once, 9.9 with one).
+template <int T, bool KV4>
+constexpr int kAppBatch = T == 16 || KV4 ? 1 : 2;
+
 template <int D, int T, bool KV4>
-__global__ void __launch_bounds__(kAppWarps * 32, T == 16 ? 3 : 2) append_rope_kernel(const AppendParams p, int page_slots,
-                                                                        unsigned kv_ctas, int head_blocks)
+__global__ void __launch_bounds__(kAppWarps * 32, kAppBatch<T, KV4> == 1 ? 3 : 2)
+    append_rope_kernel(const AppendParams p, int page_slots, unsigned kv_ctas, int head_blocks)
 {
     using Page = Kv4Page<D, T>;
     constexpr int kLanes = D / 16;      // lanes of a row
     constexpr int kRows = 32 / kLanes;  // rows a warp moves at once
-    constexpr int kBatch = T == 16 ? 1 : 2;  // passes loaded together
+    constexpr int kBatch = kAppBatch<T, KV4>;  // passes loaded together
     static_assert(T % (kRows * kBatch) == 0, "whole batches");
     pdl_wait_then_release();  // the pools, table and metadata may be in use by the previous kernel
     const int lane = threadIdx.x & 31;
@@ -570,7 +581,7 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream)
     const int slots = static_cast<int>(span < p.Pmax ? span : p.Pmax);
     const long long items = static_cast<long long>(p.B) * slots * p.Hkv;
     const long long kv_ctas = (items + kAppWarps - 1) / kAppWarps;
-    // queries: a warp takes kQueryPasses * 32 / (D/16) rows, whole blocks of a token's heads where these divide them
+    // queries: whole blocks of a token's heads where these divide them, else rows of the list
     constexpr int kHeads = kQueryPasses * 32 / (D / 16);
     const int head_blocks = p.Hq % kHeads == 0 ? p.Hq / kHeads : 0;
     const long long rows = p.q.data ? static_cast<long long>(p.B) * p.n_new * p.Hq : 0;

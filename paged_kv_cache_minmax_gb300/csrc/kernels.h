@@ -308,7 +308,7 @@ struct GatherParams {
 struct Kv4AttnParams {
     int32_t B, L, Hq, Hkv, G, D, T, Pmax, Kmax, layer;
     int32_t b0, nb;  // the batch entries of this launch: b0 .. b0 + nb - 1
-    int32_t C;       // CTAs a unit (a cluster each); 0: the pages of all units are dealt evenly to the CTAs
+    int32_t C;       // CTAs a unit (a cluster each, set by the launch); 0: the pages of all units are dealt evenly to the CTAs
     int32_t early;   // 1: seq_len and the table may be read before the preceding kernel has finished
     int64_t n_phys;
     float scale_log2;  // sm_scale * k_scale * log2(e)

@@ -6,9 +6,10 @@
 // in one pass with a running reference m (sm_scale, k_scale and log2(e) are one
 // factor on z; v_scale is applied to the result).
 //
-// Work.  With selections and no more units than SMs, each unit has a cluster of
-// CTAs (as many as all run at once), which share its Kmax places and merge their
-// parts through distributed shared memory.  Else the pages of all units form one
+// Work.  With no more units than SMs, and with selections or short sequences
+// (kShortTiles), each unit has a cluster of CTAs (as many as all run at once),
+// which share its places (selections: Kmax) or its sequence's pages and merge
+// their parts through distributed shared memory.  Else the pages of all units form one
 // list (with selections, Kmax places a unit) and CTA c of the N launched, one for
 // each SM, takes the c-th of N equal pieces of it, whatever the sequences'
 // lengths, so there is one wave without a tail.  Sixteen warps take a CTA's pages
@@ -71,7 +72,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kShortTiles = 256;               // tiles of 16 tokens a CTA may have for a cluster a unit over every page
+constexpr int kShortTiles = 256;               // over every page: most 16-token tiles a CTA of a unit's cluster has
 constexpr int kStep = 32;                      // tokens of a step: two pages of 16, or one of 32
 constexpr uint64_t kWaitNs = 1000000000ull;    // far beyond any legitimate wait
 __host__ __device__ constexpr int ring_depth(int D) { return D == 64 ? 4 : 2; }  // steps in flight a warp
@@ -948,7 +949,9 @@ cudaError_t launch(Kv4AttnParams p, cudaStream_t stream)
         // the SMs: with selections, or when a CTA's share of the longest sequence is short (kShortTiles).  What an
         // uneven batch then loses to its longest sequence is less than what dealing its pages evenly costs: the sum of
         // the lengths, the units that end inside a CTA and the merge through memory.  Six sequences of up to 1,914
-        // tokens, 8 KV heads: @@a us against @@b; at the border, @@c.
+        // tokens, 8 KV heads: 9.3 us against 17.2; at the border, two of 32K 25.0 against 27.4, one of 64K 25.1
+        // against 23.1.  Beyond it the SMs that whole clusters leave empty (24 of 152) cost more: two of 60,000 tokens
+        // 40.4 against 37.0, one of 128K 43.7 against 34.9.
         const int places = p.sel_idx ? p.Kmax : p.Pmax;
         p.C = 0;
         if (units <= known.sms) {

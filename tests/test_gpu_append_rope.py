@@ -103,6 +103,8 @@ CASES = {
     "token-first": dict(n=1, begin=(0, 95), end=(1, 96), D=128, Hq=2),
     "ragged": dict(B=5, n=20, begin=(0, 7, 16, 90, 3), end=(20, 7, 17, 96, 22), Hkv=3, Hq=3),
     "wide-range": dict(spread=6.0, n=24, begin=(4, 9), end=(28, 33)),
+    "blocks-d64-t32": dict(Hq=32, Hkv=4, T=32, n=35, begin=(30, 0), end=(65, 20), Pmax=4, rope="pairs"),
+    "rows-d128": dict(B=3, Hq=12, Hkv=3, D=128, T=32, n=5, begin=(30, 0, 96), end=(35, 0, 101), Pmax=4),
     "eight-heads": dict(Hq=64, Hkv=8, D=128, n=2, begin=(3, 31), end=(5, 33), L=1, layer=0),
 }
 

@@ -223,6 +223,33 @@ def test_one_long_sequence_falls_on_every_cta(G):
     c.check()
 
 
+@pytest.mark.parametrize("G,T", [(4, 16), (5, 32)])
+def test_long_sequences_are_dealt_evenly(G, T):
+    """Longer than a cluster a unit is taken for: pieces that hold parts of units, whole ones and empty ones."""
+    c = Cache([70003, 3, 0, 33000], Hq=2 * G, Hkv=2, D=64, T=T, L=1, layer=0, Pmax=-(-70003 // T) + 9)
+    c.spoil_behind()
+    for _ in range(2):  # the counters are back at zero
+        c.out.fill_(5.0)
+        c.attend(v_scale=0.5)
+        torch.cuda.synchronize()
+        assert int(c.err) == 0
+        c.check(v_scale=0.5)
+    assert int(c.ws[:1024].max()) == 0
+
+
+@pytest.mark.parametrize("G", [1, 4, 5, 8])
+@pytest.mark.parametrize("D,T", [(64, 16), (64, 32), (128, 16), (128, 32)])
+def test_ragged_sequences_share_clusters(D, T, G):
+    """A cluster of several CTAs a unit over every page: lengths that leave most of its CTAs, or all, without a page."""
+    c = Cache([2001, 0, 1, 777, 16 * T, 1234], Hq=2 * G, Hkv=2, D=D, T=T, L=1, layer=0)
+    c.spoil_behind()
+    c.table[0, 0, 1, 2:5] = -1
+    c.attend(early_reads=G == 4)
+    torch.cuda.synchronize()
+    assert int(c.err) == kvmm.ERR_NULL_BLOCK
+    c.check()
+
+
 @pytest.mark.parametrize("K", [1, 16, 17, 47, 130, 300])
 @pytest.mark.parametrize("B,Hkv,G,D,T", [(1, 1, 8, 128, 16), (1, 3, 1, 64, 16), (3, 2, 5, 128, 32), (7, 5, 4, 64, 32)])
 def test_clusters_of_every_size(K, B, Hkv, G, D, T):
