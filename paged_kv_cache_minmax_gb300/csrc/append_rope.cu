@@ -27,8 +27,8 @@
 // query and 8 KV heads of 128 channels (830 MB): 133 us, 0.92 of a copy's rate;
 // the first version, with a store between every two rows' loads and angles for
 // every head, took 240.  One token a sequence, batch 32: 5.2 us on the device.
-// Two prompts' 8K tokens into 4 bits (453 MB): 81 us, 0.82; the first version,
-// with a division a channel besides, took 151.
+// Two chunks of 8K tokens into 4 bits and, by kv4_gather, back (453 MB): 81 us,
+// 0.82; the first version, with a division a channel besides, took 151.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -260,9 +260,9 @@ constexpr int kQueryPasses = 4;  // rows of one token a lane turns: its loads in
 // Loads come before the stores that follow them in each batch: the compiler may not move a load over a store that
 // could alias it, so the order written is the number of bytes in flight.
 // Rows in flight: one pass a warp with 24 warps an SM, or two with 16.  The first is as fast or faster where the work
-// between load and store is long or a page is two passes (32K prompt, pages of 16: 133 us against 143; 336 tokens of 45
-// sequences into pages of 32 in 4 bits: 39 against 46); bf16 pages of 32 have four passes in a chain and little else
-// (short prompts: 8.4 us with two at once, 9.9 with one).
+// between load and store is long or a page has few passes (32K prompt, pages of 16: 133 us against 143; 336 tokens of 45
+// sequences into 4-bit pages of 32 and back: 39 against 46); bf16 pages of 32 have twice the passes in a chain and little
+// else (short prompts: 8.4 us with two at once, 9.9 with one).
 template <int T, bool KV4>
 constexpr int kAppBatch = T == 16 || KV4 ? 1 : 2;
 

@@ -423,3 +423,49 @@ def test_binding_refuses():
         t = torch.zeros(9, 2, 8, device="cuda")
         kvmm.kv_append_rope(c.shape, 1, None, c.k, c.v, c.tb, c.te, c.k_pool, c.v_pool, c.table, c.meta,
                             rope=kvmm.Rope(t, 16))
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_offsets_beyond_32_bits(four):
+    """Pages and rows that lie more than 2^31 elements and 2^32 bytes into their buffers: the bits of a small pool's."""
+    c = Case(D=128, T=32, n=70, begin=(5, 0), end=(75, 70), Pmax=3, L=1, layer=0, Hq=4, Hkv=2)
+    page = kvmm.kv4_page_bytes(c.shape)
+    n_phys = (5 << 30) // (page if four else 32 * 128 * 2)
+    far = n_phys - c.n_phys
+    shape = kvmm.make_shape(c.B, c.L, c.Hq, c.Hkv, c.D, c.T, c.Pmax, 4, n_phys)
+    wide = torch.empty(70 << 25, dtype=torch.bfloat16, device="cuda")
+
+    def strided(x):  # (one at a time: they share the buffer)
+        y = wide.as_strided(x.shape, (x.shape[2] * x.shape[3], 1 << 25, x.shape[3], 1))
+        y.copy_(x)
+        return y
+
+    def run(shape, q, k, v, pools, table):
+        meta, q_out = torch.zeros_like(c.meta), torch.zeros_like(c.q_out)
+        if four:
+            kvmm.kv4_append_rope(shape, 0, q, k, v, c.tb, c.te, *pools, table, meta, rope=c.rope, q_out=q_out, err=c.err)
+        else:
+            kvmm.kv_append_rope(shape, 0, q, k, v, c.tb, c.te, *pools, table, meta, rope=c.rope, q_out=q_out, err=c.err)
+        torch.cuda.synchronize()
+        assert int(c.err) == 0
+        return meta, q_out
+
+    if four:
+        near_pools = [torch.zeros(c.n_phys, page, dtype=torch.uint8, device="cuda")]
+    else:
+        near_pools = [torch.zeros_like(c.k_pool), torch.zeros_like(c.v_pool)]
+    far_pools = [torch.empty(n_phys, *p.shape[1:], dtype=p.dtype, device="cuda") for p in near_pools]
+    for p in far_pools:
+        p[far:] = 0
+    want = run(c.shape, c.q, c.k, c.v, near_pools, c.table)
+    got = run(shape, c.q, strided(c.k), c.v, far_pools, c.table + far)
+    for x, y in zip(want, got):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    for x, y in zip(near_pools, far_pools):
+        assert torch.equal(x.view(torch.uint8), y[far:].view(torch.uint8))
+    again = [torch.zeros_like(p) for p in near_pools]
+    got = run(c.shape, strided(c.q), c.k, c.v, again, c.table)
+    assert torch.equal(want[1], got[1])
+    run(c.shape, c.q, c.k, strided(c.v), again, c.table)
+    for x, y in zip(near_pools, again):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))

@@ -391,6 +391,43 @@ def test_invalid_entries_are_reported_and_skipped():
     f.check()
 
 
+def test_pages_beyond_32_bits():
+    """Pages more than 2^32 bytes into the pool: the bits of a small pool's."""
+    c = Cache([700, 333], D=128, T=32, Hq=8)
+    c.attend()
+    n_phys = (5 << 30) // c.pool.shape[1]
+    far = n_phys - c.n_phys
+    pool = torch.empty(n_phys, c.pool.shape[1], dtype=torch.uint8, device="cuda")
+    pool[far:] = c.pool
+    shape = kvmm.make_shape(c.B, c.L, c.Hq, c.Hkv, c.D, c.T, c.Pmax, 4, n_phys)
+    out = torch.zeros_like(c.out)
+    kvmm.sparse_paged_decode_attn_kv4(shape, 1, c.q, pool, c.table + far, c.seq_len, None, None, out, c.ws, err=c.err)
+    rows = [torch.zeros(2, 700, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kvmm.kv4_gather(c.shape, 1, c.pool, c.table, None, c.seq_len, rows[0], None, err=c.err)
+    kvmm.kv4_gather(shape, 1, pool, c.table + far, None, c.seq_len, rows[1], None, err=c.err)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    assert torch.equal(out, c.out) and torch.equal(*rows)
+
+
+@pytest.mark.parametrize("every", [False, True])
+def test_padded_batch_and_repeated_pages(every):
+    """Entries without a token, whose table rows and selections hold anything, and table rows behind a sequence's last
+    page; a page that is selected twice, or that two sequences share, counts for each."""
+    c = Cache([0, 100, 0, 100, 0], Pmax=40)
+    c.table[1::2, :, :, 7:] = 0x7FFFFFFF
+    c.table[0::2] = -0x80000000
+    c.table[3, 1, :, :4] = c.table[1, 1, :, :4]  # a shared prefix
+    if not every:
+        c.select(5)
+        c.sel[0::2] = 0x7FFFFFFF
+        c.sel[1, 1, 0, :5] = torch.tensor([2, 2, 6, 6, 6], dtype=torch.int32)
+    c.attend()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    c.check()
+
+
 def test_without_lse_and_error_word():
     c = Cache([300, 40])
     c.attend()
