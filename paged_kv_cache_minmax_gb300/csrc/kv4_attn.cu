@@ -81,26 +81,30 @@ __host__ __device__ constexpr int step_bytes(int D) { return kStep * (D + D / 8)
 struct Shared {
     uint64_t full[kWarps][4];  // a step has landed
     int2 meta[kWarps][4];      // per tile of the step: unit * 64 + valid tokens
-    uint64_t done[2], clear[2];  // a unit's partials are all stored; ... are merged (the buffers of G <= 4)
-    float m[2][kWarps][8];     // each warp's (in the final merge: each group's) reference and sum per head
-    float l[2][kWarps][8];
+    float m[2 * kWarps][8];    // each part's reference per head
+    float l[2 * kWarps][8];    // ... and sum
+    int unit[2 * kWarps];      // ... and unit, -1: none
+    float weight[2 * kWarps][8];  // the parts there are, in order: their weights
+    int at[2 * kWarps];           // ... and places
     int scan[kWarps];
     int total;                 // pages of the list
-    int last[2];
+    int span[2][2];            // units that several CTAs share: the first CTA, and, for the one that merges, how many
     float recv[8 * 128 + kKv4MaxCluster];  // received: every CTA's partial of this CTA's slice of the outputs
     float rstat[kKv4MaxCluster][16];       // received: (reference, sum) per head of every CTA of the cluster
 };
 
-// A warp's partial: a row of D + 8 floats a head, the D/8 channels of a row group one float apart from the next group's
-// (the lanes of a store then fall on different banks).  G <= 4: two buffers, so that a warp goes on to the next unit
-// without waiting for the slowest.
+// A warp's part of a unit: a row of D + 8 floats a head, the D/8 channels of a row group one float apart from the next
+// group's (the lanes of a store then fall on different banks).  A warp has two at most: part 2 * warp, of the unit that
+// began before its piece and ends in it, has a place of its own; part 2 * warp + 1, of the unit its piece ends in, goes
+// where its ring was.
 __host__ __device__ constexpr int part_row(int D) { return D + 8; }
-__host__ __device__ constexpr int part_buffers(int G) { return G <= 4 ? 2 : 1; }
-// dynamic shared memory: [rings][partials][first pages and page counts of the batch]
+static_assert(8 * part_row(128) * sizeof(float) <= ring_depth(128) * step_bytes(128) &&
+              8 * part_row(64) * sizeof(float) <= ring_depth(64) * step_bytes(64), "a part fits the ring");
+// dynamic shared memory: [rings][parts][first pages and page counts of the batch]
 __host__ __device__ constexpr size_t part_offset(int D) { return size_t(kWarps) * ring_depth(D) * step_bytes(D); }
 __host__ __device__ inline size_t list_offset(int D, int G)
 {
-    return part_offset(D) + size_t(part_buffers(G)) * kWarps * G * part_row(D) * sizeof(float);
+    return part_offset(D) + size_t(kWarps) * G * part_row(D) * sizeof(float);
 }
 inline size_t smem_bytes(int D, int G, int nb) { return list_offset(D, G) + size_t(2 * nb + 1) * sizeof(int); }
 
@@ -139,9 +143,10 @@ __device__ __forceinline__ int clamped_seq(const Kv4AttnParams& p, int b, bool t
 
 // The launch's page list: Kmax places a unit (selections), or the pages of every batch entry's sequence, head after
 // head.  Units count from the launch's first batch entry.
+template <int T>
 struct List {
     const int* first;  // every page: the first page of each batch entry, and the total
-    const int* count;  // ... and its pages
+    const int* seq;    // ... and its tokens
     int per, Hkv, nb;  // selections: places a unit (0: every page)
     __device__ __forceinline__ int batch_of(int f) const  // the last entry that starts at or before page f
     {
@@ -153,11 +158,12 @@ struct List {
         }
         return a;
     }
+    __device__ __forceinline__ int count(int b) const { return (seq[b] + T - 1) / T; }
     __device__ __forceinline__ int unit_of(int f) const
     {
         if (per) return f / per;
         const int b = batch_of(f);
-        return b * Hkv + (f - first[b]) / count[b];
+        return b * Hkv + (f - first[b]) / count(b);
     }
     __device__ __forceinline__ void range(int u, int& beg, int& end) const
     {
@@ -165,7 +171,7 @@ struct List {
             beg = u * per;
             end = beg + per;
         } else {
-            const int b = u / Hkv, n = count[b];
+            const int b = u / Hkv, n = count(b);
             beg = first[b] + (u - b * Hkv) * n;
             end = beg + n;
         }
@@ -192,16 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const int N = gridDim.x, rank = blockIdx.x;
     float* part = reinterpret_cast<float*>(smem + part_offset(D));
     int* first = reinterpret_cast<int*>(smem + list_offset(D, G));
-    int* count = first + p.nb + 1;
+    int* tokens = first + p.nb + 1;
 
     if (tid < kWarps * kDepth) {
         mbar_init(&sh.full[tid / kDepth][tid % kDepth], kPages);
-        if (tid < 2) {
-            mbar_init(&sh.done[tid], kWarps);
-            mbar_init(&sh.clear[tid], kWarps);
-        }
         fence_barrier_init();
     }
+    if (tid < 2 * kWarps) sh.unit[tid] = -1;
     __syncwarp();  // converged for the aligned barrier
     if (p.C > 1) cluster_arrive();  // passed before anything reaches another CTA
     // Every input may come from the preceding kernels.  Where the caller vouches for seq_len and the table, a launch
@@ -219,9 +222,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     } else {
         for (int base = 0; base < p.nb; base += kThreads) {
             const int i = base + tid;
-            int n = 0, inc;
-            if (i < p.nb) n = (clamped_seq(p, p.b0 + i, rank == 0) + T - 1) / T;
-            inc = n * p.Hkv;
+            int seq = 0;
+            if (i < p.nb) seq = clamped_seq(p, p.b0 + i, rank == 0);
+            const int n = (seq + T - 1) / T;
+            int inc = n * p.Hkv;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int o = __shfl_up_sync(kFullMask, inc, off);
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             }
             if (i < p.nb) {
                 first[i] = before + inc - n * p.Hkv;
-                count[i] = n;
+                tokens[i] = seq;
             }
             if (p.nb > base + kThreads) __syncthreads();
         }
@@ -246,25 +250,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         __syncthreads();
     }
     // places a unit has in the list: Kmax, or, with a cluster a unit, Pmax; 0: its pages, summed above
-    const List list{first, count, p.sel_idx != nullptr ? p.Kmax : p.C > 0 ? p.Pmax : 0, p.Hkv, p.nb};
+    const List<T> list{first, tokens, p.sel_idx != nullptr ? p.Kmax : p.C > 0 ? p.Pmax : 0, p.Hkv, p.nb};
     // (integer divisions are a large part of what comes before the first copy: a cluster's CTA makes few)
-    int lo, hi, first_unit;
+    int lo, hi, wlo, whi, first_unit;  // the CTA's piece, this warp's places in it (every stride-th step) and first unit
+    int stride = kWarps * kPages;
+    int unit_seq = 0;  // every page, a cluster a unit: its tokens
     if (p.C > 0) {  // a unit's places (every page: those its sequence fills) dealt to its C CTAs
         const int c = p.C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
         first_unit = p.C > 1 ? static_cast<int>(cluster_id()) : rank;
         int n = p.Kmax;
-        if (p.sel_idx == nullptr) n = (clamped_seq(p, p.b0 + first_unit / p.Hkv, c == 0 && first_unit % p.Hkv == 0) + T - 1) / T;
+        if (p.sel_idx == nullptr) {
+            unit_seq = clamped_seq(p, p.b0 + first_unit / p.Hkv, c == 0 && first_unit % p.Hkv == 0);
+            n = (unit_seq + T - 1) / T;
+        }
         lo = first_unit * list.per + n * c / p.C;  // (n <= 32768, C <= 16)
-        hi = first_unit * list.per + n * (c + 1) / p.C;
-    } else {
-        lo = hi = first_unit = 0;
+        hi = whi = first_unit * list.per + n * (c + 1) / p.C;
+        wlo = lo + kPages * warp;
+    } else {  // a piece of the CTA's piece, in whole steps, so that a warp meets few units
+        lo = hi = wlo = whi = first_unit = 0;
+        stride = kPages;
         if (total > 0) {
             const Pieces pieces(total, min(N, total));  // no piece is empty: the CTAs behind have none
             if (tid == 0) sh.total = total;
             if (rank < pieces.n) {
                 lo = pieces.start(rank);
                 hi = pieces.start(rank + 1);
-                first_unit = list.unit_of(lo);
+                const int steps = (hi - lo + kPages - 1) / kPages;
+                const int each = steps / kWarps, more = steps % kWarps;
+                wlo = lo + kPages * (each * warp + more * warp / kWarps);
+                whi = min(hi, lo + kPages * (each * (warp + 1) + more * (warp + 1) / kWarps));
+                if (wlo < whi) first_unit = list.unit_of(wlo);
             }
         }
     }
@@ -283,12 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             qv[i] = head < G ? reinterpret_cast<const uint4*>(qh)[i] : make_uint4(0u, 0u, 0u, 0u);
     };
 
-    // ---- this warp's steps: round r is pages lo + r * kStride + kPages * warp .. + kPages - 1 --------------------
-    constexpr int kStride = kWarps * kPages;
+    // ---- this warp's steps: round r is pages wlo + r * stride .. + kPages - 1 -------------------------------------
     constexpr int kBatch = 32 / kPages;  // rounds looked up at once, a page a lane
     uint8_t* ring = smem + static_cast<size_t>(warp) * kDepth * kSlot;
-    const int my_first = lo + kPages * warp;
-    const unsigned rounds = my_first < hi ? static_cast<unsigned>(hi - my_first + kStride - 1) / kStride : 0u;
+    const unsigned rounds = wlo < whi ? static_cast<unsigned>(whi - wlo + stride - 1) / static_cast<unsigned>(stride) : 0u;
     const uint64_t policy = l2_policy_evict_first();
     // A lane's page of the batch that starts with round rb: where it is held, and its word (unit * 64 + valid tokens;
     // without tokens there is nothing to copy).  Two dependent loads (the place in the selection, the table entry)
@@ -298,17 +311,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     int pmeta = 0;
     auto look_up = [&](int rb) {
         // (unsigned: a place behind the last may pass 2^31)
-        const unsigned at = static_cast<unsigned>(my_first) + static_cast<unsigned>(rb + lane / kPages) * kStride + lane % kPages;
+        const unsigned at = static_cast<unsigned>(wlo) + static_cast<unsigned>(rb + lane / kPages) * stride + lane % kPages;
         pmeta = 0x7fffffc0;  // behind the piece: after every unit
-        if (at >= static_cast<unsigned>(hi)) return;
+        if (at >= static_cast<unsigned>(whi)) return;
         const int f = static_cast<int>(at);
-        int b, h, lp, n, u;
+        int b, h, lp, u, seq;
         size_t unit;
         if (p.C > 0 && p.sel_idx == nullptr) {
             u = first_unit;
             b = u / p.Hkv;
             h = u - b * p.Hkv;
             lp = f - u * p.Pmax;
+            seq = unit_seq;
             unit = (static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + h;
             pmeta = u * 64;
         } else if (p.sel_idx != nullptr) {
@@ -317,24 +331,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             b = u / p.Hkv;
             h = u - b * p.Hkv;
             unit = (static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + h;
-            n = p.sel_cnt[unit];
+            const int n = p.sel_cnt[unit];
             lp = p.sel_idx[unit * p.Kmax + i];
-            const int seq = p.seq_len[p.b0 + b];
+            seq = p.seq_len[p.b0 + b];
             if (i == 0 && (n < 0 || n > p.Kmax || seq < 0 || seq > p.Pmax * T)) report(p.err, KVMM_ERR_OUT_OF_RANGE);
             pmeta = u * 64;
             if (i >= n) return;
+            seq = min(max(seq, 0), p.Pmax * T);
+            if (lp < 0 || lp >= (seq + T - 1) / T) {
+                report(p.err, KVMM_ERR_OUT_OF_RANGE);
+                return;
+            }
         } else {  // (the sum of the page counts has told of lengths out of range)
             b = list.batch_of(f);
-            h = (f - first[b]) / count[b];
-            lp = f - first[b] - h * count[b];
+            seq = tokens[b];
+            const int n = list.count(b);
+            h = (f - first[b]) / n;
+            lp = f - first[b] - h * n;
             u = b * p.Hkv + h;
             unit = (static_cast<size_t>(p.b0 + b) * p.L + p.layer) * p.Hkv + h;
             pmeta = u * 64;
-        }
-        const int seq = min(max(p.seq_len[p.b0 + b], 0), p.Pmax * T);
-        if (lp < 0 || lp >= (seq + T - 1) / T) {
-            report(p.err, KVMM_ERR_OUT_OF_RANGE);
-            return;
         }
         const int32_t phys = p.block_table[unit * p.Pmax + lp];
         if (phys < 0 || phys >= p.n_phys) {
@@ -365,13 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             if (nv > 0) bulk_copy_g2s_hint_at(copy_at + slot * kSlot, src, Page::kBytes, bar_at + slot * 8, policy);
         }
     };
-    if (!early && (p.C > 0 || lo < hi)) load_queries(first_unit);  // on their way while the pages are looked up
+    if (!early && (p.C > 0 || wlo < whi)) load_queries(first_unit);  // on their way while the pages are looked up
     look_up(0);
     if (early) pdl_wait_then_release();
     if (p.C == 0 && p.sel_idx == nullptr) {
         // sequences without a token: their results are written here, spread over the CTAs
         for (int b = rank; b < p.nb; b += N) {
-            if (count[b] != 0) continue;
+            if (tokens[b] != 0) continue;
             float* o = p.out + static_cast<size_t>(p.b0 + b) * p.Hq * D;
             for (int e = tid; e < p.Hq * D; e += kThreads) o[e] = 0.f;
             if (p.lse)
@@ -379,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         }
     }
     if (p.C == 0 && lo >= hi) return;  // (a cluster's CTA without a page takes part in its merge)
-    if (early) load_queries(first_unit);
+    if (early && (p.C > 0 || wlo < whi)) load_queries(first_unit);
 #pragma unroll
     for (unsigned r = 0; r < kDepth; ++r)
         if (r < rounds) issue(r);
@@ -390,64 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     const uint32_t v0_off = t0 * Page::kRow + gid * (D / 16), v1_off = t1 * Page::kRow + gid * (D / 16);
     const uint32_t vs0_off = t0 * Page::kGroups + gid * kMine / 16, vs1_off = t1 * Page::kGroups + gid * kMine / 16;
     unsigned r = 0;
-    int seg_unit[2] = {-1, -1};  // units whose parts this CTA stores: the one that began before, the one that goes on
 
-    // one output channel of one head over the warps' partials: unnormalised, with the reference and the sum
-    auto combine = [&](int e, int buf, float& M, float& L) {
-        const int g = e / D, d = e % D;
-        const float* x = part + (static_cast<size_t>(buf) * kWarps * G + g) * kPartRow + (d / kMine) * (kMine + 1) + d % kMine;
-        float m[kWarps];
-        M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            m[w] = sh.m[buf][w][g];
-            M = fmaxf(M, m[w]);
-        }
-        L = 0.f;
-        if (M == -INFINITY) return 0.f;
-        float O = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = fast_exp2(m[w] - M);
-            const float y = x[w * G * kPartRow];
-            L = fmaf(sh.l[buf][w][g], f, L);
-            O = fmaf(m[w] == -INFINITY ? 0.f : y, f, O);  // (a warp without a page of the unit left nothing)
-        }
-        return O;
+    auto part_at = [&](int k) {  // in bytes
+        return k & 1 ? static_cast<unsigned>(k >> 1) * (kDepth * kSlot)
+                     : static_cast<unsigned>(part_offset(D)) + static_cast<unsigned>(k >> 1) * (G * kPartRow * sizeof(float));
     };
-    // a unit's results, or this CTA's part of them
-    auto finish = [&](int u, int buf) {
-        int ubeg, uend;
-        list.range(u, ubeg, uend);
-        const bool whole = p.C > 0 || (ubeg >= lo && uend <= hi);
-        const int side = ubeg < lo ? 0 : 1;
-        if (!whole) seg_unit[side] = u;
-        float* slotp = p.partial + (static_cast<size_t>(rank) * 2 + side) * kv4_partial_floats(D);
-        for (int e = tid; e < G * D; e += kThreads) {
-            const int g = e / D;
-            float M, L;
-            const float O = combine(e, buf, M, L);
-            const size_t row = (static_cast<size_t>(p.b0) * p.Hkv + u) * G;
-            if (whole) {
-                p.out[row * D + e] = L > 0.f ? O * (p.v_scale / L) : 0.f;
-                if (e == g * D && p.lse) p.lse[row + g] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-            } else {
-                slotp[e] = O;
-                if (e == g * D) {
-                    slotp[8 * D + g] = M;
-                    slotp[8 * D + 8 + g] = L;
-                }
-            }
-        }
-    };
-    // the k-th time (from 0) that every warp has arrived
-    auto wait_warps = [&](uint64_t* bar, int k) {
-        if (!mbar_wait_bounded(bar, k & 1, 4 * kWaitNs) && lane == 0) report(p.err, KVMM_ERR_TIMEOUT);
-        __syncwarp();
-    };
-    int seg = 0, before = 0;  // units this CTA has finished with; the last one, whose partials wait to be merged
 
-    for (int u = first_unit;; ++u) {
+    for (int u = first_unit; p.C > 0 || wlo < whi; ++u) {
         int ubeg, uend;
         list.range(u, ubeg, uend);
         if (uend == ubeg) continue;  // an empty sequence (a page of another follows: hi is beyond)
@@ -683,204 +648,316 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             }
         }
 
-        if (p.C == 0 && uend < hi) {  // the next unit's queries are on their way during the merge
+        const bool last = p.C > 0 || uend >= whi;
+        if (!last) {  // the next unit's queries are on their way while this one's results are stored
             int nu = u + 1, b0, b1;
-            for (list.range(nu, b0, b1); b0 == b1; list.range(nu, b0, b1)) ++nu;  // (a unit with pages follows: hi is beyond)
+            for (list.range(nu, b0, b1); b0 == b1; list.range(nu, b0, b1)) ++nu;  // (a unit with pages follows: whi is beyond)
             load_queries(nu);
         }
-        // ---- the unit ends here (or this CTA's piece of it): merge the warps ---------------------------------------
+        // ---- the unit ends here (or this warp's piece of it) ------------------------------------------------------
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             l0 += __shfl_xor_sync(kFullMask, l0, off);
             l1 += __shfl_xor_sync(kFullMask, l1, off);
         }
-        const int buf = DUP ? seg & 1 : 0;
-        if (DUP && seg >= 2) wait_warps(&sh.clear[buf], (seg >> 1) - 1);
-        if (gid == 0 && (!DUP || tig < 2)) {
-            sh.m[buf][warp][col0] = m0;
-            sh.m[buf][warp][col0 + 1] = m1;
-            sh.l[buf][warp][col0] = l0;
-            sh.l[buf][warp][col0 + 1] = l1;
-        }
-        if (m0 != -INFINITY) {  // this warp had a page of the unit
-            float* mine = part + static_cast<size_t>(buf * kWarps + warp) * G * kPartRow + gid * (kMine + 1);
+        // a unit that this warp has alone is written out, else its part is stored
+        const bool whole = p.C == 0 && ubeg >= wlo && uend <= whi;
+        const int k = 2 * warp + (last ? 1 : 0);
+        const size_t row = (static_cast<size_t>(p.b0) * p.Hkv + u) * G;
+        __syncwarp();  // the last reads of the ring
+        auto results = [&](auto put) {  // put(which of the lane's heads, channel of its row group, value)
 #pragma unroll
             for (int i = 0; i < (DUP ? kTiles / 2 : kTiles); ++i) {
                 float v[4];
                 int d = i;
                 if (DUP) {  // hi + lo: the lanes with the hi columns take the first half of the tiles, the others the rest
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float give = tig < 2 ? o[i + kTiles / 2][k] : o[i][k];
-                        const float keep = tig < 2 ? o[i][k] : o[i + kTiles / 2][k];
-                        v[k] = keep + __shfl_xor_sync(kFullMask, give, 2);
+                    for (int j = 0; j < 4; ++j) {
+                        const float give = tig < 2 ? o[i + kTiles / 2][j] : o[i][j];
+                        const float keep = tig < 2 ? o[i][j] : o[i + kTiles / 2][j];
+                        v[j] = keep + __shfl_xor_sync(kFullMask, give, 2);
                     }
                     if (tig >= 2) d += kTiles / 2;
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = o[i][k];
+                    for (int j = 0; j < 4; ++j) v[j] = o[i][j];
                 }
                 if (col0 < G) {
-                    mine[col0 * kPartRow + d] = v[0];
-                    mine[col0 * kPartRow + d + kTiles] = v[2];
+                    put(0, d, v[0]);
+                    put(0, d + kTiles, v[2]);
                 }
                 if (col0 + 1 < G) {
-                    mine[(col0 + 1) * kPartRow + d] = v[1];
-                    mine[(col0 + 1) * kPartRow + d + kTiles] = v[3];
+                    put(1, d, v[1]);
+                    put(1, d + kTiles, v[3]);
                 }
             }
-        }
-        if (p.C > 1) {
-            // the unit's CTAs are a cluster: each stores, into every other, its references and sums and the slice of
-            // its outputs that the other owns; after one cluster barrier every CTA combines its slice
-            const int C = p.C, rc = static_cast<int>(cluster_ctarank());
-            const int slice = (G * D + C - 1) / C;
-            __syncthreads();
-            cluster_wait();
-            for (int e = tid; e < G * D; e += kThreads) {
-                const int c = e / slice;
-                float M, L;
-                const float O = combine(e, buf, M, L);
-                st_dsmem_f32(&sh.recv[rc * slice + (e - c * slice)], c, O);
-                if (e % D == 0)
-                    for (int k = 0; k < C; ++k) {
-                        st_dsmem_f32(&sh.rstat[rc][e / D], k, M);
-                        st_dsmem_f32(&sh.rstat[rc][8 + e / D], k, L);
-                    }
+        };
+        const bool tell = gid == 0 && (!DUP || tig < 2);
+        if (whole) {
+            float* dst = p.out + (row + col0) * D + gid * kMine;
+            const float f[2] = {l0 > 0.f ? p.v_scale / l0 : 0.f, l1 > 0.f ? p.v_scale / l1 : 0.f};
+            results([&](int h, int d, float v) { dst[h * D + d] = v * f[h]; });
+            if (p.lse && tell) {
+                if (col0 < G) p.lse[row + col0] = l0 > 0.f ? (m0 + log2f(l0)) * 0.6931471805599453f : -INFINITY;
+                if (col0 + 1 < G) p.lse[row + col0 + 1] = l1 > 0.f ? (m1 + log2f(l1)) * 0.6931471805599453f : -INFINITY;
             }
-            __syncwarp();
-            cluster_sync();
-            const size_t row0 = (static_cast<size_t>(p.b0) * p.Hkv + u) * G;
-            for (int i = tid; i < slice; i += kThreads) {
-                const int e = rc * slice + i, g = e / D;
-                if (e >= G * D) break;
-                float M = -INFINITY, L = 0.f, O = 0.f;
-                for (int c = 0; c < C; ++c) M = fmaxf(M, sh.rstat[c][g]);
-                if (M != -INFINITY)
-                    for (int c = 0; c < C; ++c) {
-                        const float f = exp2f(sh.rstat[c][g] - M);
-                        L = fmaf(sh.rstat[c][8 + g], f, L);
-                        O = fmaf(sh.recv[c * slice + i], f, O);
-                    }
-                p.out[row0 * D + e] = L > 0.f ? O * (p.v_scale / L) : 0.f;
-                if (p.lse && e == g * D) p.lse[row0 + g] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        } else {  // (zeros where the warp had no page of the unit)
+            const uint32_t dst = smem_addr(smem) + part_at(k) + (col0 * kPartRow + gid * (kMine + 1)) * sizeof(float);
+            results([&](int h, int d, float v) { sts_u32(dst + (h * kPartRow + d) * sizeof(float), __float_as_uint(v)); });
+            if (lane == 0) sh.unit[k] = u;
+            if (tell) {
+                sh.m[k][col0] = m0;
+                sh.m[k][col0 + 1] = m1;
+                sh.l[k][col0] = l0;
+                sh.l[k][col0 + 1] = l1;
+            }
+        }
+        if (last) break;
+    }
+    __syncthreads();  // the parts are stored
+
+    if (p.C > 0) {
+        const uint32_t ring0 = smem_addr(smem);
+        const size_t row = (static_cast<size_t>(p.b0) * p.Hkv + first_unit) * G;
+        auto write = [&](int e, float O, float M, float L) {
+            p.out[row * D + e] = L > 0.f ? O * (p.v_scale / L) : 0.f;
+            if (p.lse && e % D == 0) p.lse[row + e / D] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        };
+        // one output channel over the warps' parts: unnormalised, with the reference and the sum
+        auto combine = [&](int e, float& M, float& L) {
+            const int g = e / D, d = e % D;
+            const uint32_t at = ring0 + (g * kPartRow + d / kMine * (kMine + 1) + d % kMine) * sizeof(float);
+            float m[kWarps];
+            M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                m[w] = sh.m[2 * w + 1][g];
+                M = fmaxf(M, m[w]);
+            }
+            L = 0.f;
+            if (M == -INFINITY) return 0.f;
+            float O = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = fast_exp2(m[w] - M);
+                const float y = __uint_as_float(lds_u32<0>(at + w * (kDepth * kSlot)));
+                L = fmaf(sh.l[2 * w + 1][g], f, L);
+                O = fmaf(y, f, O);
+            }
+            return O;
+        };
+        if (p.C == 1) {
+            for (int e = tid; e < G * D; e += kThreads) {
+                float M, L;
+                const float O = combine(e, M, L);
+                write(e, O, M, L);
             }
             return;
         }
-        if (DUP) {  // the unit before this one has been left by every warp by now, or soon
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.done[buf]);
-            if (seg >= 1) {
-                wait_warps(&sh.done[buf ^ 1], (seg - 1) >> 1);
-                finish(before, buf ^ 1);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.clear[buf ^ 1]);
-            }
-            before = u;
-        } else {
-            __syncthreads();
-            finish(u, 0);
-            __syncthreads();  // the partials are free again
+        // the unit's CTAs are a cluster: each stores, into every other, its references and sums and the slice of
+        // its outputs that the other owns; after one cluster barrier every CTA combines its slice
+        const int C = p.C, rc = static_cast<int>(cluster_ctarank());
+        const int slice = (G * D + C - 1) / C;
+        cluster_wait();
+        for (int e = tid; e < G * D; e += kThreads) {
+            const int c = e / slice;
+            float M, L;
+            const float O = combine(e, M, L);
+            st_dsmem_f32(&sh.recv[rc * slice + (e - c * slice)], c, O);
+            if (e % D == 0)
+                for (int k = 0; k < C; ++k) {
+                    st_dsmem_f32(&sh.rstat[rc][e / D], k, M);
+                    st_dsmem_f32(&sh.rstat[rc][8 + e / D], k, L);
+                }
         }
-        ++seg;
-        if (p.C > 0 || uend >= hi) break;
+        __syncwarp();
+        cluster_sync();
+        for (int i = tid; i < slice; i += kThreads) {
+            const int e = rc * slice + i, g = e / D;
+            if (e >= G * D) break;
+            float M = -INFINITY, L = 0.f, O = 0.f;
+            for (int c = 0; c < C; ++c) M = fmaxf(M, sh.rstat[c][g]);
+            if (M != -INFINITY)
+                for (int c = 0; c < C; ++c) {
+                    const float f = exp2f(sh.rstat[c][g] - M);
+                    L = fmaf(sh.rstat[c][8 + g], f, L);
+                    O = fmaf(sh.recv[c * slice + i], f, O);
+                }
+            write(e, O, M, L);
+        }
+        return;
     }
-    if (DUP) {
-        wait_warps(&sh.done[(seg - 1) & 1], (seg - 1) >> 1);
-        finish(before, (seg - 1) & 1);
+
+    // ---- units that fell on several warps: the parts of one follow one another ----------------------------------
+    // (What follows is run once a launch: short loops, since its instructions come from memory that others are reading
+    // at full rate.  With the parts' reads unrolled and a running reference it took 7,800 clocks, so 1,900.)
+    const int mine = sh.unit[lane];  // a part a lane
+    const unsigned there = __ballot_sync(kFullMask, mine >= 0);
+    const unsigned behind = lane == 31 ? 0u : there & (~0u << (lane + 1));
+    const int next = __shfl_sync(kFullMask, mine, behind ? __ffs(behind) - 1 : lane);
+    const bool ends = mine >= 0 && (behind == 0u || next != mine);  // the last part of its unit
+    bool whole = false, begins = true;                              // the unit lies in this CTA; begins in it
+    if (mine >= 0) {
+        int ubeg, uend;
+        list.range(mine, ubeg, uend);
+        whole = ubeg >= lo && uend <= hi;
+        begins = ubeg >= lo;
     }
-    if (p.C > 0) return;
+    const int rank_of = __popc(there & ((1u << lane) - 1u));
+    if (warp == 0 && mine >= 0) sh.at[rank_of] = static_cast<int>(part_at(lane));
+    const unsigned ending = __ballot_sync(kFullMask, ends);
+    // the CTA's two places in the workspace: for the unit that began before, and the one that goes on
+    float* const slot0 = p.partial + static_cast<size_t>(rank) * 2 * kv4_partial_floats(D);
+    if (warp < G) {  // a head a warp: the parts' weights
+        float m = -INFINITY, l = 0.f;
+        if (mine >= 0) m = sh.m[lane][warp], l = sh.l[lane][warp];
+        const unsigned done = ending & ((1u << lane) - 1u), open = ending & (~0u << lane);
+        const int s = done ? 32 - __clz(done) : 0, t = open ? __ffs(open) - 1 : 31;  // the lanes of this part's unit
+        float M = m;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float x = __shfl_up_sync(kFullMask, M, off);
+            if (lane - off >= s) M = fmaxf(M, x);
+        }
+        M = __shfl_sync(kFullMask, M, t);
+        const float f = M == -INFINITY ? 0.f : exp2f(m - M);
+        float L = l * f;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float x = __shfl_up_sync(kFullMask, L, off);
+            if (lane - off >= s) L += x;
+        }
+        L = __shfl_sync(kFullMask, L, t);
+        if (mine >= 0) sh.weight[rank_of][warp] = !whole ? f : L > 0.f ? f * (p.v_scale / L) : 0.f;
+        if (ends) {
+            if (whole) {
+                if (p.lse)
+                    p.lse[(static_cast<size_t>(p.b0) * p.Hkv + mine) * G + warp] =
+                        L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            } else {
+                float* stat = slot0 + (begins ? kv4_partial_floats(D) : 0) + 8 * D + warp;
+                stat[0] = M;
+                stat[8] = L;
+            }
+        }
+    }
+    const unsigned whole_mask = __ballot_sync(kFullMask, whole), begin_mask = __ballot_sync(kFullMask, begins);
+    __syncthreads();
+    for (int e = tid; e < G * D; e += kThreads) {
+        const int g = e / D, d = e % D;
+        const uint32_t here = smem_addr(smem) + (g * kPartRow + d / kMine * (kMine + 1) + d % kMine) * sizeof(float);
+        int i = 0;
+#pragma unroll 1
+        for (unsigned left = ending; left != 0u; left &= left - 1u) {  // a unit a round
+            const int t = __ffs(left) - 1, to = __popc(there & ((2u << t) - 1u));
+            float* dst = whole_mask >> t & 1u ? p.out + (static_cast<size_t>(p.b0) * p.Hkv + sh.unit[t]) * G * D
+                                              : slot0 + (begin_mask >> t & 1u ? kv4_partial_floats(D) : 0);
+            float acc = 0.f;
+#pragma unroll 4
+            for (; i < to; ++i) acc = fmaf(sh.weight[i][g], __uint_as_float(lds_u32<0>(here + sh.at[i])), acc);
+            dst[e] = acc;
+        }
+    }
+    // units that several CTAs share: the first of them, and how many
+    int shared_unit[2], c0 = 0, np = 0;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const unsigned those = there & ~whole_mask & (side ? begin_mask : ~begin_mask);
+        shared_unit[side] = those ? sh.unit[__ffs(those) - 1] : -1;
+    }
+    if (tid < 2) {
+        sh.span[tid][1] = 0;
+        const int u = tid ? shared_unit[1] : shared_unit[0];
+        if (u >= 0) {
+            int beg, end;
+            list.range(u, beg, end);
+            const Pieces pieces(sh.total, min(N, sh.total));
+            c0 = pieces.owner(beg);
+            np = pieces.owner(end - 1) - c0 + 1;
+        }
+    }
     __syncthreads();  // this CTA's parts are stored
 
     // ---- units that fell on several CTAs: whoever stored the last part combines them ---------------------------
     // A unit's counter is that of the first CTA it lies in, which can be the first for one such unit only.
-    const Pieces pieces(sh.total, min(N, sh.total));
-    if (tid < 2) {
-        sh.last[tid] = 0;
-        const int u = seg_unit[tid];
-        if (u >= 0) {
-            int beg, end;
-            list.range(u, beg, end);
-            const int c0 = pieces.owner(beg), np = pieces.owner(end - 1) - c0 + 1;
-            // release: this CTA's parts, stored before the barrier above; acquire: the other CTAs'
-            int before;
-            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.counter + c0) : "memory");
-            if (before == np - 1) {
-                p.counter[c0] = 0;  // as the next call has to find it
-                sh.last[tid] = 1;
-            }
+    if (np > 0) {  // (threads 0 and 1)
+        // release: this CTA's parts, stored before the barrier above; acquire: the other CTAs'
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.counter + c0) : "memory");
+        if (before == np - 1) {
+            p.counter[c0] = 0;  // as the next call has to find it
+            sh.span[tid][0] = c0;
+            sh.span[tid][1] = np;
         }
     }
     __syncthreads();
+#pragma unroll 1
     for (int side = 0; side < 2; ++side) {
-        if (!sh.last[side]) continue;
-        const int u = seg_unit[side];
-        int beg, end;
-        list.range(u, beg, end);
-        const int c0 = pieces.owner(beg), np = pieces.owner(end - 1) - c0 + 1;
-        const size_t stride = kv4_partial_floats(D);
-        // A thread takes four channels of one head from every ngrp-th part, eight at a time with a running reference;
-        // the groups' results are then combined in shared memory (where the warps' partials were, so ngrp <= kWarps).
+        const int c0 = sh.span[side][0], np = sh.span[side][1];
+        if (np == 0) continue;
+        const size_t row = (static_cast<size_t>(p.b0) * p.Hkv + (side ? shared_unit[1] : shared_unit[0])) * G;
         // The first part is its CTA's last unit, the others are their CTAs' first.
+        constexpr size_t kPart = kv4_partial_floats(D);
+        const float* parts = p.partial + static_cast<size_t>(c0) * 2 * kPart;
+        auto part_of = [&](int k) { return parts + (k == 0 ? kPart : static_cast<size_t>(2 * k) * kPart); };
+        float* weight = reinterpret_cast<float*>(smem);  // [np][8], then the sums: where the rings were
+        float* sum = weight + kKv4MaxCtas * 8;
+        for (int i = tid; i < np * 8; i += kThreads) {
+            const float* stat = part_of(i >> 3) + 8 * D + (i & 7);
+            weight[i] = __ldcg(stat);
+            sum[i] = __ldcg(stat + 8);
+        }
+        // a thread takes four channels of one head from every ngrp-th part, eight loads in flight
         const int nf4 = G * D / 4, ngrp = min(min(kThreads / nf4, kWarps), np);
         const int grp = tid / nf4, e = tid - grp * nf4, g = 4 * e / D;
-        if (grp < ngrp) {
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            float M = -INFINITY, L = 0.f;
-            for (int k0 = grp; k0 < np; k0 += 8 * ngrp) {
-                float m[8], l[8];
-                float4 x[8];
+        float4 x[8];
+        auto load = [&](int k0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int k = k0 + i * ngrp;
-                    m[i] = -INFINITY;
-                    l[i] = 0.f;
-                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (k < np) {
-                        const float* slot = p.partial + (static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * stride;
-                        m[i] = __ldcg(slot + 8 * D + g);
-                        l[i] = __ldcg(slot + 8 * D + 8 + g);
-                        x[i] = __ldcg(reinterpret_cast<const float4*>(slot) + e);
-                    }
-                }
-                float top = M;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, m[i]);
-                if (top == -INFINITY) continue;  // no part has seen a token yet
-                const float old = exp2f(M - top);
-                L *= old;
-                a.x *= old, a.y *= old, a.z *= old, a.w *= old;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float f = exp2f(m[i] - top);
-                    L = fmaf(l[i], f, L);
-                    a.x = fmaf(x[i].x, f, a.x);
-                    a.y = fmaf(x[i].y, f, a.y);
-                    a.z = fmaf(x[i].z, f, a.z);
-                    a.w = fmaf(x[i].w, f, a.w);
-                }
-                M = top;
+            for (int i = 0; i < 8; ++i) {
+                const int k = k0 + i * ngrp;
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (grp < ngrp && k < np) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(k)) + e);
             }
-            reinterpret_cast<float4*>(part)[tid] = a;
-            if (4 * e == g * D) {
-                sh.m[0][grp][g] = M;
-                sh.l[0][grp][g] = L;
+        };
+        load(grp);
+        __syncthreads();
+        if (warp < G) {
+            float M = -INFINITY, L = 0.f;
+            for (int k = lane; k < np; k += 32) M = fmaxf(M, weight[8 * k + warp]);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
+            for (int k = lane; k < np; k += 32) {
+                const float f = M == -INFINITY ? 0.f : exp2f(weight[8 * k + warp] - M);
+                weight[8 * k + warp] = f;
+                L = fmaf(sum[8 * k + warp], f, L);
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(kFullMask, L, off);
+            if (lane == 0) {
+                sh.l[0][warp] = L > 0.f ? p.v_scale / L : 0.f;
+                if (p.lse) p.lse[row + warp] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
             }
         }
         __syncthreads();
-        const size_t row0 = (static_cast<size_t>(p.b0) * p.Hkv + u) * G;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k0 = grp; k0 < np; k0 += 8 * ngrp) {
+            if (k0 != grp) load(k0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = k0 + i * ngrp < np ? weight[8 * (k0 + i * ngrp) + g] : 0.f;
+                a.x = fmaf(x[i].x, f, a.x);
+                a.y = fmaf(x[i].y, f, a.y);
+                a.z = fmaf(x[i].z, f, a.z);
+                a.w = fmaf(x[i].w, f, a.w);
+            }
+        }
+        if (grp < ngrp) reinterpret_cast<float4*>(part)[tid] = a;  // (ngrp <= kWarps: they fit where the parts were)
+        __syncthreads();
         for (int i = tid; i < G * D; i += kThreads) {
-            const int h = i / D;
-            float M = -INFINITY, L = 0.f, O = 0.f;
-            for (int k = 0; k < ngrp; ++k) M = fmaxf(M, sh.m[0][k][h]);
-            if (M != -INFINITY)
-                for (int k = 0; k < ngrp; ++k) {
-                    const float f = exp2f(sh.m[0][k][h] - M);
-                    L = fmaf(sh.l[0][k][h], f, L);
-                    O = fmaf(part[k * G * D + i], f, O);
-                }
-            p.out[row0 * D + i] = L > 0.f ? O * (p.v_scale / L) : 0.f;
-            if (p.lse && i == h * D) p.lse[row0 + h] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            float O = 0.f;
+            for (int k = 0; k < ngrp; ++k) O += part[k * G * D + i];
+            p.out[row * D + i] = O * sh.l[0][i / D];
         }
         __syncthreads();
     }
