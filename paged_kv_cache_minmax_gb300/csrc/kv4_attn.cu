@@ -9,17 +9,20 @@
 // Work.  With no more units than SMs, and with selections or short sequences
 // (kShortTiles), each unit has a cluster of CTAs (as many as all run at once),
 // which share its places (selections: Kmax) or its sequence's pages and merge
-// their parts through distributed shared memory.  Else the pages of all units form one
-// list (with selections, Kmax places a unit) and CTA c of the N launched, one for
-// each SM, takes the c-th of N equal pieces of it, whatever the sequences'
-// lengths, so there is one wave without a tail.  Sixteen warps take a CTA's pages
-// in turn, two pages of 16 tokens or one of 32 a step, each through a private
-// ring of steps filled by one bulk copy a page (with the L2 policy of data read
-// once), running ahead across unit boundaries.  Where a unit ends (or the piece
-// does) the warps' partial results are merged in shared memory.  A unit that lies
-// in one CTA is written out at once; the parts of the others (two a CTA at most:
-// its first and its last unit) go to the workspace, and the CTA that stores a
-// unit's last part, as a counter tells it, combines them.
+// their parts through distributed shared memory.  Else the pages of all units
+// form one list (with selections, Kmax places a unit) and CTA c of the N
+// launched, one for each SM, takes the c-th of N equal pieces of it, whatever
+// the sequences' lengths, so there is one wave without a tail.
+// A step is two pages of 16 tokens or one of 32.  Sixteen warps take a cluster
+// CTA's steps in turn; of an even piece each takes a run, so that it meets few
+// units (832 units of up to 764 tokens: 28.9 us; in turn, with every unit merged
+// from all sixteen, 46.7).  Each warp's steps pass through a ring of its own,
+// filled by one bulk copy a page (with the L2 policy of data read once), and run
+// ahead across units.  What a warp has of a unit that is not its alone goes to
+// shared memory, and once a CTA the parts are joined.  A unit that lies in one
+// CTA is then written out; the parts of the others (two a CTA at most: its first
+// and its last unit) go to the workspace, and the CTA that stores a unit's last
+// part, as a counter tells it, combines them.
 //
 // A 16-token tile.  S^T[16 tok x 8 head] = K[16 x D] Q^T and O^T[D x 8] +=
 // V^T[D x 16] P^T on mma.sync m16n8k16 in fp16, fp32 accumulation: a group of
@@ -45,20 +48,22 @@
 //
 // Bound and measured (one GB300, us a launch in a graph of launches over three
 // inputs; the bytes are what the tokens hold, against the 6.78 TB/s of a copy).
-//   every page, one 128K sequence, 8 KV heads (151 MB)          34.3  0.65
-//   every page, 32 ragged sequences up to 16K tokens (449 MB)   88.4  0.75
-//   128 selected pages a head, 32K context, batch 8 (19 MB)     10.1  0.28
-//   64 pages of 32 tokens, five heads a KV head, batch 16 (36 MB) 13.4  0.39
+//   every page, one 128K sequence, 8 KV heads (151 MB)          35.3  0.63
+//   every page, 32 ragged sequences up to 16K tokens (449 MB)   83.6  0.79
+//   128 selected pages a head, 32K context, batch 8 (19 MB)     10.4  0.27
+//   64 pages of 32 tokens, five heads a KV head, batch 16 (36 MB) 13.7  0.39
 // Inside the long calls a tile takes 99 clocks an SM at 128K, the rate of the
 // memory; 237 of its 312 instructions are the tile's own (68 conversions, 64
 // products with scales, 16 MMAs).  What is left is latency: lengths, table and
-// first pages (3 us), the merge of warps, then of CTAs (4 us), the next launch
-// (2 us).  Short calls are that and the tiles' 95 clocks, on the 128 SMs that
-// whole clusters fill.
+// first pages (4 us), warps that end up to 2 us apart, the joins of warps, then
+// of CTAs (4 us), the next launch (2 us).  Short calls are that and the tiles' 95
+// clocks, on the 128 SMs that whole clusters fill.
 // Measured and not kept: a second launch for the merge (6 us of 20 at 32K), a
 // producer warp for all rings (the copies of one warp's lanes go out one after
 // another, 70 clocks each: 111 us against 97 for the ragged batch then), 8 or 12
-// warps with longer rings (124 and 112 against 106 then).
+// warps with longer rings (124 and 112 against 106 then), runs joined with all
+// their parts' reads unrolled (34.0 us against 28.9 for the 832 units) or a
+// cluster's by that short loop (12.2 against 10.4 for the selections).
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -789,8 +794,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     }
 
     // ---- units that fell on several warps: the parts of one follow one another ----------------------------------
-    // (What follows is run once a launch: short loops, since its instructions come from memory that others are reading
-    // at full rate.  With the parts' reads unrolled and a running reference it took 7,800 clocks, so 1,900.)
     const int mine = sh.unit[lane];  // a part a lane
     const unsigned there = __ballot_sync(kFullMask, mine >= 0);
     const unsigned behind = lane == 31 ? 0u : there & (~0u << (lane + 1));
@@ -1026,9 +1029,9 @@ cudaError_t launch(Kv4AttnParams p, cudaStream_t stream)
         // the SMs: with selections, or when a CTA's share of the longest sequence is short (kShortTiles).  What an
         // uneven batch then loses to its longest sequence is less than what dealing its pages evenly costs: the sum of
         // the lengths, the units that end inside a CTA and the merge through memory.  Six sequences of up to 1,914
-        // tokens, 8 KV heads: 9.3 us against 17.2; at the border, two of 32K 25.0 against 27.4, one of 64K 25.1
-        // against 23.1.  Beyond it the SMs that whole clusters leave empty (24 of 152) cost more: two of 60,000 tokens
-        // 40.4 against 37.0, one of 128K 43.7 against 34.9.
+        // tokens, 8 KV heads: 9.6 us against 16.0; at the border, sixteen of up to 4,096 19.2 against 24.7, four
+        // of up to 16K 20.3 against 21.7, one of 64K 25.5 against 23.4.  Beyond it the SMs that whole clusters leave
+        // empty (24 of 152) cost more: two of 60,000 tokens 40.8 against 33.6, one of 128K 44.1 against 35.3.
         const int places = p.sel_idx ? p.Kmax : p.Pmax;
         p.C = 0;
         if (units <= known.sms) {
