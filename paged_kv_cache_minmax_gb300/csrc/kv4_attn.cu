@@ -48,7 +48,7 @@
 //
 // Bound and measured (one GB300, us a launch in a graph of launches over three
 // inputs; the bytes are what the tokens hold, against the 6.78 TB/s of a copy).
-//   every page, one 128K sequence, 8 KV heads (151 MB)          35.3  0.63
+//   every page, one 128K sequence, 8 KV heads (151 MB)          35.0  0.64
 //   every page, 32 ragged sequences up to 16K tokens (449 MB)   83.6  0.79
 //   128 selected pages a head, 32K context, batch 8 (19 MB)     10.4  0.27
 //   64 pages of 32 tokens, five heads a KV head, batch 16 (36 MB) 13.7  0.39
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         lo = first_unit * list.per + n * c / p.C;  // (n <= 32768, C <= 16)
         hi = whi = first_unit * list.per + n * (c + 1) / p.C;
         wlo = lo + kPages * warp;
-    } else {  // a piece of the CTA's piece, in whole steps, so that a warp meets few units
+    } else {  // a run of the CTA's piece, so that a warp meets few units
         lo = hi = wlo = whi = first_unit = 0;
         stride = kPages;
         if (total > 0) {
@@ -280,10 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             if (rank < pieces.n) {
                 lo = pieces.start(rank);
                 hi = pieces.start(rank + 1);
-                const int steps = (hi - lo + kPages - 1) / kPages;
-                const int each = steps / kWarps, more = steps % kWarps;
-                wlo = lo + kPages * (each * warp + more * warp / kWarps);
-                whi = min(hi, lo + kPages * (each * (warp + 1) + more * (warp + 1) / kWarps));
+                const int each = (hi - lo) / kWarps, more = (hi - lo) % kWarps;
+                wlo = lo + each * warp + more * warp / kWarps;
+                whi = lo + each * (warp + 1) + more * (warp + 1) / kWarps;
                 if (wlo < whi) first_unit = list.unit_of(wlo);
             }
         }
@@ -1031,7 +1030,7 @@ cudaError_t launch(Kv4AttnParams p, cudaStream_t stream)
         // the lengths, the units that end inside a CTA and the merge through memory.  Six sequences of up to 1,914
         // tokens, 8 KV heads: 9.6 us against 16.0; at the border, sixteen of up to 4,096 19.2 against 24.7, four
         // of up to 16K 20.3 against 21.7, one of 64K 25.5 against 23.4.  Beyond it the SMs that whole clusters leave
-        // empty (24 of 152) cost more: two of 60,000 tokens 40.8 against 33.6, one of 128K 44.1 against 35.3.
+        // empty (24 of 152) cost more: two of 60,000 tokens 40.8 against 33.6, one of 128K 44.1 against 35.0.
         const int places = p.sel_idx ? p.Kmax : p.Pmax;
         p.C = 0;
         if (units <= known.sms) {
