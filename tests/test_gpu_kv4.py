@@ -488,6 +488,48 @@ def test_early_reads_give_the_same_bits():
         assert torch.equal(c.out, want)
 
 
+@pytest.mark.parametrize("seq,Hkv,T", [([70000, 0, 1200], 2, 16), ([70000, 40000], 2, 32), ([50, 0, 333, 17] * 50, 2, 16)])
+def test_units_across_ctas_early_captured_and_on_two_streams(seq, Hkv, T):
+    """Pages dealt evenly: early reads, two calls at once with their own workspaces, and a captured pair of calls
+    replayed with other lengths, all give the bits of a call by itself."""
+    c, d = (Cache(seq, Hq=Hkv * G, Hkv=Hkv, D=64, T=T, L=1, layer=0, seed=G, Pmax=4500) for G in (4, 7))
+    want = []
+    for x in (c, d):
+        x.attend()
+        torch.cuda.synchronize()
+        x.check(units={(b, h) for b in list(range(8)) + [len(seq) - 1] for h in range(Hkv)})
+        want.append((x.out.clone(), x.lse.clone()))
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for early in (False, True):
+        for x in (c, d):
+            x.out.fill_(3.0), x.lse.fill_(3.0)
+        torch.cuda.synchronize()
+        for _ in range(4):
+            c.attend(stream=streams[0], early_reads=early)
+            d.attend(stream=streams[1], early_reads=early)
+        torch.cuda.synchronize()
+        for x, (out, lse) in zip((c, d), want):
+            assert int(x.err) == 0
+            assert torch.equal(x.out, out) and torch.equal(x.lse, lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.attend(early_reads=True)
+        c.attend()
+    other = [(7 * n + 11) % (max(seq) + 1) for n in seq]
+    for lengths in (other, seq, [0] * len(seq), seq):
+        c.seq_len.copy_(torch.tensor(lengths, dtype=torch.int32))
+        c.out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(c.err) == 0
+        if lengths is seq:
+            assert torch.equal(c.out, want[0][0]) and torch.equal(c.lse, want[0][1])
+        c.seq = lengths
+        c.check(units={(b, h) for b in range(min(3, len(seq))) for h in range(Hkv)})
+        c.seq = list(seq)
+    assert int(c.ws[:1024].max()) == 0
+
+
 def test_early_reads_behind_an_append():
     """The append writes the pool, not the lengths or the table: the attention behind it may read those early."""
     D, T, Hkv, B = 128, 16, 2, 3
