@@ -610,7 +610,9 @@ typedef struct kvmm_rope {
  * tok_begin[b] <= n_new; rows behind that are neither read nor written.
  * rope NULL: nothing turns.  A rotated channel is rounded to bf16 once
  * (nearest even).  meta NULL: no MinMax is kept.  A query row is written
- * whatever its keys' table entries are.
+ * whatever its keys' table entries are.  A page that a call writes to belongs
+ * to one sequence and head: two ranges that reach the same physical page race
+ * (pages shared by sequences are read only).
  */
 kvmm_status kv_append_rope(const kvmm_shape* shape, int32_t layer, const kvmm_rows* q, const kvmm_rows* new_k,
                            const kvmm_rows* new_v, int32_t n_new, const int32_t* tok_begin, const int32_t* tok_end,
