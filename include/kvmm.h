@@ -632,11 +632,13 @@ kvmm_status kv_append_rope(const kvmm_shape* shape, int32_t layer, const kvmm_ro
  * held as y = x * fl(1 / k_scale) in fp32; scale = max |y| of the 16 channels
  * divided by 6, rounded to e4m3 (nearest even, at most 448); code = the
  * nearest e2m1 to y / scale (ties to the even code, at most 6 in magnitude),
- * 0 where the scale is 0.  code * scale has at most six significant bits, so
- * it is exact in bf16: the MinMax metadata of a 4-bit page are the exact
- * bounds of its keys over k_scale.  A positive factor common to a layer does
- * not change which pages page_score_topk selects; its scores are then those
- * over k_scale.
+ * 0 where the scale is 0.  An infinite y (of an infinity in a row, or of finite
+ * channels whose rotation or product with fl(1 / k_scale) leaves fp32's range)
+ * counts as fp32's largest value of its sign: scale 448, code +-6.
+ * code * scale has at most six significant bits, so it is exact in bf16: the
+ * MinMax metadata of a 4-bit page are the exact bounds of its keys over
+ * k_scale.  A positive factor common to a layer does not change which pages
+ * page_score_topk selects; its scores are then those over k_scale.
  *
  * kvmm_kv4_page_bytes: T * (D + D/8), 0 for an unsupported shape.
  *

@@ -29,6 +29,9 @@
 // every head, took 240.  One token a sequence, batch 32: 5.2 us on the device.
 // Two chunks of 8K tokens into 4 bits and, by kv4_gather, back (453 MB): 81 us,
 // 0.82; the first version, with a division a channel besides, took 151.
+#include <cfloat>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -122,10 +125,19 @@ __device__ __forceinline__ Pieces pieces(const AppendParams& p, int sub)
     return {2 * r + (sub - r), 2 * r + rest + (sub - r), false};
 }
 
-// x / d from r = 1/d (rounded): the product and one correction by its residual (Markstein 1990), x/d to within 2^-45
-// before the one rounding.  Where it is taken, what matters is that a quotient that is a border of the next, coarser
-// rounding comes out as that border and every other on its side of it: x has 24 significant bits and the product of d
-// and a border at most seven, so x/d is off a border by at least 1.01 half-steps of fp32 there, or not at all.
+// x with its magnitude limited to fp32's largest: an infinity becomes that value of its sign; NaN stays
+__device__ __forceinline__ float limited(float x)
+{
+    float y;
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(FLT_MAX));
+    return y;
+}
+
+// x / d for finite x, from r = 1/d (rounded): the product and one correction by its residual (Markstein 1990), x/d to
+// within 2^-45 before the one rounding.  Where it is taken, what matters is that a quotient that is a border of the
+// next, coarser rounding comes out as that border and every other on its side of it: x has 24 significant bits and the
+// product of d and a border at most seven, so x/d is off a border by at least 1.01 half-steps of fp32 there, or not at
+// all.
 __device__ __forceinline__ float quotient(float x, float d, float r)
 {
     const float q = __fmul_rn(x, r);
@@ -134,17 +146,26 @@ __device__ __forceinline__ float quotient(float x, float d, float r)
 
 // Hold a lane's two pieces in 4 bits: codes (eight nibbles a piece) and the
 // scales' bytes; `a`, `b` become x / factor.  Every lane of the warp calls.
+// LIMIT: an infinite x / factor counts as fp32's largest value.  Else it gives a
+// wrong scale and codes (the residual of its quotient is NaN), and `most`, the
+// running largest magnitude, tells of it.
+template <bool LIMIT>
 __device__ __forceinline__ void hold4(float (&a)[8], float (&b)[8], float inv, uint32_t& code_a, uint32_t& code_b,
-                                      uint32_t& scale_a, uint32_t& scale_b)
+                                      uint32_t& scale_a, uint32_t& scale_b, float& most)
 {
     float ma = 0.f, mb = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         a[i] = __fmul_rn(a[i], inv);
         b[i] = __fmul_rn(b[i], inv);
+        if (LIMIT) {
+            a[i] = limited(a[i]);
+            b[i] = limited(b[i]);
+        }
         ma = fmaxf(ma, fabsf(a[i]));
         mb = fmaxf(mb, fabsf(b[i]));
     }
+    if (!LIMIT) most = fmaxf(fmaxf(most, ma), mb);
     ma = fmaxf(ma, __shfl_xor_sync(kFullMask, ma, 1));  // the other eight channels of the scale
     mb = fmaxf(mb, __shfl_xor_sync(kFullMask, mb, 1));
     constexpr float kSixth = 1.f / 6.f;
@@ -395,110 +416,120 @@ __global__ void __launch_bounds__(kAppWarps * 32, kAppBatch<T, KV4> == 1 ? 3 : 2
     kvmm_bf16* vpage = KV4 ? nullptr : p.v_pool + static_cast<size_t>(phys) * T * D;
     constexpr unsigned kBatchRows = kRows * kBatch == 32 ? ~0u : (1u << (kRows * kBatch)) - 1u;
 
+    // Infinite values of 4-bit rows are looked for once a page, over the largest magnitudes that are there anyway, and
+    // the page's rows are then done again with limits (two chunks of 8K: 64.4 us; limits on every channel 65.8, a vote
+    // a row 65.2, without either 64.7).
     Bounds ba, bb;
-    ba.clear();
-    bb.clear();
+    float most = 0.f;
+    auto rows = [&](auto limit) {
+        ba.clear();
+        bb.clear();
 #pragma unroll 1
-    for (int i0 = 0; i0 < T; i0 += kRows * kBatch) {
-        const unsigned here = kBatchRows << i0;
-        if ((held & here) != 0u) {
-            uint4 va[kBatch], vb[kBatch];
-            if (KV4) {
-                uint32_t ca[kBatch], cb[kBatch], sa[kBatch], sb[kBatch];
+        for (int i0 = 0; i0 < T; i0 += kRows * kBatch) {
+            const unsigned here = kBatchRows << i0;
+            if ((held & here) != 0u) {
+                uint4 va[kBatch], vb[kBatch];
+                if (KV4) {
+                    uint32_t ca[kBatch], cb[kBatch], sa[kBatch], sb[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int r = i0 + i * kRows + rsub;
-                    const uint32_t* cd = reinterpret_cast<const uint32_t*>(page4 + r * Page::kRow);
-                    const uint8_t* sc = page4 + Page::kKeyScales + r * Page::kGroups;
-                    ca[i] = cd[pc.a], cb[i] = cd[pc.b], sa[i] = sc[pc.a >> 1], sb[i] = sc[pc.b >> 1];
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = i0 + i * kRows + rsub;
+                        const uint32_t* cd = reinterpret_cast<const uint32_t*>(page4 + r * Page::kRow);
+                        const uint8_t* sc = page4 + Page::kKeyScales + r * Page::kGroups;
+                        ca[i] = cd[pc.a], cb[i] = cd[pc.b], sa[i] = sc[pc.a >> 1], sb[i] = sc[pc.b >> 1];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) va[i] = held8(ca[i], sa[i]), vb[i] = held8(cb[i], sb[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const uint4* src = reinterpret_cast<const uint4*>(kpage + (i0 + i * kRows + rsub) * D);
+                        va[i] = src[pc.a];
+                        vb[i] = src[pc.b];
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) va[i] = held8(ca[i], sa[i]), vb[i] = held8(cb[i], sb[i]);
-            } else {
+                for (int i = 0; i < kBatch; ++i)
+                    if (held >> (i0 + i * kRows + rsub) & 1u) {
+                        ba.add(va[i]);
+                        bb.add(vb[i]);
+                    }
+            }
+            if ((fresh & here) == 0u) continue;
+            uint4 va[kBatch], vb[kBatch], wa[KV4 ? kBatch : 1], wb[KV4 ? kBatch : 1];
+            Angles g[kBatch];
+            bool mine[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const uint4* src = reinterpret_cast<const uint4*>(kpage + (i0 + i * kRows + rsub) * D);
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = i0 + i * kRows + rsub;
+                const int at = __shfl_sync(kFullMask, pos, r);
+                mine[i] = at >= 0;
+                va[i] = vb[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (KV4) wa[i] = wb[i] = va[i];
+                if (mine[i]) {
+                    const uint4* src = reinterpret_cast<const uint4*>(k_src + r * p.k.token_stride);
                     va[i] = src[pc.a];
                     vb[i] = src[pc.b];
+                    if (KV4) {
+                        src = reinterpret_cast<const uint4*>(v_src + r * p.v.token_stride);
+                        wa[i] = src[pc.a];
+                        wb[i] = src[pc.b];
+                    }
+                    if (pc.turns) g[i] = angles(p, at, pc);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (held >> (i0 + i * kRows + rsub) & 1u) {
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = i0 + i * kRows + rsub;
+                float a[8], c[8];
+                unpack8(va[i], a);
+                unpack8(vb[i], c);
+                if (mine[i] && pc.turns) rotate(p, g[i], a, c);
+                if (KV4) {
+                    uint32_t ca, cb, sa, sb;
+                    hold4<decltype(limit)::value>(a, c, p.k_inv, ca, cb, sa, sb, most);
+                    float x[8], y[8];
+                    unpack8(wa[i], x);
+                    unpack8(wb[i], y);
+                    uint32_t da, db, ta, tb4;
+                    hold4<decltype(limit)::value>(x, y, p.v_inv, da, db, ta, tb4, most);
+                    if (mine[i]) {
+                        uint32_t* cd = reinterpret_cast<uint32_t*>(page4 + r * Page::kRow);
+                        cd[pc.a] = ca;
+                        cd[pc.b] = cb;
+                        cd = reinterpret_cast<uint32_t*>(page4 + Page::kValues + r * Page::kRow);
+                        cd[pc.a] = da;
+                        cd[pc.b] = db;
+                        if ((sub & 1) == 0) {
+                            uint8_t* sc = page4 + Page::kKeyScales + r * Page::kGroups;
+                            sc[pc.a >> 1] = static_cast<uint8_t>(sa);
+                            sc[pc.b >> 1] = static_cast<uint8_t>(sb);
+                            sc = page4 + Page::kValueScales + r * Page::kGroups;
+                            sc[pc.a >> 1] = static_cast<uint8_t>(ta);
+                            sc[pc.b >> 1] = static_cast<uint8_t>(tb4);
+                        }
+                        if (p.meta != nullptr) {
+                            ba.add(held8(ca, sa));
+                            bb.add(held8(cb, sb));
+                        }
+                    }
+                } else if (mine[i]) {
+                    if (pc.turns) {
+                        va[i] = pack8(a);
+                        vb[i] = pack8(c);
+                    }
+                    uint4* dst = reinterpret_cast<uint4*>(kpage + r * D);
+                    dst[pc.a] = va[i];
+                    dst[pc.b] = vb[i];
                     ba.add(va[i]);
                     bb.add(vb[i]);
                 }
-        }
-        if ((fresh & here) == 0u) continue;
-        uint4 va[kBatch], vb[kBatch], wa[KV4 ? kBatch : 1], wb[KV4 ? kBatch : 1];
-        Angles g[kBatch];
-        bool mine[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = i0 + i * kRows + rsub;
-            const int at = __shfl_sync(kFullMask, pos, r);
-            mine[i] = at >= 0;
-            va[i] = vb[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (KV4) wa[i] = wb[i] = va[i];
-            if (mine[i]) {
-                const uint4* src = reinterpret_cast<const uint4*>(k_src + r * p.k.token_stride);
-                va[i] = src[pc.a];
-                vb[i] = src[pc.b];
-                if (KV4) {
-                    src = reinterpret_cast<const uint4*>(v_src + r * p.v.token_stride);
-                    wa[i] = src[pc.a];
-                    wb[i] = src[pc.b];
-                }
-                if (pc.turns) g[i] = angles(p, at, pc);
             }
         }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = i0 + i * kRows + rsub;
-            float a[8], c[8];
-            unpack8(va[i], a);
-            unpack8(vb[i], c);
-            if (mine[i] && pc.turns) rotate(p, g[i], a, c);
-            if (KV4) {
-                uint32_t ca, cb, sa, sb;
-                hold4(a, c, p.k_inv, ca, cb, sa, sb);
-                float x[8], y[8];
-                unpack8(wa[i], x);
-                unpack8(wb[i], y);
-                uint32_t da, db, ta, tb4;
-                hold4(x, y, p.v_inv, da, db, ta, tb4);
-                if (mine[i]) {
-                    uint32_t* cd = reinterpret_cast<uint32_t*>(page4 + r * Page::kRow);
-                    cd[pc.a] = ca;
-                    cd[pc.b] = cb;
-                    cd = reinterpret_cast<uint32_t*>(page4 + Page::kValues + r * Page::kRow);
-                    cd[pc.a] = da;
-                    cd[pc.b] = db;
-                    if ((sub & 1) == 0) {
-                        uint8_t* sc = page4 + Page::kKeyScales + r * Page::kGroups;
-                        sc[pc.a >> 1] = static_cast<uint8_t>(sa);
-                        sc[pc.b >> 1] = static_cast<uint8_t>(sb);
-                        sc = page4 + Page::kValueScales + r * Page::kGroups;
-                        sc[pc.a >> 1] = static_cast<uint8_t>(ta);
-                        sc[pc.b >> 1] = static_cast<uint8_t>(tb4);
-                    }
-                    if (p.meta != nullptr) {
-                        ba.add(held8(ca, sa));
-                        bb.add(held8(cb, sb));
-                    }
-                }
-            } else if (mine[i]) {
-                if (pc.turns) {
-                    va[i] = pack8(a);
-                    vb[i] = pack8(c);
-                }
-                uint4* dst = reinterpret_cast<uint4*>(kpage + r * D);
-                dst[pc.a] = va[i];
-                dst[pc.b] = vb[i];
-                ba.add(va[i]);
-                bb.add(vb[i]);
-            }
-        }
+    };
+    rows(std::false_type{});
+    if constexpr (KV4) {
+        if (__any_sync(kFullMask, most > FLT_MAX)) rows(std::true_type{});
     }
     if (p.meta != nullptr) {
 #pragma unroll
