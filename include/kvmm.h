@@ -34,8 +34,8 @@
  *   - Faults found on the device never trap: they OR a KVMM_ERR_* bit into
  *     the caller's device word *err (which the caller zeroes and reads after
  *     synchronising) and the offending page or row is skipped.
- *   - NaN or Inf inputs are not supported; they give undefined values but
- *     no fault.
+ *   - NaN or Inf inputs are not supported where a call does not say what
+ *     they give: they give undefined values but no fault.
  *   - Calls that share a workspace, or write the same outputs, must not
  *     run concurrently (calls on one stream never do).
  */
@@ -634,7 +634,9 @@ kvmm_status kv_append_rope(const kvmm_shape* shape, int32_t layer, const kvmm_ro
  * nearest e2m1 to y / scale (ties to the even code, at most 6 in magnitude),
  * 0 where the scale is 0.  An infinite y (of an infinity in a row, or of finite
  * channels whose rotation or product with fl(1 / k_scale) leaves fp32's range)
- * counts as fp32's largest value of its sign: scale 448, code +-6.
+ * counts as fp32's largest value of its sign: scale 448, code +-6.  A NaN makes
+ * its group's scale the e4m3 NaN (0x7f) and the 16 codes 7: they read back as
+ * NaN, and the MinMax hold it as kv_minmax_update does, above every number.
  * code * scale has at most six significant bits, so it is exact in bf16: the
  * MinMax metadata of a 4-bit page are the exact bounds of its keys over
  * k_scale.  A positive factor common to a layer does not change which pages

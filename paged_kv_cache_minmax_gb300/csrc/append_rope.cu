@@ -133,6 +133,13 @@ __device__ __forceinline__ float limited(float x)
     return y;
 }
 
+// the largest of m, |x| and |y|, NaN if one of them is (fmaxf would drop it, and the channel become a number)
+__device__ __forceinline__ float largest(float m, float x, float y)
+{
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(x), "f"(y));
+    return m;
+}
+
 // x / d for finite x, from r = 1/d (rounded): the product and one correction by its residual (Markstein 1990), x/d to
 // within 2^-45 before the one rounding.  Where it is taken, what matters is that a quotient that is a border of the
 // next, coarser rounding comes out as that border and every other on its side of it: x has 24 significant bits and the
@@ -146,6 +153,7 @@ __device__ __forceinline__ float quotient(float x, float d, float r)
 
 // Hold a lane's two pieces in 4 bits: codes (eight nibbles a piece) and the
 // scales' bytes; `a`, `b` become x / factor.  Every lane of the warp calls.
+// A NaN makes the scale NaN (0x7f) and the group's quotients NaN, whose code is 7.
 // LIMIT: an infinite x / factor counts as fp32's largest value.  Else it gives a
 // wrong scale and codes (the residual of its quotient is NaN), and `most`, the
 // running largest magnitude, tells of it.
@@ -153,7 +161,6 @@ template <bool LIMIT>
 __device__ __forceinline__ void hold4(float (&a)[8], float (&b)[8], float inv, uint32_t& code_a, uint32_t& code_b,
                                       uint32_t& scale_a, uint32_t& scale_b, float& most)
 {
-    float ma = 0.f, mb = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         a[i] = __fmul_rn(a[i], inv);
@@ -162,12 +169,16 @@ __device__ __forceinline__ void hold4(float (&a)[8], float (&b)[8], float inv, u
             a[i] = limited(a[i]);
             b[i] = limited(b[i]);
         }
-        ma = fmaxf(ma, fabsf(a[i]));
-        mb = fmaxf(mb, fabsf(b[i]));
     }
-    if (!LIMIT) most = fmaxf(fmaxf(most, ma), mb);
-    ma = fmaxf(ma, __shfl_xor_sync(kFullMask, ma, 1));  // the other eight channels of the scale
-    mb = fmaxf(mb, __shfl_xor_sync(kFullMask, mb, 1));
+    float ma = 0.f, mb = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        ma = largest(ma, a[i], a[i + 1]);
+        mb = largest(mb, b[i], b[i + 1]);
+    }
+    if (!LIMIT) most = fmaxf(fmaxf(most, ma), mb);  // (a group with a NaN needs no limits)
+    ma = largest(ma, __shfl_xor_sync(kFullMask, ma, 1), 0.f);  // the other eight channels of the scale
+    mb = largest(mb, __shfl_xor_sync(kFullMask, mb, 1), 0.f);
     constexpr float kSixth = 1.f / 6.f;
     scale_a = float_to_e4m3(quotient(ma, 6.f, kSixth));
     scale_b = float_to_e4m3(quotient(mb, 6.f, kSixth));

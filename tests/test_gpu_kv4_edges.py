@@ -63,3 +63,71 @@ def test_rotations_beyond_the_range_saturate(rope):
     pool0, meta0 = pool.clone(), c.meta.clone()
     append4(c, pool)
     check_four(c, pool0, pool, meta0, 1.0, 1.0)
+
+
+# ---- NaN ------------------------------------------------------------------------------------------------------
+def value_bits(codes, scales):
+    """bf16 bits of held values; 0x7fff where the scale is the NaN."""
+    v = kp.value(codes, scales).astype(np.float32).view(np.uint32) >> 16
+    return np.where(np.repeat(scales == 0x7F, 16, -1), 0x7FFF, v).astype(np.int64)
+
+
+def ordered(bits):
+    """bf16 bits -> integers in the order of the values (-0 below +0, NaN of either sign outermost)."""
+    return np.where(bits & 0x8000, 0x7FFF - bits, bits)
+
+
+def bounds_bits(bits):
+    at = ordered(bits)
+    take = lambda i: np.take_along_axis(bits, i[None], 0)[0]  # noqa: E731
+    return np.stack([take(at.argmin(0)), take(at.argmax(0))])
+
+
+def hold_nan(x, scale):
+    """kp.hold, with the groups that have a NaN: scale 0x7f, codes 7."""
+    bad = np.isnan(x).reshape(*x.shape[:-1], -1, 16).any(-1)
+    codes, scales = kp.hold(np.where(np.isnan(x), 0.0, x), scale)
+    return np.where(np.repeat(bad, 16, -1), 7, codes).astype(np.uint8), np.where(bad, 0x7F, scales).astype(np.uint8)
+
+
+@pytest.mark.parametrize("D,T", [(64, 16), (64, 32), (128, 16), (128, 32)])
+@pytest.mark.parametrize("payload", [0x7FC0, 0xFFC0, 0x7F81])
+@pytest.mark.filterwarnings("ignore::RuntimeWarning")
+def test_nan_stays_nan(D, T, payload):
+    """A NaN, of either sign, alone or beside an infinity, makes its group's scale the NaN, and no other group's."""
+    c = Case(Hq=2, D=D, T=T, n=24, begin=(4, 9), end=(28, 33), rope="none")
+    nan = torch.tensor([payload], dtype=torch.int32).to(torch.int16).view(torch.bfloat16).cuda()
+    rng = np.random.default_rng(D + T)
+    for rows in (c.k, c.v):
+        for b in range(2):
+            for i in range(0, 24, 3):
+                d = int(rng.integers(D))
+                rows[b, i, i % 2, d:d + 1] = nan
+                if i % 2:
+                    rows[b, i, i % 2, d ^ 1] = math.inf
+        rows[1, 5, 0] = nan  # a whole row
+    pool = fill_pool4(c)
+    want, meta0 = pool.cpu().numpy().copy(), c.meta.clone()
+    append4(c, pool, k_scale=2.0, v_scale=0.37)
+    want_m = meta0.view(torch.int16).cpu().numpy().astype(np.int64) & 0xFFFF
+    k, v = (x.float().cpu().numpy().astype(np.float64) for x in (c.k, c.v))
+    for b, tb, te in c.ranges():
+        (kc, ks), (vc, vs) = hold_nan(k[b], 2.0), hold_nan(v[b], 0.37)
+        for h in range(c.Hkv):
+            row = c.table[b, c.layer, h].cpu().numpy()
+            for t in range(tb, te):
+                for side, (codes, scales) in enumerate(((kc, ks), (vc, vs))):
+                    kp.put_row(want[row[t // T]], T, D, t % T, bool(side), codes[t - tb, h], scales[t - tb, h])
+            for p in range(tb // T, -(-te // T)):
+                held = value_bits(*kp.page_rows(want[row[p]], T, D, False))[:min(T, te - p * T)]
+                want_m[b, c.layer, h, p] = bounds_bits(held)
+    assert np.array_equal(pool.cpu().numpy(), want)
+    assert np.array_equal(c.meta.view(torch.int16).cpu().numpy().astype(np.int64) & 0xFFFF, want_m)
+    # read back: NaN in those groups, numbers elsewhere
+    out = [torch.zeros(2, 24, 2, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kvmm.kv4_gather(c.shape, c.layer, pool, c.table, c.tb, c.te, *out, k_scale=2.0, v_scale=0.37, err=c.err)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    for x, got in zip((k, v), out):
+        bad = np.repeat(np.isnan(x).reshape(2, 24, 2, -1, 16).any(-1), 16, -1)
+        assert np.array_equal(torch.isnan(got).cpu().numpy(), bad)
