@@ -631,8 +631,8 @@ kvmm_status kv_append_rope(const kvmm_shape* shape, int32_t layer, const kvmm_ro
  * and one for its values keeps the scales inside e4m3's range).  A row x is
  * held as y = x * fl(1 / k_scale) in fp32; scale = max |y| of the 16 channels
  * divided by 6, rounded to e4m3 (nearest even, at most 448); code = the
- * nearest e2m1 to y / scale (ties to the even code, at most 6 in magnitude),
- * 0 where the scale is 0.  An infinite y (of an infinity in a row, or of finite
+ * nearest e2m1 to y / scale (ties to the even code, at most 6 in magnitude, y's
+ * sign also where it is zero), 0 where the scale is 0.  An infinite y (of an infinity in a row, or of finite
  * channels whose rotation or product with fl(1 / k_scale) leaves fp32's range)
  * counts as fp32's largest value of its sign: scale 448, code +-6.  A NaN makes
  * its group's scale the e4m3 NaN (0x7f) and the 16 codes 7: they read back as

@@ -144,11 +144,11 @@ __device__ __forceinline__ float largest(float m, float x, float y)
 // within 2^-45 before the one rounding.  Where it is taken, what matters is that a quotient that is a border of the
 // next, coarser rounding comes out as that border and every other on its side of it: x has 24 significant bits and the
 // product of d and a border at most seven, so x/d is off a border by at least 1.01 half-steps of fp32 there, or not at
-// all.
+// all.  The residual is taken as q d - x, so that a zero x, whose residual is +0 either way, keeps its sign.
 __device__ __forceinline__ float quotient(float x, float d, float r)
 {
     const float q = __fmul_rn(x, r);
-    return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+    return __fmaf_rn(-__fmaf_rn(q, d, -x), r, q);
 }
 
 // Hold a lane's two pieces in 4 bits: codes (eight nibbles a piece) and the

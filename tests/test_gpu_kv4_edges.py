@@ -131,3 +131,19 @@ def test_nan_stays_nan(D, T, payload):
     for x, got in zip((k, v), out):
         bad = np.repeat(np.isnan(x).reshape(2, 24, 2, -1, 16).any(-1), 16, -1)
         assert np.array_equal(torch.isnan(got).cpu().numpy(), bad)
+
+
+# ---- signed zeros ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("rope", ["none", "half"])
+def test_zeros_keep_their_signs(rope):
+    """-0 is held as code 8 where its group's scale is not zero, as a negative value that rounds to zero is."""
+    c = Case(Hq=2, D=64, n=24, begin=(4, 9), end=(28, 33), rope=rope)
+    for rows in (c.k, c.v):
+        rows[:, :, :, 0::3] = -0.0
+        rows[:, :, :, 1::7] = 0.0
+        rows[:, ::2, :, 32:48] = -0.0  # groups of nothing else
+        rows[:, 1::2, :, 5] = -1e-3    # next to values near 1: rounds to zero
+    pool = fill_pool4(c)
+    pool0, meta0 = pool.clone(), c.meta.clone()
+    append4(c, pool)
+    check_four(c, pool0, pool, meta0, 1.0, 1.0)
