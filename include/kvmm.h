@@ -675,7 +675,9 @@ kvmm_status kv4_gather(const kvmm_shape* shape, int32_t layer, const uint8_t* kv
  * the cache holds, accumulated in fp32, with the same results for empty units
  * (out = 0, lse = -inf), invalid selections and table entries.  sel_idx and
  * sel_cnt both NULL: every page of the sequence (Kmax is then not used).
- * What a page holds behind its sequence's last token is not looked at.
+ * What a page holds behind its sequence's last token is not looked at.  A NaN
+ * in a query makes its head's results NaN, one in a key (a NaN scale) those of
+ * its unit, one in a value the unit's outputs in that scale's channels.
  * With no more units (batch entries x KV heads) than SMs, and selections or a
  * short table (Pmax), a cluster of CTAs shares a unit's Kmax places or its
  * pages.  Else the pages of all units are dealt evenly to one CTA for each

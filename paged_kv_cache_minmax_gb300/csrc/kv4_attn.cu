@@ -135,6 +135,18 @@ struct Pieces {
     }
 };
 
+// What parts of a unit are weighted against, M being their largest reference.  Without a score M is -inf: the parts are
+// then zeros, or NaN where every score was NaN, and keep that under the weight 2^(-inf - 0) = 0.
+__device__ __forceinline__ float base_of(float M) { return M == -INFINITY ? 0.f : M; }
+
+// The factor on a unit's sum of weighted values, and its lse, for the sum of weights L: 0 and -inf without a token
+// (L = 0), NaN where L is.
+__device__ __forceinline__ float out_factor(float v_scale, float L) { return L != 0.f ? v_scale / L : 0.f; }
+__device__ __forceinline__ float lse_of(float M, float L)
+{
+    return L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
 __device__ __forceinline__ int clamped_seq(const Kv4AttnParams& p, int b, bool tell)
 {
     const int cap = p.Pmax * p.T;
@@ -699,11 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         const bool tell = gid == 0 && (!DUP || tig < 2);
         if (whole) {
             float* dst = p.out + (row + col0) * D + gid * kMine;
-            const float f[2] = {l0 > 0.f ? p.v_scale / l0 : 0.f, l1 > 0.f ? p.v_scale / l1 : 0.f};
+            const float f[2] = {out_factor(p.v_scale, l0), out_factor(p.v_scale, l1)};
             results([&](int h, int d, float v) { dst[h * D + d] = v * f[h]; });
             if (p.lse && tell) {
-                if (col0 < G) p.lse[row + col0] = l0 > 0.f ? (m0 + log2f(l0)) * 0.6931471805599453f : -INFINITY;
-                if (col0 + 1 < G) p.lse[row + col0 + 1] = l1 > 0.f ? (m1 + log2f(l1)) * 0.6931471805599453f : -INFINITY;
+                if (col0 < G) p.lse[row + col0] = lse_of(m0, l0);
+                if (col0 + 1 < G) p.lse[row + col0 + 1] = lse_of(m1, l1);
             }
         } else {  // (zeros where the warp had no page of the unit)
             const uint32_t dst = smem_addr(smem) + part_at(k) + (col0 * kPartRow + gid * (kMine + 1)) * sizeof(float);
@@ -724,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         const uint32_t ring0 = smem_addr(smem);
         const size_t row = (static_cast<size_t>(p.b0) * p.Hkv + first_unit) * G;
         auto write = [&](int e, float O, float M, float L) {
-            p.out[row * D + e] = L > 0.f ? O * (p.v_scale / L) : 0.f;
-            if (p.lse && e % D == 0) p.lse[row + e / D] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            p.out[row * D + e] = O * out_factor(p.v_scale, L);
+            if (p.lse && e % D == 0) p.lse[row + e / D] = lse_of(M, L);
         };
         // one output channel over the warps' parts: unnormalised, with the reference and the sum
         auto combine = [&](int e, float& M, float& L) {
@@ -738,12 +750,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                 m[w] = sh.m[2 * w + 1][g];
                 M = fmaxf(M, m[w]);
             }
+            const float base = base_of(M);
             L = 0.f;
-            if (M == -INFINITY) return 0.f;
             float O = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = fast_exp2(m[w] - M);
+                const float f = fast_exp2(m[w] - base);
                 const float y = __uint_as_float(lds_u32<0>(at + w * (kDepth * kSlot)));
                 L = fmaf(sh.l[2 * w + 1][g], f, L);
                 O = fmaf(y, f, O);
@@ -781,12 +793,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             if (e >= G * D) break;
             float M = -INFINITY, L = 0.f, O = 0.f;
             for (int c = 0; c < C; ++c) M = fmaxf(M, sh.rstat[c][g]);
-            if (M != -INFINITY)
-                for (int c = 0; c < C; ++c) {
-                    const float f = exp2f(sh.rstat[c][g] - M);
-                    L = fmaf(sh.rstat[c][8 + g], f, L);
-                    O = fmaf(sh.recv[c * slice + i], f, O);
-                }
+            const float base = base_of(M);
+            for (int c = 0; c < C; ++c) {
+                const float f = exp2f(sh.rstat[c][g] - base);
+                L = fmaf(sh.rstat[c][8 + g], f, L);
+                O = fmaf(sh.recv[c * slice + i], f, O);
+            }
             write(e, O, M, L);
         }
         return;
@@ -822,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             if (lane - off >= s) M = fmaxf(M, x);
         }
         M = __shfl_sync(kFullMask, M, t);
-        const float f = M == -INFINITY ? 0.f : exp2f(m - M);
+        const float f = exp2f(m - base_of(M));
         float L = l * f;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -830,12 +842,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             if (lane - off >= s) L += x;
         }
         L = __shfl_sync(kFullMask, L, t);
-        if (mine >= 0) sh.weight[rank_of][warp] = !whole ? f : L > 0.f ? f * (p.v_scale / L) : 0.f;
+        if (mine >= 0) sh.weight[rank_of][warp] = whole ? f * out_factor(p.v_scale, L) : f;
         if (ends) {
             if (whole) {
                 if (p.lse)
-                    p.lse[(static_cast<size_t>(p.b0) * p.Hkv + mine) * G + warp] =
-                        L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                    p.lse[(static_cast<size_t>(p.b0) * p.Hkv + mine) * G + warp] = lse_of(M, L);
             } else {
                 float* stat = slot0 + (begins ? kv4_partial_floats(D) : 0) + 8 * D + warp;
                 stat[0] = M;
@@ -929,15 +940,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
             for (int k = lane; k < np; k += 32) {
-                const float f = M == -INFINITY ? 0.f : exp2f(weight[8 * k + warp] - M);
+                const float f = exp2f(weight[8 * k + warp] - base_of(M));
                 weight[8 * k + warp] = f;
                 L = fmaf(sum[8 * k + warp], f, L);
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(kFullMask, L, off);
             if (lane == 0) {
-                sh.l[0][warp] = L > 0.f ? p.v_scale / L : 0.f;
-                if (p.lse) p.lse[row + warp] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                sh.l[0][warp] = out_factor(p.v_scale, L);
+                if (p.lse) p.lse[row + warp] = lse_of(M, L);
             }
         }
         __syncthreads();

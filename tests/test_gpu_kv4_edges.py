@@ -9,6 +9,7 @@ import torch
 from paged_kv_cache_minmax_gb300 import kvmm
 from tests import kv4_plain as kp
 from tests.test_gpu_append_rope import Case, check_four, fill_pool4
+from tests.test_gpu_kv4 import Cache
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +148,92 @@ def test_zeros_keep_their_signs(rope):
     pool0, meta0 = pool.clone(), c.meta.clone()
     append4(c, pool)
     check_four(c, pool0, pool, meta0, 1.0, 1.0)
+
+
+# ---- NaN in the attention -------------------------------------------------------------------------------------
+class Poisoned(Cache):
+    """A cache whose numbers (`rows`) are kept as they were before some became NaN."""
+
+    def keep(self):
+        self.rows(0, 0)
+        self.q0 = self.q.clone()
+        G = self.Hq // self.Hkv
+        self.bad_out = np.zeros((self.B, self.Hkv, G, self.D), dtype=bool)
+        self.bad_lse = np.zeros((self.B, self.Hkv, G), dtype=bool)
+
+    def token(self, b, h, t):
+        """The page of token t and where its key and value scales begin."""
+        o, w = kp.offsets(self.T, self.D), self.D // 16
+        page = self.pool[int(self.table[b, self.layer, h, t // self.T])]
+        return page, o[1] + t % self.T * w, o[3] + t % self.T * w
+
+    def nan_query(self, b, head):
+        G = self.Hq // self.Hkv
+        self.q[b, head, 3] = math.nan
+        self.bad_out[b, head // G, head % G] = self.bad_lse[b, head // G, head % G] = True
+
+    def nan_key(self, b, h, t, group=1):
+        page, k, _ = self.token(b, h, t)
+        page[k + group] = 0x7F
+        self.bad_out[b, h] = self.bad_lse[b, h] = True
+
+    def nan_value(self, b, h, t, group=2):
+        page, _, v = self.token(b, h, t)
+        page[v + group] = 0x7F
+        self.bad_out[b, h, :, 16 * group:16 * group + 16] = True
+
+    def check_nan(self, units):
+        G = self.Hq // self.Hkv
+        out, lse, q = (x.float().cpu().numpy().astype(np.float64) for x in (self.out, self.lse, self.q0))
+        for b, h in units:
+            pages = None
+            if self.sel is not None:
+                pages = self.sel[b, self.layer, h, :int(self.cnt[b, self.layer, h])].cpu().numpy()
+            k, v = self.rows(b, h, pages)
+            g = slice(h * G, (h + 1) * G)
+            assert np.array_equal(np.isnan(out[b, g]), self.bad_out[b, h]), (b, h)
+            assert np.array_equal(np.isnan(lse[b, g]), self.bad_lse[b, h]), (b, h)
+            if k.shape[0] == 0:
+                assert (out[b, g] == 0).all() and (lse[b, g] == -np.inf).all(), (b, h)
+                continue
+            want, wl, zsum = kp.unit_attention(q[b, g], k, v, 1 / math.sqrt(self.D))
+            tol = kp.out_tolerance(self.D, zsum, np.abs(v).max())
+            assert np.nanmax(np.abs(out[b, g] - want), initial=0.0) <= tol, (b, h)
+            ok = ~self.bad_lse[b, h]
+            assert (np.abs(lse[b, g] - wl) <= kp.lse_tolerance(self.D, zsum, wl))[ok].all(), (b, h)
+
+
+@pytest.mark.parametrize("G,D,T", [(1, 128, 16), (4, 64, 32), (5, 128, 32), (8, 64, 16)])
+@pytest.mark.parametrize("mode", ["one CTA a unit", "clusters", "selections", "dealt, short", "dealt, long",
+                                  "dealt, selections"])
+def test_nan_reaches_the_results(mode, G, D, T):
+    """A NaN in a query reaches its head's results, one in a key its unit's, one in a value its channels', however the
+    pages were dealt; no other number changes its place among the tolerances."""
+    if mode == "one CTA a unit":
+        c = Poisoned([200, 33, 0], Hq=2 * G, D=D, T=T)
+    elif mode == "clusters":
+        c = Poisoned([2001, 777, 0], Hq=2 * G, D=D, T=T, L=1, layer=0)
+    elif mode == "selections":
+        c = Poisoned([2001, 777, 0], Hq=2 * G, D=D, T=T, L=1, layer=0)
+        c.select(c.Pmax, seed=3)
+    elif mode == "dealt, long":
+        c = Poisoned([70003, 20000, 0], Hq=2 * G, D=D, T=T, L=1, layer=0)
+    else:
+        c = Poisoned([200, 33, 0, 17] * 30, Hq=2 * G, D=D, T=T, L=1, layer=0)
+        if mode == "dealt, selections":
+            c.select(c.Pmax, seed=3)
+    c.keep()
+    c.nan_query(0, G - 1)      # the last head of the first group
+    c.nan_value(0, 1, 130)     # the other unit of that sequence
+    c.nan_key(1, 0, 0)         # the first token
+    c.nan_value(1, 1, 32, group=0)
+    c.nan_query(1, 2 * G - 1)
+    if c.B > 3:
+        c.nan_key(4, 1, 199)   # the last token
+        c.nan_value(5, 0, 15)
+    for _ in range(2):
+        c.attend()
+        torch.cuda.synchronize()
+        assert int(c.err) == 0
+        c.check_nan([(b, h) for b in range(min(c.B, 9)) for h in range(2)])
+    assert int(c.ws[:1024].max()) == 0
