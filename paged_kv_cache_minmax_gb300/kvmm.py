@@ -579,6 +579,19 @@ def _rows(t: torch.Tensor, name: str, B: int, n: int, H: int, D: int, here: int)
     return _pack_rows(t.data_ptr(), sb if B > 1 else 0, st if n > 1 else 0, sh if H > 1 else 0)
 
 
+def _dense(t: torch.Tensor, name: str, shape: tuple[int, ...]) -> None:
+    """The axes of a dense t step as those of [shape] do: one with longer rows, or rows in another order, holds them
+    elsewhere, however many elements it has."""
+    if t.shape == shape:
+        return
+    steps, step = {1}, 1
+    for n in reversed(shape[1:]):
+        step *= n
+        steps.add(step)
+    if any(n > 1 and st not in steps for n, st in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
 def _append_rows(f, q, new_k, new_v, tok_begin, tok_end, rope, q_out, here):
     """The arguments kv_append_rope and kv4_append_rope share, from q to q_out."""
     B, _, Hq, Hkv, D = f[:5]
@@ -590,6 +603,8 @@ def _append_rows(f, q, new_k, new_v, tok_begin, tok_end, rope, q_out, here):
             raise ValueError(f"the rope's table is on {rope.table.device}, the call on cuda:{here}")
         if rope.positions is not None and (rope.positions.numel() < B * n or rope.positions.get_device() != here):
             raise ValueError(f"positions needs {B * n} elements on cuda:{here}")
+        if rope.positions is not None:
+            _dense(rope.positions, "positions", (B, n))
     return (None if q is None else _rows(q, "q", B, n, Hq, D, here), _rows(new_k, "new_k", B, n, Hkv, D, here),
             _rows(new_v, "new_v", B, n, Hkv, D, here), n, _arg(tok_begin, "tok_begin", torch.int32, B, here),
             _arg(tok_end, "tok_end", torch.int32, B, here), None if rope is None else rope.ref,

@@ -1,0 +1,52 @@
+"""What the Python binding of the rotated appends checks and hands on, without a GPU: tensors that only say that they
+are on one."""
+import pytest
+import torch
+
+from paged_kv_cache_minmax_gb300 import kvmm
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that passes for one on device 0."""
+
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def here(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice)
+
+
+B, N, HQ, HKV, D = 3, 4, 8, 2, 64
+
+
+def arguments(rope=None, q_out=None, n=N):
+    """What _append_rows makes of n new rows of B sequences."""
+    f = (B, 1, HQ, HKV, D)
+    tok = here(B, dtype=torch.int32)
+    return kvmm._append_rows(f, here(B, n, HQ, D), here(B, n, HKV, D), here(B, n, HKV, D), tok, tok, rope,
+                             here(B, n, HQ, D) if q_out is None else q_out, 0)
+
+
+def turn(positions=None):
+    return kvmm.Rope(here(9, 2, D // 2, dtype=torch.float32), D, positions=positions)
+
+
+def ints(*shape):
+    return here(*shape, dtype=torch.int32)
+
+
+# ---- positions are [B][n_new] ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("shape", [(B, N), (B + 2, N), (B * N,), (B * N + 5,), (1, B * N), (B * N, 1), (B, N, 1)])
+def test_positions_that_are_dense_rows_pass(shape):
+    pos = ints(*shape)
+    assert arguments(turn(pos))[6] is not None
+
+
+@pytest.mark.parametrize("shape", [(B, N + 1), (B, 2 * N), (N, B), (B, 1), (B, 2, N), (B - 1, N), (B * N - 1,)])
+def test_positions_of_other_rows_are_refused(shape):
+    """A wider or otherwise laid out tensor has its rows where the kernel does not look for them."""
+    with pytest.raises(ValueError, match="positions"):
+        arguments(turn(ints(*shape)))
