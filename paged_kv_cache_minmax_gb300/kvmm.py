@@ -605,6 +605,8 @@ def _append_rows(f, q, new_k, new_v, tok_begin, tok_end, rope, q_out, here):
             raise ValueError(f"positions needs {B * n} elements on cuda:{here}")
         if rope.positions is not None:
             _dense(rope.positions, "positions", (B, n))
+    if q_out is not None and (n != 1 or q_out.shape != (B, Hq, D)):
+        _dense(q_out, "q_out", (B, n, Hq, D))
     return (None if q is None else _rows(q, "q", B, n, Hq, D, here), _rows(new_k, "new_k", B, n, Hkv, D, here),
             _rows(new_v, "new_v", B, n, Hkv, D, here), n, _arg(tok_begin, "tok_begin", torch.int32, B, here),
             _arg(tok_end, "tok_end", torch.int32, B, here), None if rope is None else rope.ref,

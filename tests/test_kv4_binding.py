@@ -50,3 +50,17 @@ def test_positions_of_other_rows_are_refused(shape):
     """A wider or otherwise laid out tensor has its rows where the kernel does not look for them."""
     with pytest.raises(ValueError, match="positions"):
         arguments(turn(ints(*shape)))
+
+
+# ---- so is q_out ----------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("n,shape", [(N, (B, N, HQ, D)), (N, (B + 1, N, HQ, D)), (N, (B * N * HQ * D + 64,)), (1, (B, HQ, D)),
+                                     (1, (B, 1, HQ, D)), (1, (B + 4, HQ, D)), (N, (B, N, HQ * D)), (N, (B * N, HQ, D))])
+def test_q_out_of_dense_rows_passes(n, shape):
+    assert arguments(q_out=here(*shape), n=n)[7] is not None
+
+
+@pytest.mark.parametrize("n,shape", [(N, (B, N + 1, HQ, D)), (N, (B, N, HQ + 1, D)), (N, (B, N, HQ, 2 * D)), (1, (B, 2, HQ, D)),
+                                     (N, (B, HQ, N, D)), (1, (B, HQ, 2 * D)), (1, (B, 2 * HQ, D))])
+def test_q_out_of_other_rows_is_refused(n, shape):
+    with pytest.raises(ValueError, match="q_out"):
+        arguments(q_out=here(*shape), n=n)
