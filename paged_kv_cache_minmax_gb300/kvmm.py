@@ -70,16 +70,34 @@ class RopeStruct(ctypes.Structure):
 class Rope:
     """The position rotation of kv_append_rope and kv4_append_rope: ``table`` [rows, 2, dim/2] float32 (cosines, then
     sines, of each position), the first ``dim`` channels turned in pairs (i, i + dim/2), or (2i, 2i + 1) with
-    ``interleaved``.  ``positions`` [B, n_new] int32: the tokens' positions when they are not their indices."""
+    ``interleaved``.  ``positions`` [B, n_new] int32: the tokens' positions when they are not their indices; it may be
+    replaced between calls, the table stays."""
 
     def __init__(self, table: torch.Tensor, dim: int, interleaved: bool = False, positions: torch.Tensor | None = None):
         if table.dim() != 3 or table.shape[1] != 2 or table.shape[2] * 2 != dim:
             raise ValueError(f"table must be [rows, 2, {dim // 2}], got {tuple(table.shape)}")
-        self.table, self.positions, self.dim = table, positions, dim
-        self.c = RopeStruct(_dev(table, "table", torch.float32),
-                            _dev(positions, "positions", torch.int32, optional=True), table.shape[0], dim,
-                            int(bool(interleaved)))
+        self._table = table
+        self.c = RopeStruct(_dev(table, "table", torch.float32), None, table.shape[0], dim, int(bool(interleaved)))
         self.ref = ctypes.byref(self.c)
+        self.positions = positions
+
+    @property
+    def table(self) -> torch.Tensor:
+        return self._table
+
+    @property
+    def dim(self) -> int:
+        return self.c.dim
+
+    @property
+    def positions(self) -> torch.Tensor | None:
+        return self._positions
+
+    @positions.setter
+    def positions(self, positions: torch.Tensor | None) -> None:
+        # (the struct holds the address that the kernel reads: checked and set together)
+        self.c.positions = _dev(positions, "positions", torch.int32, optional=True)
+        self._positions = positions
 
 
 def make_shape(B, L, Hq, Hkv, D, T, Pmax, Kmax, n_phys) -> Shape:

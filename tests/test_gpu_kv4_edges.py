@@ -237,3 +237,24 @@ def test_nan_reaches_the_results(mode, G, D, T):
         assert int(c.err) == 0
         c.check_nan([(b, h) for b in range(min(c.B, 9)) for h in range(2)])
     assert int(c.ws[:1024].max()) == 0
+
+
+# ---- positions replaced between calls -------------------------------------------------------------------------
+def test_positions_replaced_between_calls():
+    """A call turns its rows by the positions that its rope has then, whatever it had when it was made."""
+    a, b = (Case(n=5, begin=(3, 20), end=(8, 25)) for _ in range(2))
+    rope = kvmm.Rope(a.angles, a.dim, positions=torch.zeros(2, 5, dtype=torch.int32, device="cuda"))
+    for pos in ([[9, 1, 7, 30, 2], [5, 5, 6, 8, 0]], None, [[0, 1, 2, 3, 4], [90, 91, 92, 93, 94]]):
+        rope.positions = None if pos is None else torch.tensor(pos, dtype=torch.int32, device="cuda")
+        junk = torch.full((2, 5), 95, dtype=torch.int32, device="cuda")  # may take the memory of the ones before
+        fresh = kvmm.Rope(b.angles, b.dim, positions=rope.positions)
+        for c, r in ((a, rope), (b, fresh)):
+            kvmm.kv_append_rope(c.shape, 1, c.q, c.k, c.v, c.tb, c.te, c.k_pool, c.v_pool, c.table, c.meta, rope=r,
+                                q_out=c.q_out, err=c.err)
+        torch.cuda.synchronize()
+        assert int(a.err) == int(b.err) == 0 and int(junk[0, 0]) == 95
+        at = np.array(pos) if pos is not None else np.array([range(3, 8), range(20, 25)])
+        for i in range(2):
+            want = kp.bf16(a.turned(a.q[i].float().cpu().numpy().astype(np.float64), at[i]))
+            assert np.array_equal(a.q_out[i].float().cpu().numpy().astype(np.float64), want)
+        assert torch.equal(a.q_out, b.q_out) and torch.equal(a.k_pool, b.k_pool) and torch.equal(a.meta, b.meta)

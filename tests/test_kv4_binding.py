@@ -1,5 +1,7 @@
 """What the Python binding of the rotated appends checks and hands on, without a GPU: tensors that only say that they
 are on one."""
+import ctypes
+
 import pytest
 import torch
 
@@ -64,3 +66,33 @@ def test_q_out_of_dense_rows_passes(n, shape):
 def test_q_out_of_other_rows_is_refused(n, shape):
     with pytest.raises(ValueError, match="q_out"):
         arguments(q_out=here(*shape), n=n)
+
+
+# ---- a rope's tensors -----------------------------------------------------------------------------------------
+def handed_on(rope):
+    """The struct that a call with this rope gets."""
+    return ctypes.cast(arguments(rope)[6], ctypes.POINTER(kvmm.RopeStruct)).contents
+
+
+def test_positions_may_be_replaced():
+    """The pointer handed on is that of the tensor that was checked."""
+    rope = turn()
+    assert rope.positions is None and handed_on(rope).positions is None
+    for pos in (ints(B, N), ints(B, N), None, ints(B * N)):
+        rope.positions = pos
+        assert rope.positions is pos
+        assert handed_on(rope).positions == (None if pos is None else pos.data_ptr())
+    for bad, error in ((torch.zeros(B, N, dtype=torch.int32), "CUDA"), (here(B, N, dtype=torch.int64), "int32"),
+                       (ints(N, B).t(), "contiguous")):
+        with pytest.raises(ValueError, match=error):
+            rope.positions = bad
+    assert rope.positions is pos  # a refused tensor changes nothing
+    assert handed_on(rope).positions == pos.data_ptr()
+
+
+def test_the_table_stays():
+    rope = turn()
+    for name, value in (("table", here(9, 2, D // 2, dtype=torch.float32)), ("dim", 32)):
+        with pytest.raises(AttributeError):
+            setattr(rope, name, value)
+    assert handed_on(rope).table == rope.table.data_ptr() and rope.dim == D
