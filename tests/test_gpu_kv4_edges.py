@@ -258,3 +258,65 @@ def test_positions_replaced_between_calls():
             want = kp.bf16(a.turned(a.q[i].float().cpu().numpy().astype(np.float64), at[i]))
             assert np.array_equal(a.q_out[i].float().cpu().numpy().astype(np.float64), want)
         assert torch.equal(a.q_out, b.q_out) and torch.equal(a.k_pool, b.k_pool) and torch.equal(a.meta, b.meta)
+
+
+# ---- batches of more than one launch --------------------------------------------------------------------------
+def many(B, **kw):
+    """Short sequences, empty ones where the launches meet, longer ones among the last."""
+    rng = np.random.default_rng(B)
+    seq = [int(x) for x in rng.integers(0, 40, B)]
+    for b in (0, 511, 512, 1023, 1024, B - 2):
+        if b < B:
+            seq[b] = 0
+    seq[B - 1], seq[B - 3] = 630, 333
+    return Cache(seq, L=1, layer=0, Pmax=40, **kw)
+
+
+@pytest.mark.parametrize("early", [False, True])
+@pytest.mark.parametrize("B,Hkv,G,D,T", [(1030, 2, 4, 64, 16), (1030, 1, 3, 64, 32), (520, 1, 8, 128, 16), (517, 2, 5, 128, 32)])
+def test_every_page_in_several_launches(B, Hkv, G, D, T, early):
+    """More than 512 sequences: each launch's offsets into queries, outputs, lengths and table, its own way of dealing
+    the pages (the last few sequences by clusters), one workspace."""
+    c = many(B, Hq=Hkv * G, Hkv=Hkv, D=D, T=T)
+    c.spoil_behind()
+    for _ in range(2):
+        c.out.fill_(5.0), c.lse.fill_(5.0)
+        torch.cuda.synchronize()
+        c.attend(early_reads=early, v_scale=0.5)
+        torch.cuda.synchronize()
+        assert int(c.err) == 0
+        c.check(v_scale=0.5)
+    assert int(c.ws[:1024].max()) == 0
+
+
+@pytest.mark.parametrize("early", [False, True])
+@pytest.mark.parametrize("B,Hkv,G,D,T", [(1030, 2, 4, 64, 16), (520, 1, 8, 128, 32)])
+def test_selections_in_several_launches(B, Hkv, G, D, T, early):
+    c = many(B, Hq=Hkv * G, Hkv=Hkv, D=D, T=T)
+    rng = np.random.default_rng(7)
+    c.select(20, cnt=[int(x) for x in rng.integers(0, 21, B * Hkv)])
+    c.attend(early_reads=early)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    c.check()
+    assert int(c.ws[:1024].max()) == 0
+
+
+def test_bad_entries_in_a_later_launch():
+    """A length, a table entry and a selection out of their ranges in the second launch set their bits, and the other
+    sequences have their results."""
+    c = many(520, Hq=4, Hkv=1, D=64, T=16)
+    c.seq_len[515] = 9999
+    c.attend()
+    torch.cuda.synchronize()
+    assert int(c.err) == kvmm.ERR_OUT_OF_RANGE
+    units = {(b, 0) for b in range(520)} - {(515, 0)}
+    c.check(units=units)
+    c.seq_len[515] = c.seq[515]
+    c.err.zero_()
+    c.table[519, 0, 0, 5] = -1
+    c.__dict__.pop("_np")
+    c.attend()
+    torch.cuda.synchronize()
+    assert int(c.err) == kvmm.ERR_NULL_BLOCK
+    c.check()
