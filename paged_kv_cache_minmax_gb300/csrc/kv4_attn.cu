@@ -237,31 +237,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
         if (p.C == 0) total = p.nb * p.Hkv * p.Kmax;
         __syncthreads();  // the barriers exist
     } else {
-        for (int base = 0; base < p.nb; base += kThreads) {
-            const int i = base + tid;
-            int seq = 0;
-            if (i < p.nb) seq = clamped_seq(p, p.b0 + i, rank == 0);
-            const int n = (seq + T - 1) / T;
-            int inc = n * p.Hkv;
+        // a sequence a thread
+        static_assert(kKv4MaxBatch <= kThreads, "one pass sums the batch's pages");
+        int seq = 0;
+        if (tid < p.nb) seq = clamped_seq(p, p.b0 + tid, rank == 0);
+        const int pages = (seq + T - 1) / T * p.Hkv;
+        int inc = pages;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(kFullMask, inc, off);
-                if (lane >= off) inc += o;
-            }
-            if (lane == 31) sh.scan[warp] = inc;
-            __syncthreads();
-            int before = total;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(kFullMask, inc, off);
+            if (lane >= off) inc += o;
+        }
+        if (lane == 31) sh.scan[warp] = inc;
+        __syncthreads();
+        int before = 0;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const int v = sh.scan[w];
-                if (w < warp) before += v;
-                total += v;
-            }
-            if (i < p.nb) {
-                first[i] = before + inc - n * p.Hkv;
-                tokens[i] = seq;
-            }
-            if (p.nb > base + kThreads) __syncthreads();
+        for (int w = 0; w < kWarps; ++w) {
+            const int v = sh.scan[w];
+            if (w < warp) before += v;
+            total += v;
+        }
+        if (tid < p.nb) {
+            first[tid] = before + inc - pages;
+            tokens[tid] = seq;
         }
         if (tid == 0) first[p.nb] = total;
         __syncthreads();
