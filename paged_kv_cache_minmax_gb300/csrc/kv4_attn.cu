@@ -113,6 +113,16 @@ __host__ __device__ inline size_t list_offset(int D, int G)
 }
 inline size_t smem_bytes(int D, int G, int nb) { return list_offset(D, G) + size_t(2 * nb + 1) * sizeof(int); }
 
+// o += c for the four accumulators of a tile, two additions an instruction
+__device__ __forceinline__ void add4(float (&o)[4], const float (&c)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; k += 2)
+        asm("{.reg .b64 p, q; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %3}; add.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p;}"
+            : "+f"(o[k]), "+f"(o[k + 1])
+            : "f"(c[k]), "f"(c[k + 1]));
+}
+
 __device__ __forceinline__ float fast_exp2(float x)
 {
     float y;
@@ -208,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     constexpr int kMine = D / 8;     // output channels of a lane's row group
     constexpr int kVWords = D / 64;  // code words of a lane's V token
     constexpr int kPartRow = part_row(D);
+    constexpr int kChain = DUP ? 16 : 8;  // most steps of a unit that the tensor core adds up in a row: 32 products
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -463,9 +474,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        // The tensor core rounds its sums toward zero: over a run of n products outputs come out too small by n * 2^-26 or
+        // so (1.1e-6 at 63).  A longer run than kChain has its steps' sums added in fp32, rounded to nearest (32 ragged
+        // sequences, 80 products: error against 64 bits 1.5e-6 -> 3.3e-7, 83.8 -> 85.8 us; every step of every run that
+        // way: 13.4 -> 14.0 us for 64 pages of 32 and five heads).
+        const bool long_run =
+            (p.C > 0 ? static_cast<int>(rounds) * kPages : min(uend, whi) - max(ubeg, wlo)) > kChain * kPages;
         // One step.  FULL: both tiles are the unit's and have all their tokens (nearly every step: without its masks and
-        // branches, every page of 32 sequences up to 16K tokens takes 87 us, with them 95).
-        auto step = [&](auto whole_step, const uint32_t pg, const int nv0, const int nv1) {
+        // branches, every page of 32 sequences up to 16K tokens takes 87 us, with them 95).  APART: its
+        // sums are added in fp32.
+        auto step = [&](auto whole_step, auto apart, const uint32_t pg, const int nv0, const int nv1) {
             constexpr bool full = decltype(whole_step)::value;
             // tile j: tokens 16j .. 16j + 15 of the step, in page j (or the second half of the page)
             constexpr int kTile = kPages == 2 ? Page::kBytes : 16 * Page::kRow;
@@ -570,65 +588,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
                 }
             }
             // ---- values: channels gid * kMine .. + kMine - 1 of tokens t0, t1, t0 + 8, t1 + 8 of a tile -----------
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (j == 1 && !two) break;
-                uint32_t w[4][kVWords];
-                uint32_t sc[4];
-                auto values = [&](auto jc) {
-                    constexpr int kAt = Page::kValues + decltype(jc)::value * kTile;
-                    constexpr int kSc = Page::kValueScales + decltype(jc)::value * kTileScales;
-                    if constexpr (D == 128) {
-                        const uint2 y0 = lds_v2<kAt>(pg + v0_off), y1 = lds_v2<kAt>(pg + v1_off);
-                        const uint2 y2 = lds_v2<kAt + 8 * Page::kRow>(pg + v0_off), y3 = lds_v2<kAt + 8 * Page::kRow>(pg + v1_off);
-                        w[0][0] = y0.x, w[0][1] = y0.y, w[1][0] = y1.x, w[1][1] = y1.y;
-                        w[2][0] = y2.x, w[2][1] = y2.y, w[3][0] = y3.x, w[3][1] = y3.y;
-                    } else {
-                        w[0][0] = lds_u32<kAt>(pg + v0_off), w[1][0] = lds_u32<kAt>(pg + v1_off);
-                        w[2][0] = lds_u32<kAt + 8 * Page::kRow>(pg + v0_off), w[3][0] = lds_u32<kAt + 8 * Page::kRow>(pg + v1_off);
-                    }
-                    sc[0] = lds_u8<kSc>(pg + vs0_off), sc[1] = lds_u8<kSc>(pg + vs1_off);
-                    sc[2] = lds_u8<kSc + 8 * Page::kGroups>(pg + vs0_off), sc[3] = lds_u8<kSc + 8 * Page::kGroups>(pg + vs1_off);
-                };
-                if (j == 0) values(std::integral_constant<int, 0>{});
-                else values(std::integral_constant<int, 1>{});
+            // byte b of an even / odd word: channel 2b / 2b + 1 of a token pair
+            uint32_t ev01[2][kVWords], od01[2][kVWords], ev23[2][kVWords], od23[2][kVWords], s01[2], s23[2];
+            auto load = [&](auto jc) {
+                constexpr int j = decltype(jc)::value;
+                constexpr int kAt = Page::kValues + j * kTile, kSc = Page::kValueScales + j * kTileScales;
+                uint32_t w[4][kVWords], sc[4];
+                if constexpr (D == 128) {
+                    const uint2 y0 = lds_v2<kAt>(pg + v0_off), y1 = lds_v2<kAt>(pg + v1_off);
+                    const uint2 y2 = lds_v2<kAt + 8 * Page::kRow>(pg + v0_off), y3 = lds_v2<kAt + 8 * Page::kRow>(pg + v1_off);
+                    w[0][0] = y0.x, w[0][1] = y0.y, w[1][0] = y1.x, w[1][1] = y1.y;
+                    w[2][0] = y2.x, w[2][1] = y2.y, w[3][0] = y3.x, w[3][1] = y3.y;
+                } else {
+                    w[0][0] = lds_u32<kAt>(pg + v0_off), w[1][0] = lds_u32<kAt>(pg + v1_off);
+                    w[2][0] = lds_u32<kAt + 8 * Page::kRow>(pg + v0_off), w[3][0] = lds_u32<kAt + 8 * Page::kRow>(pg + v1_off);
+                }
+                sc[0] = lds_u8<kSc>(pg + vs0_off), sc[1] = lds_u8<kSc>(pg + vs1_off);
+                sc[2] = lds_u8<kSc + 8 * Page::kGroups>(pg + vs0_off), sc[3] = lds_u8<kSc + 8 * Page::kGroups>(pg + vs1_off);
                 if (!full) {  // a scale of zero: codes are always finite
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (((k & 1) ? t1 : t0) + (k >> 1) * 8 >= (j == 0 ? nv0 : nv1)) sc[k] = 0u;
                 }
-                const uint32_t s01 = e4m3x2_to_half2(prmt(sc[0], sc[1], 0x0040));
-                const uint32_t s23 = e4m3x2_to_half2(prmt(sc[2], sc[3], 0x0040));
-                // byte i of an even / odd word: channel 2i / 2i + 1 of a token pair
-                uint32_t ev01[kVWords], od01[kVWords], ev23[kVWords], od23[kVWords];
+                s01[j] = e4m3x2_to_half2(prmt(sc[0], sc[1], 0x0040));
+                s23[j] = e4m3x2_to_half2(prmt(sc[2], sc[3], 0x0040));
 #pragma unroll
                 for (int i = 0; i < kVWords; ++i) {
-                    ev01[i] = (w[0][i] & 0x0f0f0f0fu) | ((w[1][i] << 4) & 0xf0f0f0f0u);
-                    od01[i] = ((w[0][i] >> 4) & 0x0f0f0f0fu) | (w[1][i] & 0xf0f0f0f0u);
-                    ev23[i] = (w[2][i] & 0x0f0f0f0fu) | ((w[3][i] << 4) & 0xf0f0f0f0u);
-                    od23[i] = ((w[2][i] >> 4) & 0x0f0f0f0fu) | (w[3][i] & 0xf0f0f0f0u);
+                    ev01[j][i] = (w[0][i] & 0x0f0f0f0fu) | ((w[1][i] << 4) & 0xf0f0f0f0u);
+                    od01[j][i] = ((w[0][i] >> 4) & 0x0f0f0f0fu) | (w[1][i] & 0xf0f0f0f0u);
+                    ev23[j][i] = (w[2][i] & 0x0f0f0f0fu) | ((w[3][i] << 4) & 0xf0f0f0f0u);
+                    od23[j][i] = ((w[2][i] >> 4) & 0x0f0f0f0fu) | (w[3][i] & 0xf0f0f0f0u);
                 }
-                // tile i: rows gid are channel i of the lane's, rows gid + 8 channel kTiles + i
-                auto tile = [&](auto ic) {
-                    constexpr int i = decltype(ic)::value;
-                    constexpr int a = i, b = kTiles + i;  // channels
-                    constexpr int ba = (a % 8) / 2, bb = (b % 8) / 2;
-                    const uint32_t xa = (a & 1) ? od01[a / 8] : ev01[a / 8], xb = (b & 1) ? od01[b / 8] : ev01[b / 8];
-                    const uint32_t ya = (a & 1) ? od23[a / 8] : ev23[a / 8], yb = (b & 1) ? od23[b / 8] : ev23[b / 8];
-                    const uint32_t a0 = half2_mul(e2m1x2_to_half2<ba>(xa), s01), a1 = half2_mul(e2m1x2_to_half2<bb>(xb), s01);
-                    const uint32_t a2 = half2_mul(e2m1x2_to_half2<ba>(ya), s23), a3 = half2_mul(e2m1x2_to_half2<bb>(yb), s23);
-                    mma_f16_16816(o[i], a0, a1, a2, a3, bh[j][0], bh[j][1]);
-                    if (!DUP) mma_f16_16816(o[i], a0, a1, a2, a3, bl[j][0], bl[j][1]);
-                };
-                tile(std::integral_constant<int, 0>{});
-                tile(std::integral_constant<int, 1>{});
-                tile(std::integral_constant<int, 2>{});
-                tile(std::integral_constant<int, 3>{});
+            };
+            // m-tile i of token tile j: rows gid are channel i of the lane's, rows gid + 8 channel kTiles + i
+            auto product = [&](auto ic, const int j, float (&c)[4]) {
+                constexpr int a = decltype(ic)::value, b = kTiles + a;  // channels
+                constexpr int ba = (a % 8) / 2, bb = (b % 8) / 2;
+                const uint32_t xa = (a & 1) ? od01[j][a / 8] : ev01[j][a / 8], xb = (b & 1) ? od01[j][b / 8] : ev01[j][b / 8];
+                const uint32_t ya = (a & 1) ? od23[j][a / 8] : ev23[j][a / 8], yb = (b & 1) ? od23[j][b / 8] : ev23[j][b / 8];
+                const uint32_t a0 = half2_mul(e2m1x2_to_half2<ba>(xa), s01[j]), a1 = half2_mul(e2m1x2_to_half2<bb>(xb), s01[j]);
+                const uint32_t a2 = half2_mul(e2m1x2_to_half2<ba>(ya), s23[j]), a3 = half2_mul(e2m1x2_to_half2<bb>(yb), s23[j]);
+                mma_f16_16816(c, a0, a1, a2, a3, bh[j][0], bh[j][1]);
+                if (!DUP) mma_f16_16816(c, a0, a1, a2, a3, bl[j][0], bl[j][1]);
+            };
+            auto each = [&](auto f) {
+                f(std::integral_constant<int, 0>{});
+                f(std::integral_constant<int, 1>{});
+                f(std::integral_constant<int, 2>{});
+                f(std::integral_constant<int, 3>{});
                 if constexpr (kTiles == 8) {
-                    tile(std::integral_constant<int, 4>{});
-                    tile(std::integral_constant<int, 5>{});
-                    tile(std::integral_constant<int, 6>{});
-                    tile(std::integral_constant<int, 7>{});
+                    f(std::integral_constant<int, 4>{});
+                    f(std::integral_constant<int, 5>{});
+                    f(std::integral_constant<int, 6>{});
+                    f(std::integral_constant<int, 7>{});
+                }
+            };
+            load(std::integral_constant<int, 0>{});
+            if constexpr (decltype(apart)::value) {
+                load(std::integral_constant<int, 1>{});
+                each([&](auto ic) {
+                    float c[4] = {};
+                    product(ic, 0, c);
+                    product(ic, 1, c);
+                    add4(o[decltype(ic)::value], c);
+                });
+            } else {
+                each([&](auto ic) { product(ic, 0, o[decltype(ic)::value]); });
+                if (two) {
+                    load(std::integral_constant<int, 1>{});
+                    each([&](auto ic) { product(ic, 1, o[decltype(ic)::value]); });
                 }
             }
         };
@@ -645,13 +673,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
             const int2 meta = sh.meta[warp][slot];
             const uint32_t pg = ring_at + slot * kSlot;
             if (meta.x == u * 64 + 16 && meta.y == u * 64 + 16) {
-                step(std::true_type{}, pg, 16, 16);
+                if (long_run) step(std::true_type{}, std::true_type{}, pg, 16, 16);
+                else step(std::true_type{}, std::false_type{}, pg, 16, 16);
             } else {
                 if ((meta.x >> 6) > u) break;  // the step is of a later unit
                 const int nv0 = (meta.x >> 6) == u ? meta.x & 63 : 0, nv1 = (meta.y >> 6) == u ? meta.y & 63 : 0;
-                if (nv0 > 0) step(std::false_type{}, pg, nv0, nv1);
+                if (nv0 > 0) step(std::false_type{}, std::false_type{}, pg, nv0, nv1);
                 // the first page is of the unit before, or could not be read
-                else if (kPages == 2 && nv1 > 0) step(std::false_type{}, pg + Page::kBytes, nv1, 0);
+                else if (kPages == 2 && nv1 > 0) step(std::false_type{}, std::false_type{}, pg + Page::kBytes, nv1, 0);
                 if ((meta.y >> 6) > u && (meta.y & 63) != 0) break;  // the second page is of a later unit
             }
             ++r;

@@ -320,3 +320,55 @@ def test_bad_entries_in_a_later_launch():
     torch.cuda.synchronize()
     assert int(c.err) == kvmm.ERR_NULL_BLOCK
     c.check()
+
+
+# ---- long sums ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("G,D,T", [(4, 128, 16), (8, 128, 32), (2, 64, 32), (5, 64, 16)])
+@pytest.mark.parametrize("mode", ["every page", "selections, clusters", "selections, one CTA a unit", "a few tiles"])
+def test_long_sums_are_not_rounded_one_way(mode, G, D, T):
+    """Hundreds of tiles a warp: the mean error of outputs that are means of positive values.
+
+    With a query of zeros every probability is the same power of two and the sum of weights is exact, so all that is
+    rounded is the values' sum.  The tensor core rounds toward zero, at most 2^-23 of what it has, and may add up 32
+    products of one run at most, the k-th onto k/32 of the sum: (32 + 1) / 2 * 2^-23 = 2^-18.95 of it; on average over
+    the places in a step (half of it) and over where a sum lies between powers of two (0.72), 2^-20.4.  What is rounded
+    to nearest has no direction, and its mean over thousands of outputs vanishes beside that.  Longer runs rounded
+    toward zero would be off by their length over 32 times as much.
+    """
+    n_phys = 700
+    if mode == "every page":
+        B, Hkv, Pmax, K = 6, 4, 32768, 1
+    elif mode == "selections, clusters":
+        B, Hkv, Pmax, K = 2, 4, 64, 32768
+    elif mode == "selections, one CTA a unit":
+        B, Hkv, Pmax, K = 20, 5, 64, 6000
+    else:
+        B, Hkv, Pmax, K = 9, 2, 200, 1
+    g = torch.Generator(device="cuda").manual_seed(D + T)
+    shape = kvmm.make_shape(B, 1, Hkv * G, Hkv, D, T, Pmax, K, n_phys)
+    pool = torch.randint(0, 256, (n_phys, kvmm.kv4_page_bytes(shape)), generator=g, device="cuda", dtype=torch.uint8)
+    pool &= 0x77  # no signs; scales up to 2^7 * 15/8, with low bits that a long sum cannot keep
+    table = torch.randint(0, n_phys, (B, 1, Hkv, Pmax), generator=g, device="cuda", dtype=torch.int32)
+    seq = torch.full((B,), Pmax * T, dtype=torch.int32, device="cuda")
+    sel = cnt = None
+    pages = table[:, 0]
+    if K > 1:
+        sel = torch.randint(0, Pmax, (B, 1, Hkv, K), generator=g, device="cuda", dtype=torch.int32)
+        cnt = torch.full((B, 1, Hkv), K, dtype=torch.int32, device="cuda")
+        pages = table[:, 0].gather(2, sel[:, 0].long())
+    q = torch.zeros(B, Hkv * G, D, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.zeros(B, Hkv * G, D, device="cuda"), torch.zeros(B, Hkv * G, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvmm.sparse_paged_decode_attn_kv4(shape, 0, q, pool, table, seq, sel, cnt, out, kvmm.alloc_kv4_workspace(shape),
+                                      lse=lse, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    held = pool.cpu().numpy()
+    mean = np.stack([kp.value(*kp.page_rows(held[i], T, D, True)).mean(0) for i in range(n_phys)])  # a page's
+    count = np.stack([np.bincount(x, minlength=n_phys) for x in pages.reshape(B * Hkv, -1).cpu().numpy()])
+    want = (count @ mean / pages.shape[-1]).reshape(B, Hkv, 1, D)
+    off = out.double().cpu().numpy().reshape(B, Hkv, G, D) / want - 1
+    mean_off = float(off.mean())
+    assert abs(mean_off) <= 2.0 ** -20.4
+    tokens = pages.shape[-1] * T
+    assert np.abs(lse.cpu().numpy() - math.log(tokens)).max() <= 2.0 ** -22 * math.log(tokens) + 2.0 ** -22
