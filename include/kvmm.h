@@ -584,7 +584,8 @@ kvmm_status topk_stability_rco(const kvmm_shape* shape, const int32_t* hist_idx,
  * the sequence, or positions[b * n_new + j] for row j of batch b when
  * positions ([B][n_new] int32) is not NULL.  A row whose position lies
  * outside [0, rows) sets KVMM_ERR_OUT_OF_RANGE and is not written (neither
- * its query nor its key and value).
+ * its query nor its key and value; what its place in the page held stays, and
+ * counts for the page's MinMax).
  */
 typedef struct kvmm_rows {
     const kvmm_bf16* data;
@@ -689,7 +690,8 @@ kvmm_status kv4_gather(const kvmm_shape* shape, int32_t layer, const uint8_t* kv
  * counters zero again and nothing else in it matters to the next.
  * flags: 0, or KVMM_EARLY_READS: the caller guarantees that no kernel still
  * running when this launch starts writes seq_len or the layer's block-table
- * rows; the launch may then read them while that kernel drains.
+ * rows; the launch may then read them while that kernel drains (over every
+ * page; with selections the flag changes nothing).
  */
 size_t kvmm_kv4_workspace_size(const kvmm_shape* shape);
 

@@ -22,13 +22,15 @@
 // angles are looked up once, else rows of the whole list (32K prompt, 32 heads:
 // 133 us by blocks, 137 by rows; two 8K prompts, pages of 32: 71 and 77).
 //
-// Bound and measured (one GB300): prompts by the bytes they move, single tokens
-// by the chain of dependent loads (range, table entry, rows).  A 32K prompt, 32
-// query and 8 KV heads of 128 channels (830 MB): 133 us, 0.92 of a copy's rate;
-// the first version, with a store between every two rows' loads and angles for
-// every head, took 240.  One token a sequence, batch 32: 5.2 us on the device.
-// Two chunks of 8K tokens into 4 bits and, by kv4_gather, back (453 MB): 81 us,
-// 0.82; the first version, with a division a channel besides, took 151.
+// Bound and measured (one GB300): prompts by the bytes they move.  Single tokens
+// by a chain of loads: range, table entry, then the begun page's rows in passes
+// of which each waits for its loads (D = 128: four, 4-bit pages of 32 eight),
+// and after the MinMax the bf16 value row.  A 32K prompt, 32 query and 8 KV
+// heads of 128 channels (830 MB): 134 us, 0.91 of a copy's rate; the first
+// version, with a store between every two rows' loads and angles for every head,
+// took 240.  One token a sequence, batch 32: 5.1 us on the device.  Two chunks of
+// 8K tokens into 4 bits 64.5 us (364 MB, 0.83) and, by kv4_gather, back 81 (453
+// MB, 0.83); the first version, with a division a channel besides, took 151.
 #include <cfloat>
 #include <type_traits>
 
@@ -291,10 +293,11 @@ constexpr int kQueryPasses = 4;  // rows of one token a lane turns: its loads in
 
 // Loads come before the stores that follow them in each batch: the compiler may not move a load over a store that
 // could alias it, so the order written is the number of bytes in flight.
-// Rows in flight: one pass a warp with 24 warps an SM, or two with 16.  The first is as fast or faster where the work
-// between load and store is long or a page has few passes (32K prompt, pages of 16: 133 us against 143; 336 tokens of 45
-// sequences into 4-bit pages of 32 and back: 39 against 46); bf16 pages of 32 have twice the passes in a chain and little
-// else (short prompts: 8.4 us with two at once, 9.9 with one).
+// Rows in flight: one pass a warp with 24 warps an SM (80 registers a thread; the 4-bit kernels spill 32 or 36 bytes,
+// the bf16 ones 8 or 36), or two with 16 (no spills).  The first is as fast or faster where the work between load and
+// store is long or a page has few passes (32K prompt, pages of 16: 133 us against 143; 336 tokens of 45 sequences into
+// 4-bit pages of 32 and back: 39 against 46); bf16 pages of 32 have twice the passes in a chain and little else (short
+// prompts: 8.4 us with two at once, 9.9 with one).
 template <int T, bool KV4>
 constexpr int kAppBatch = T == 16 || KV4 ? 1 : 2;
 

@@ -15,8 +15,8 @@
 // the sequences' lengths, so there is one wave without a tail.
 // A step is two pages of 16 tokens or one of 32.  Sixteen warps take a cluster
 // CTA's steps in turn; of an even piece each takes a run, so that it meets few
-// units (832 units of up to 764 tokens: 28.9 us; in turn, with every unit merged
-// from all sixteen, 46.7).  Each warp's steps pass through a ring of its own,
+// units (832 units of up to 764 tokens: 46.7 us in turn, with every unit merged
+// from all sixteen, against 28.9 when runs came; 29.9 now).  Each warp's steps pass through a ring of its own,
 // filled by one bulk copy a page (with the L2 policy of data read once), and run
 // ahead across units.  What a warp has of a unit that is not its alone goes to
 // shared memory, and once a CTA the parts are joined.  A unit that lies in one
@@ -48,16 +48,17 @@
 //
 // Bound and measured (one GB300, us a launch in a graph of launches over three
 // inputs; the bytes are what the tokens hold, against the 6.78 TB/s of a copy).
-//   every page, one 128K sequence, 8 KV heads (151 MB)          35.0  0.64
-//   every page, 32 ragged sequences up to 16K tokens (449 MB)   83.6  0.79
-//   128 selected pages a head, 32K context, batch 8 (19 MB)     10.4  0.27
+//   every page, one 128K sequence, 8 KV heads (151 MB)          35.6  0.63
+//   every page, 32 ragged sequences up to 16K tokens (449 MB)   85.7  0.77
+//   128 selected pages a head, 32K context, batch 8 (19 MB)     10.9  0.26
 //   64 pages of 32 tokens, five heads a KV head, batch 16 (36 MB) 13.7  0.39
 // Inside the long calls a tile takes 99 clocks an SM at 128K, the rate of the
-// memory; 237 of its 312 instructions are the tile's own (68 conversions, 64
-// products with scales, 16 MMAs).  What is left is latency: lengths, table and
-// first pages (4 us), warps that end up to 2 us apart, the joins of warps, then
-// of CTAs (4 us), the next launch (2 us).  Short calls are that and the tiles' 95
-// clocks, on the 128 SMs that whole clusters fill.
+// memory.  Of the launch's 338 instructions a tile (all of them over all tiles)
+// 237 are the tile's own (68 conversions, 64 products with scales, 16 MMAs).
+// What is left is latency (clock stamps at 128K, of a state of 36.2 us): lengths,
+// table and first pages 4.0 us, warps that end up to 2.9 us apart, the joins of
+// warps, then of CTAs 6.6 us.  Short calls are that and the tiles' 95 clocks, on
+// the 128 SMs that whole clusters fill.
 // Measured and not kept: a second launch for the merge (6 us of 20 at 32K), a
 // producer warp for all rings (the copies of one warp's lanes go out one after
 // another, 70 clocks each: 111 us against 97 for the ragged batch then), 8 or 12
@@ -237,8 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnPara
     if (p.C > 1) cluster_arrive();  // passed before anything reaches another CTA
     // Every input may come from the preceding kernels.  Where the caller vouches for seq_len and the table, a launch
     // over every page sums the lengths and looks its first pages up while the preceding kernel drains, and waits for
-    // it before it reads a query or a page or stores anything but error bits (selections come from that kernel: with
-    // them there is nothing to read early).
+    // it before it reads a query or a page or stores anything but error bits.  That saves 1.2 to 2.6 us behind an
+    // append (one 128K sequence, both calls: 40.0 -> 37.9 us).  A launch with selections waits first: the pages come
+    // from them, and its table rows are not fetched ahead.
     const bool early = p.early != 0 && p.sel_idx == nullptr;
     if (!early) pdl_wait_then_release();
 

@@ -693,8 +693,8 @@ def sparse_paged_decode_attn_kv4(shape: Shape, layer: int, q, kv4_pool, block_ta
                                  workspace, lse=None, err=None, k_scale: float = 1.0, v_scale: float = 1.0,
                                  sm_scale: float = 0.0, stream=None, early_reads: bool = False) -> None:
     """Attention over the selected pages of the 4-bit cache, or, with sel_idx and sel_cnt None, over every page.
-    workspace: alloc_kv4_workspace.  ``early_reads``: no kernel still running when this launch starts writes seq_len
-    or the layer's block-table rows."""
+    workspace: alloc_kv4_workspace; calls that may run at once need one each.  ``early_reads``: no kernel still running
+    when this launch starts writes seq_len or the layer's block-table rows (used over every page alone)."""
     B, L, Hq, Hkv, D, T, Pmax, Kmax, n_phys = _fields(shape)
     if (sel_idx is None) != (sel_cnt is None):
         raise ValueError("sel_idx and sel_cnt are given together or not at all")
