@@ -59,7 +59,7 @@ def listed():
         # trees of 16 drawn without replacement for a batch of 8, a vocabulary of odd size
         _verify_case("verify_tree_b8", B=8, V=100003, n=16, width=3, draft="distinct"),
         # candidates that a head proposes with certainty, 24 a tree
-        _verify_case("verify_certain_b16", B=16, V=131072, n=24, width=4, draft="certain"),
+        _verify_case("verify_certain_b16", B=16, V=131072, n=24, width=4, draft="certain", sharp=6.0),
         # chains of seven for a batch of 64
         _verify_case("verify_chain_b64", B=64, V=131072, n=8),
         # one sequence's accepted nodes in 32 layers
@@ -80,7 +80,7 @@ def draw(rng):
     if kind == "verify":
         n, V = _log(rng, 1, 64), _log(rng, 50, 160000)
         return dict(kind=kind, n=n, V=V, B=_log(rng, 1, max(1, min(64, (1 << 26) // (n * V)))), width=rng.choice([1, 1, 2, 3, 5]),
-                    draft=rng.choice(["rows", "rows", "distinct", "certain"]), sharp=rng.choice([1.0, 2.5, 4.0]))
+                    draft=rng.choice(["rows", "rows", "distinct", "certain"]), sharp=rng.choice([1.0, 2.5, 4.0, 6.0]))
     D, T = rng.choice([64, 128, 128]), rng.choice([16, 32])
     Hkv, n = rng.choice([1, 2, 3, 4, 5, 8, 8]), _log(rng, 1, 64)
     if kind == "keep":
