@@ -702,6 +702,122 @@ kvmm_status sparse_paged_decode_attn_kv4(const kvmm_shape* shape, int32_t layer,
                                          void* workspace, size_t workspace_bytes, uint32_t flags, int32_t* err,
                                          kvmm_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Speculative decoding: a step takes a tree of up to 64 tokens a sequence
+ * instead of one.
+ *
+ * The pages have no counterpart to these calls.  Node 0 of a sequence's tree
+ * is its root, the token sampled last; the others are drafted.  n_max nodes
+ * are laid out for each sequence (1 <= n_max <= 64), of which the first
+ * n_nodes[b] exist (n_nodes [B] int32, NULL: n_max everywhere; 0: a slot of
+ * the batch without a sequence).  seq_len counts the settled tokens, which
+ * do not include the root.  A step is
+ *   kv_append_rope           the nodes' rows at the tokens seq_len + i (with
+ *                            positions seq_len + depth, and meta NULL: the
+ *                            bounds are taken by kv_keep_path)
+ *   page_score_topk          with the root's query, where pages are selected
+ *   sparse_paged_tree_attn   each node over settled tokens and its ancestors
+ *   draft_verify             which path is accepted, and the token after it
+ *   kv_keep_path             the path's rows to the tokens seq_len + 0, 1, ..
+ * after which seq_len grows by path_len and the new token is the next root.
+ *
+ * sparse_paged_tree_attn -- GQA attention of every node's query heads over
+ * the settled tokens (t < seq_len[b]) of its KV head's selected pages, or of
+ * every page with sel_idx and sel_cnt both NULL, and over the nodes (tokens
+ * seq_len[b] + j, j < n_nodes[b]) that its mask shows:
+ *     z_t = sm_scale * (q . k_t),  out = sum_t exp(z_t - m) v_t / sum_t exp(z_t - m),
+ *     lse = m + log(sum_t exp(z_t - m))
+ *   q, out     [B][n_max][Hq][D] bf16 (out is rounded once, from fp32)
+ *   lse        [B][n_max][Hq] float, or NULL
+ *   tree_mask  [B][n_max] uint64 (8-byte aligned): bit j of node i's word
+ *              shows it node j (its own bit counts like any other).  NULL: a
+ *              chain, node i sees the nodes 0 .. i.  Bits from n_nodes[b] on
+ *              do not matter.
+ * Scores, softmax and sums are fp32; a weight is rounded to bf16 where it
+ * meets the bf16 values.  sm_scale <= 0 means 1/sqrt(D).  A row to which
+ * nothing is shown yields out = 0 and lse = -inf.  Rows of nodes that do not
+ * exist are neither read nor written.  A page that has to be read and whose
+ * table entry is null or out of range sets its error bit and contributes
+ * nothing, as does a selected page >= the unit's page count; counts outside
+ * [0, Kmax], lengths outside [0, Pmax*T] and n_nodes outside [0, n_max] set
+ * KVMM_ERR_OUT_OF_RANGE and are clamped, and nodes whose token would lie
+ * beyond Pmax*T set it and are not attended.  What a page holds in slots that
+ * no settled token and no node has is not looked at.  Selections list each
+ * page once.
+ * workspace: kvmm_tree_workspace_size(shape, n_max) bytes, 16-byte aligned;
+ * nothing in it matters between calls.  The workspace size is 0 for an
+ * unsupported shape or n_max.
+ */
+size_t kvmm_tree_workspace_size(const kvmm_shape* shape, int32_t n_max);
+
+kvmm_status sparse_paged_tree_attn(const kvmm_shape* shape, int32_t layer, const kvmm_bf16* q, int32_t n_max,
+                                   const int32_t* n_nodes, const uint64_t* tree_mask, const kvmm_bf16* k_pool,
+                                   const kvmm_bf16* v_pool, const int32_t* block_table, const int32_t* seq_len,
+                                   const int32_t* sel_idx, const int32_t* sel_cnt, float sm_scale, kvmm_bf16* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, int32_t* err,
+                                   kvmm_stream stream);
+
+/* draft_verify -- walk each tree from its root along accepted nodes, and draw
+ * the token that follows the last one.
+ *   target_probs [B][n_max] rows of V floats, target_stride floats apart: row
+ *                i is the target model's distribution after node i
+ *   draft_probs  rows likewise, draft_stride apart: row i is the distribution
+ *                that node i's children were drawn from (rows of leaves do
+ *                not matter).  NULL: every child was proposed with certainty.
+ *   tokens, parent [B][n_max] int32: parent[i] < i is the node that node i
+ *                hangs from (parent[0] does not matter)
+ *   u_accept     [B][n_max] float in [0, 1): node i's random number
+ *   u_next       [B] float in [0, 1): the random number of the drawn token
+ *   path         [B][n_max] int32: the accepted nodes, 0 first, then -1
+ *   path_len     [B] int32: their count (>= 1; 0 where n_nodes is 0)
+ *   out_tokens   [B][n_max] int32: the path's tokens behind the root, then
+ *                the drawn token (path_len in all), then -1
+ * At a node whose target row is p and draft row q, its children are tried in
+ * order.  A probability weighs w(x) = floor(p(x) * 2^53) (p taken as at least
+ * 0 and at most 512), a whole number, so that sums are exact in any order.
+ * With W = 2^53 and Q = 1 at first, the child of token x is accepted if
+ *     u_accept * c(x) < w(x),   c(x) = floor(fl(q(x) * f) * 2^53),  f = fl(W / 2^53 / Q)
+ * (fl rounds to fp32; f = 0 where W or Q is not above 0; the product by
+ * u_accept is one of doubles).  If it is not, every w becomes max(w - c, 0),
+ * W their sum, and, with distinct != 0, Q loses q(x): children drawn without
+ * replacement, where distinct = 0 is for children drawn independently.  With
+ * draft_probs NULL c(x) is W, a rejected child's w becomes 0 and W loses it.
+ * Where no child is left, the token drawn is the least x whose w(0) + .. +
+ * w(x) exceeds floor(u_next * sum of w) (with w of the row p itself where
+ * that sum is 0).  So the accepted path and the drawn token are distributed
+ * as if sampled from the target alone.  A greedy target is a row that holds
+ * a single 1.
+ * A node whose parent is not in [0, i) or whose token is not in [0, V) sets
+ * KVMM_ERR_OUT_OF_RANGE and is not accepted; n_nodes outside [0, n_max] sets
+ * it and is clamped.  No workspace.
+ * Requires 1 <= n_max <= 64, V >= 1, strides >= V (and <= 2^40).
+ */
+kvmm_status draft_verify(int32_t B, int32_t n_max, int32_t V, const float* target_probs, int64_t target_stride,
+                         const float* draft_probs, int64_t draft_stride, const int32_t* tokens,
+                         const int32_t* parent, const int32_t* n_nodes, const float* u_accept, const float* u_next,
+                         int32_t distinct, int32_t* path, int32_t* path_len, int32_t* out_tokens, int32_t* err,
+                         kvmm_stream stream);
+
+/* kv_keep_path -- move the accepted nodes' keys and values to the end of the
+ * settled tokens, and take the MinMax of the pages there from kept rows alone.
+ *
+ * For every batch b, KV head and layer (every one with layer = -1, in one
+ * launch), with m = path_len[b]: token seq_len[b] + j takes the rows that
+ * token seq_len[b] + path[b][j] had before the call, j < m; then meta of
+ * every page that meets [seq_len[b] rounded down to its page, seq_len[b] + m)
+ * is recomputed over the page's tokens below seq_len[b] + m (as
+ * kv_minmax_update takes it).  meta NULL: no MinMax is kept.  seq_len is not
+ * changed.  path [B][n_max] must ascend strictly within [0, n_max) over its
+ * first m entries; a path that does not, m outside [0, n_max], or seq_len
+ * outside [0, Pmax*T] sets KVMM_ERR_OUT_OF_RANGE and leaves that sequence as
+ * it was.  A row whose old or new place lies beyond Pmax*T, or in a page
+ * whose table entry is null or out of range, sets its error bit and is not
+ * moved.  The pages written belong to one sequence and head.
+ */
+kvmm_status kv_keep_path(const kvmm_shape* shape, int32_t layer, const int32_t* path, const int32_t* path_len,
+                         int32_t n_max, const int32_t* seq_len, kvmm_bf16* k_pool, kvmm_bf16* v_pool,
+                         const int32_t* block_table, kvmm_bf16* meta, int32_t* err, kvmm_stream stream);
+
 /* Workspace bytes that page_score_topk and page_score_topk_attn need
  * (sparse_paged_decode_attn needs none; num_splits is accepted for the
  * stable signature and ignored).  Returns 0 for an unsupported shape. */

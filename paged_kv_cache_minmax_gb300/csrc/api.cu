@@ -1030,4 +1030,129 @@ kvmm_status sparse_paged_decode_attn_kv4(const kvmm_shape* shape, int32_t layer,
     return launched(kvmm::launch_kv4_attention(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t kvmm_tree_workspace_size(const kvmm_shape* shape, int32_t n_max)
+{
+    if (check_shape(shape) != KVMM_OK || n_max < 1 || n_max > kvmm::kTreeMaxNodes) return 0;
+    return kvmm::tree_ws_bytes(*shape, n_max);
+}
+
+kvmm_status sparse_paged_tree_attn(const kvmm_shape* shape, int32_t layer, const kvmm_bf16* q, int32_t n_max,
+                                   const int32_t* n_nodes, const uint64_t* tree_mask, const kvmm_bf16* k_pool,
+                                   const kvmm_bf16* v_pool, const int32_t* block_table, const int32_t* seq_len,
+                                   const int32_t* sel_idx, const int32_t* sel_cnt, float sm_scale, kvmm_bf16* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, int32_t* err,
+                                   kvmm_stream stream)
+{
+    kvmm_status st = check_shape(shape);
+    if (st != KVMM_OK) return st;
+    const kvmm_shape& s = *shape;
+    if (layer < 0 || layer >= s.L || n_max < 1 || !std::isfinite(sm_scale)) return KVMM_INVALID_ARG;
+    if (n_max > kvmm::kTreeMaxNodes) return KVMM_UNSUPPORTED_SHAPE;
+    if (!req(q) || !opt4(n_nodes) || !aligned(tree_mask, 8) || !req(k_pool) || !req(v_pool) || !req4(block_table) ||
+        !req4(seq_len) || !opt4(sel_idx) || !opt4(sel_cnt) || (sel_idx == nullptr) != (sel_cnt == nullptr) ||
+        !req(out) || !opt4(lse) || !req(workspace) || !opt4(err))
+        return KVMM_INVALID_ARG;
+    if (workspace_bytes < kvmm::tree_ws_bytes(s, n_max)) return KVMM_WORKSPACE_TOO_SMALL;
+    kvmm::TreeAttnParams p{};
+    p.B = s.B;
+    p.L = s.L;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.G = s.Hq / s.Hkv;
+    p.D = s.D;
+    p.T = s.T;
+    p.Pmax = s.Pmax;
+    p.Kmax = s.Kmax;
+    p.layer = layer;
+    p.n_max = n_max;
+    p.n_phys = s.n_phys;
+    p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(s.D))) * 1.4426950408889634f;
+    if (!std::isfinite(p.scale_log2)) return KVMM_INVALID_ARG;
+    p.q = q;
+    p.n_nodes = n_nodes;
+    p.tree_mask = tree_mask;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.block_table = block_table;
+    p.seq_len = seq_len;
+    p.sel_idx = sel_idx;
+    p.sel_cnt = sel_cnt;
+    p.out = out;
+    p.lse = lse;
+    p.workspace = workspace;
+    p.err = err;
+    return launched(kvmm::launch_tree_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvmm_status draft_verify(int32_t B, int32_t n_max, int32_t V, const float* target_probs, int64_t target_stride,
+                         const float* draft_probs, int64_t draft_stride, const int32_t* tokens,
+                         const int32_t* parent, const int32_t* n_nodes, const float* u_accept, const float* u_next,
+                         int32_t distinct, int32_t* path, int32_t* path_len, int32_t* out_tokens, int32_t* err,
+                         kvmm_stream stream)
+{
+    if (B < 1 || n_max < 1 || V < 1 || target_stride < V || (draft_probs != nullptr && draft_stride < V) ||
+        (distinct != 0 && distinct != 1))
+        return KVMM_INVALID_ARG;
+    const int64_t most = int64_t(1) << 40;
+    if (n_max > kvmm::kTreeMaxNodes || B > 65535 || target_stride > most ||
+        (draft_probs != nullptr && draft_stride > most))
+        return KVMM_UNSUPPORTED_SHAPE;
+    if (!req4(target_probs) || !opt4(draft_probs) || !req4(tokens) || !req4(parent) || !opt4(n_nodes) ||
+        !req4(u_accept) || !req4(u_next) || !req4(path) || !req4(path_len) || !req4(out_tokens) || !opt4(err))
+        return KVMM_INVALID_ARG;
+    kvmm::VerifyParams p{};
+    p.B = B;
+    p.n_max = n_max;
+    p.V = V;
+    p.distinct = distinct;
+    p.target_stride = target_stride;
+    p.draft_stride = draft_stride;
+    p.target = target_probs;
+    p.draft = draft_probs;
+    p.tokens = tokens;
+    p.parent = parent;
+    p.n_nodes = n_nodes;
+    p.u_accept = u_accept;
+    p.u_next = u_next;
+    p.path = path;
+    p.path_len = path_len;
+    p.out_tokens = out_tokens;
+    p.err = err;
+    return launched(kvmm::launch_draft_verify(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvmm_status kv_keep_path(const kvmm_shape* shape, int32_t layer, const int32_t* path, const int32_t* path_len,
+                         int32_t n_max, const int32_t* seq_len, kvmm_bf16* k_pool, kvmm_bf16* v_pool,
+                         const int32_t* block_table, kvmm_bf16* meta, int32_t* err, kvmm_stream stream)
+{
+    kvmm_status st = check_shape(shape);
+    if (st != KVMM_OK) return st;
+    const kvmm_shape& s = *shape;
+    if (layer < -1 || layer >= s.L || n_max < 1) return KVMM_INVALID_ARG;
+    if (n_max > kvmm::kTreeMaxNodes || static_cast<int64_t>(s.L) * s.Hkv > INT32_MAX) return KVMM_UNSUPPORTED_SHAPE;
+    if (!req4(path) || !req4(path_len) || !req4(seq_len) || !req(k_pool) || !req(v_pool) || !req4(block_table) ||
+        !opt(meta) || !opt4(err))
+        return KVMM_INVALID_ARG;
+    kvmm::KeepParams p{};
+    p.B = s.B;
+    p.L = s.L;
+    p.Hkv = s.Hkv;
+    p.D = s.D;
+    p.T = s.T;
+    p.Pmax = s.Pmax;
+    p.n_max = n_max;
+    p.layer0 = layer < 0 ? 0 : layer;
+    p.layers = layer < 0 ? s.L : 1;
+    p.n_phys = s.n_phys;
+    p.path = path;
+    p.path_len = path_len;
+    p.seq_len = seq_len;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.block_table = block_table;
+    p.meta = meta;
+    p.err = err;
+    return launched(kvmm::launch_keep_path(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

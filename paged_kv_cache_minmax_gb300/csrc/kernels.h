@@ -332,6 +332,63 @@ constexpr size_t kKv4CounterBytes = kKv4MaxCtas * sizeof(int32_t);
 __host__ __device__ constexpr size_t kv4_partial_floats(int D) { return size_t(8) * D + 16; }  // unnormalised output, then (m, l) of 8 heads
 inline size_t kv4_ws_bytes(int D) { return kKv4CounterBytes + size_t(kKv4MaxCtas) * 2 * kv4_partial_floats(D) * sizeof(float); }
 
+// sparse_paged_tree_attn (tree_attn.cu)
+constexpr int kTreeMaxNodes = 64;
+struct TreeAttnParams {
+    int32_t B, L, Hq, Hkv, G, D, T, Pmax, Kmax, layer, n_max;
+    int64_t n_phys;
+    float scale_log2;  // sm_scale * log2(e)
+    const kvmm_bf16* q;
+    const int32_t* n_nodes;     // or null: n_max
+    const uint64_t* tree_mask;  // or null: a chain
+    const kvmm_bf16* k_pool;
+    const kvmm_bf16* v_pool;
+    const int32_t* block_table;
+    const int32_t* seq_len;
+    const int32_t* sel_idx;  // null: every page
+    const int32_t* sel_cnt;
+    kvmm_bf16* out;
+    float* lse;
+    void* workspace;
+    int32_t* err;
+};
+size_t tree_ws_bytes(const kvmm_shape& s, int n_max);
+
+// draft_verify (draft_verify.cu)
+struct VerifyParams {
+    int32_t B, n_max, V, distinct;
+    int64_t target_stride, draft_stride;
+    const float* target;
+    const float* draft;  // or null
+    const int32_t* tokens;
+    const int32_t* parent;
+    const int32_t* n_nodes;  // or null: n_max
+    const float* u_accept;
+    const float* u_next;
+    int32_t* path;
+    int32_t* path_len;
+    int32_t* out_tokens;
+    int32_t* err;
+};
+
+// kv_keep_path (keep_path.cu)
+struct KeepParams {
+    int32_t B, L, Hkv, D, T, Pmax, n_max;
+    int32_t layer0, layers;  // the layers of the call
+    int64_t n_phys;
+    const int32_t* path;
+    const int32_t* path_len;
+    const int32_t* seq_len;
+    kvmm_bf16* k_pool;
+    kvmm_bf16* v_pool;
+    const int32_t* block_table;
+    kvmm_bf16* meta;  // or null
+    int32_t* err;
+};
+
+cudaError_t launch_tree_attention(const TreeAttnParams& p, cudaStream_t stream);
+cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t stream);
+cudaError_t launch_keep_path(const KeepParams& p, cudaStream_t stream);
 cudaError_t launch_append_rope(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_gather(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, cudaStream_t stream);

@@ -28,7 +28,8 @@ EXPORTS = ("kv_minmax_update", "page_score_topk", "sparse_paged_decode_attn", "t
            "topk_stability_rco", "promote_pages", "block_table_update", "kv_meankey_update",
            "page_score_topk_mean", "kv_centroid_build", "page_score_topk_centroid", "kv_append_rope",
            "kv4_append_rope", "kv4_gather", "sparse_paged_decode_attn_kv4", "kvmm_kv4_page_bytes",
-           "kvmm_kv4_workspace_size")
+           "kvmm_kv4_workspace_size", "sparse_paged_tree_attn", "draft_verify", "kv_keep_path",
+           "kvmm_tree_workspace_size")
 
 
 class KvmmError(RuntimeError):
@@ -149,7 +150,14 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kvmm_kv4_page_bytes.restype = SZ
     lib.kvmm_kv4_workspace_size.argtypes = [SP]
     lib.kvmm_kv4_workspace_size.restype = SZ
-    for f in ("kv_append_rope", "kv4_append_rope", "kv4_gather", "sparse_paged_decode_attn_kv4"):
+    I64 = ctypes.c_int64
+    lib.sparse_paged_tree_attn.argtypes = [SP, I32, P, I32, P, P, P, P, P, P, P, P, F32, P, P, P, SZ, P, P]
+    lib.draft_verify.argtypes = [I32, I32, I32, P, I64, P, I64, P, P, P, P, P, I32, P, P, P, P, P]
+    lib.kv_keep_path.argtypes = [SP, I32, P, P, I32, P, P, P, P, P, P, P]
+    lib.kvmm_tree_workspace_size.argtypes = [SP, I32]
+    lib.kvmm_tree_workspace_size.restype = SZ
+    for f in ("kv_append_rope", "kv4_append_rope", "kv4_gather", "sparse_paged_decode_attn_kv4",
+              "sparse_paged_tree_attn", "draft_verify", "kv_keep_path"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("kv_minmax_update", "page_score_topk", "sparse_paged_decode_attn", "topk_promotion_diff",
               "page_score_topk_static_scratch", "page_score_topk_attn", "decode_layer", "topk_history_record",
@@ -709,3 +717,131 @@ def sparse_paged_decode_attn_kv4(shape: Shape, layer: int, q, kv4_pool, block_ta
         _opt(lse, "lse", torch.float32, B * Hq, here), _arg(workspace, "workspace", torch.uint8, 0, here),
         workspace.numel(), EARLY_READS if early_reads else 0, _opt(err, "err", torch.int32, 1, here), st)
     _check("sparse_paged_decode_attn_kv4", status)
+
+
+# --------------------------------------------------------------------------- #
+def tree_workspace_size(shape: Shape, n_max: int) -> int:
+    return int(load().kvmm_tree_workspace_size(ctypes.byref(shape), n_max))
+
+
+def alloc_tree_workspace(shape: Shape, n_max: int, device="cuda") -> torch.Tensor:
+    """A workspace (uint8) for sparse_paged_tree_attn with up to ``n_max`` nodes a sequence."""
+    n = tree_workspace_size(shape, n_max)
+    if n == 0:
+        raise KvmmError("kvmm_tree_workspace_size", UNSUPPORTED_SHAPE)
+    return torch.empty((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def tree_masks(parent: torch.Tensor) -> torch.Tensor:
+    """The tree_mask [B, n] (int64, bit j of node i: i sees j) in which every node sees itself and its ancestors, from
+    parent [B, n] (node 0 is the root; parent[:, i] < i).  A launch for each node: for trees that are kept."""
+    if parent.dim() != 2 or not 1 <= parent.shape[1] <= 64:
+        raise ValueError(f"parent must be [B, n] with 1 <= n <= 64, got {tuple(parent.shape)}")
+    n = parent.shape[1]
+    up = parent.long().clamp(min=0)
+    bits = torch.zeros(parent.shape, dtype=torch.int64, device=parent.device)
+    for i in range(n):
+        own = 1 << i if i < 63 else -(1 << 63)
+        bits[:, i] = bits.gather(1, up[:, i:i + 1]).squeeze(1) | own if i else own
+    return bits
+
+
+def _int_rows(t: torch.Tensor, name: str, B: int, n: int, here: int) -> int:
+    """A dense [B, n] int32 tensor."""
+    if t is None or t.shape != (B, n):
+        raise ValueError(f"{name} must be [{B}, {n}], got {None if t is None else list(t.shape)}")
+    return _arg(t, name, torch.int32, B * n, here)
+
+
+def sparse_paged_tree_attn(shape: Shape, layer: int, q, k_pool, v_pool, block_table, seq_len, out, workspace,
+                           n_nodes=None, tree_mask=None, sel_idx=None, sel_cnt=None, lse=None, err=None,
+                           sm_scale: float = 0.0, stream=None) -> None:
+    """Attention of a tree of n nodes a sequence (q, out [B, n, Hq, D] bf16, lse [B, n, Hq]): each node over the settled
+    tokens of the selected pages (every page with sel_idx and sel_cnt None) and over the nodes that tree_mask [B, n]
+    int64 shows it (``tree_masks``; None: a chain).  The nodes stand at the tokens seq_len + i.  workspace:
+    alloc_tree_workspace; calls that may run at once need one each."""
+    B, L, Hq, Hkv, D, T, Pmax, Kmax, n_phys = _fields(shape)
+    if (sel_idx is None) != (sel_cnt is None):
+        raise ValueError("sel_idx and sel_cnt are given together or not at all")
+    n = q.shape[1] if q.dim() == 4 else -1
+    for t, name in ((q, "q"), (out, "out")):
+        if t.shape != (B, n, Hq, D):
+            raise ValueError(f"{name} must be [{B}, n, {Hq}, {D}], got {list(t.shape)}")
+    if lse is not None and lse.shape != (B, n, Hq):
+        raise ValueError(f"lse must be [{B}, {n}, {Hq}], got {list(lse.shape)}")
+    if tree_mask is not None and tree_mask.shape != (B, n):
+        raise ValueError(f"tree_mask must be [{B}, {n}], got {list(tree_mask.shape)}")
+    here, st = _here(stream)
+    units = B * L * Hkv
+    status = load().sparse_paged_tree_attn(
+        ctypes.byref(shape), layer, _arg(q, "q", torch.bfloat16, 0, here), n,
+        _opt(n_nodes, "n_nodes", torch.int32, B, here), _opt(tree_mask, "tree_mask", torch.int64, 0, here),
+        _arg(k_pool, "k_pool", torch.bfloat16, n_phys * T * D, here),
+        _arg(v_pool, "v_pool", torch.bfloat16, n_phys * T * D, here),
+        _arg(block_table, "block_table", torch.int32, units * Pmax, here),
+        _arg(seq_len, "seq_len", torch.int32, B, here), _opt(sel_idx, "sel_idx", torch.int32, units * Kmax, here),
+        _opt(sel_cnt, "sel_cnt", torch.int32, units, here), sm_scale, _arg(out, "out", torch.bfloat16, 0, here),
+        _opt(lse, "lse", torch.float32, 0, here), _arg(workspace, "workspace", torch.uint8, 0, here),
+        workspace.numel(), _opt(err, "err", torch.int32, 1, here), st)
+    _check("sparse_paged_tree_attn", status)
+
+
+def _prob_rows(t: torch.Tensor, name: str, B: int, n: int, V: int, here: int) -> tuple[int, int]:
+    """The address of [B, n, V] float rows a constant step apart, and that step."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on {t.device}, the call on cuda:{here}")
+    if t.dtype is not torch.float32:
+        raise ValueError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if t.shape != (B, n, V):
+        raise ValueError(f"{name} must be {(B, n, V)}, got {tuple(t.shape)}")
+    sb, sn, sv = t.stride()
+    step = sn if n > 1 else sb if B > 1 else V  # an axis of one entry has no step: its stride may be anything
+    if (sv != 1 and V > 1) or (n > 1 and B > 1 and sb != n * sn) or step < V:
+        raise ValueError(f"{name}: the probabilities of a row must be consecutive and the rows evenly spaced")
+    return t.data_ptr(), step
+
+
+def draft_verify(target_probs, tokens, parent, u_accept, u_next, path, path_len, out_tokens, draft_probs=None,
+                 n_nodes=None, distinct: bool = False, err=None, stream=None) -> None:
+    """Walk each sequence's tree along accepted nodes and draw the token behind them (see kvmm.h for the rule).
+
+    target_probs, draft_probs [B, n, V] float32 (rows may be padded; draft_probs None: candidates proposed with
+    certainty); tokens, parent [B, n] int32; u_accept [B, n], u_next [B] float32 in [0, 1); path, out_tokens [B, n] and
+    path_len [B] int32 are written.  ``distinct``: a node's children were drawn without replacement."""
+    if target_probs.dim() != 3:
+        raise ValueError(f"target_probs must be [B, n, V], got {list(target_probs.shape)}")
+    B, n, V = target_probs.shape
+    here, st = _here(stream)
+    target, tstep = _prob_rows(target_probs, "target_probs", B, n, V, here)
+    draft, dstep = (None, 0) if draft_probs is None else _prob_rows(draft_probs, "draft_probs", B, n, V, here)
+    if u_accept.shape != (B, n):
+        raise ValueError(f"u_accept must be [{B}, {n}], got {list(u_accept.shape)}")
+    status = load().draft_verify(
+        B, n, V, target, tstep, draft, dstep, _int_rows(tokens, "tokens", B, n, here),
+        _int_rows(parent, "parent", B, n, here), _opt(n_nodes, "n_nodes", torch.int32, B, here),
+        _arg(u_accept, "u_accept", torch.float32, 0, here), _arg(u_next, "u_next", torch.float32, B, here),
+        int(bool(distinct)), _int_rows(path, "path", B, n, here), _arg(path_len, "path_len", torch.int32, B, here),
+        _int_rows(out_tokens, "out_tokens", B, n, here), _opt(err, "err", torch.int32, 1, here), st)
+    _check("draft_verify", status)
+
+
+def kv_keep_path(shape: Shape, layer: int, path, path_len, seq_len, k_pool, v_pool, block_table, meta=None, err=None,
+                 stream=None) -> None:
+    """Move the rows of the accepted nodes path [B, n] (path_len [B] of them) to the tokens seq_len + 0, 1, .. and take
+    the MinMax of the pages there again, in ``layer`` or, with -1, in every layer.  seq_len stays as it was."""
+    B, L, _, Hkv, D, T, Pmax, _, n_phys = _fields(shape)
+    if path.dim() != 2:
+        raise ValueError(f"path must be [{B}, n], got {list(path.shape)}")
+    n = path.shape[1]
+    here, st = _here(stream)
+    pages = B * L * Hkv * Pmax
+    status = load().kv_keep_path(
+        ctypes.byref(shape), layer, _int_rows(path, "path", B, n, here),
+        _arg(path_len, "path_len", torch.int32, B, here), n, _arg(seq_len, "seq_len", torch.int32, B, here),
+        _arg(k_pool, "k_pool", torch.bfloat16, n_phys * T * D, here),
+        _arg(v_pool, "v_pool", torch.bfloat16, n_phys * T * D, here),
+        _arg(block_table, "block_table", torch.int32, pages, here),
+        _opt(meta, "meta", torch.bfloat16, pages * 2 * D, here), _opt(err, "err", torch.int32, 1, here), st)
+    _check("kv_keep_path", status)

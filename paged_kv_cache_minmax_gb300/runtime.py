@@ -12,6 +12,7 @@ layer and step, the calls in the method's order:
 
 or, with steps 2 and 4 in one launch, ``page_score_topk_attn`` then the diff.
 From a projection's unrotated rows, step 1 is ``kv_append_rope``.
+:class:`TreeDecode` takes steps of several drafted tokens a sequence (speculative decoding) over such a state.
 :class:`Kv4DecodeState` is the same over a cache held in 4 bits.
 
 (FlexiCache, "Core method", sections 1-3.)  Everything runs on one CUDA
@@ -149,6 +150,78 @@ class DecodeState(_StepState):
         self.append_rope(layer, q, new_k, new_v, rope)
         self.select_attend(layer, self.q_turned[layer], rescore_mask)
         self.diff(layer, rescore_mask)
+
+
+class TreeDecode:
+    """Speculative decoding over a :class:`DecodeState`: each step hands every sequence a tree of up to ``n_max`` nodes,
+    node 0 the token sampled last and the others drafted.  Between steps ``state.seq_len`` counts the settled tokens,
+    which do not include node 0.  A step is ``begin``, ``layer_step`` for every layer, ``verify`` with the target's
+    probabilities, ``keep``; ``out_tokens[:, path_len - 1]`` are the next roots.
+
+    ``parent`` [B, n_max] int32 gives the trees (see ``kvmm.draft_verify``); they may be replaced with ``set_trees``."""
+
+    def __init__(self, state: DecodeState, parent: torch.Tensor, rope: kvmm.Rope | None = None):
+        s = state.shape
+        n = parent.shape[1]
+        dev = state.seq_len.device
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.state, self.n_max = state, n
+        self.q_turned = torch.zeros(s.L, s.B, n, s.Hq, s.D, dtype=torch.bfloat16, device=dev)
+        self.root_q = torch.zeros(s.B, s.Hq, s.D, dtype=torch.bfloat16, device=dev)
+        self.out = torch.zeros(s.L, s.B, n, s.Hq, s.D, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.zeros(s.L, s.B, n, s.Hq, dtype=torch.float32, device=dev)
+        self.path, self.out_tokens = torch.zeros(s.B, n, **i32), torch.zeros(s.B, n, **i32)
+        self.path_len = torch.zeros(s.B, **i32)
+        self.n_nodes, self.tok_end = torch.full((s.B,), n, **i32), torch.zeros(s.B, **i32)
+        self.positions = torch.zeros(s.B, n, **i32)
+        self.workspace = kvmm.alloc_tree_workspace(s, n, device=dev)
+        self.rope = None if rope is None else kvmm.Rope(rope.table, rope.dim, bool(rope.c.interleaved), self.positions)
+        self.set_trees(parent)
+
+    def set_trees(self, parent: torch.Tensor) -> None:
+        """The trees of the following steps."""
+        self.parent = parent.to(torch.int32).contiguous()
+        self.mask = kvmm.tree_masks(self.parent)
+        j = torch.arange(self.n_max, device=parent.device)
+        self.depth = ((self.mask.unsqueeze(-1) >> j) & 1).sum(-1).sub_(1).to(torch.int32)
+
+    def begin(self, n_nodes: torch.Tensor | None = None) -> None:
+        """Start a step; ``n_nodes`` [B] int32: the nodes of each tree that exist (default: all)."""
+        if n_nodes is None:
+            self.n_nodes.fill_(self.n_max)
+        else:
+            self.n_nodes.copy_(n_nodes)
+        torch.add(self.state.seq_len, self.n_nodes, out=self.tok_end)
+        torch.add(self.state.seq_len.unsqueeze(1), self.depth, out=self.positions)
+
+    def layer_step(self, layer, q, new_k, new_v, rescore_mask=None, every_page=False, sm_scale=0.0) -> None:
+        """One layer: the nodes' rows q [B, n_max, Hq, D], new_k and new_v [B, n_max, Hkv, D] (bf16 views) rotated and
+        appended, pages selected by the roots' queries, every node attended."""
+        st, qt = self.state, self.q_turned[layer]
+        kvmm.kv_append_rope(st.shape, layer, q, new_k, new_v, st.seq_len, self.tok_end, st.k_pool, st.v_pool,
+                            st.block_table, None, rope=self.rope, q_out=qt, err=st.err)
+        if not every_page:
+            self.root_q.copy_(qt[:, 0])
+            st.select(layer, self.root_q, rescore_mask)
+            st.diff(layer, rescore_mask)
+        kvmm.sparse_paged_tree_attn(st.shape, layer, qt, st.k_pool, st.v_pool, st.block_table, st.seq_len,
+                                    self.out[layer], self.workspace, n_nodes=self.n_nodes, tree_mask=self.mask,
+                                    sel_idx=None if every_page else st.sel_idx,
+                                    sel_cnt=None if every_page else st.sel_cnt, lse=self.lse[layer], err=st.err,
+                                    sm_scale=sm_scale)
+
+    def verify(self, target_probs, tokens, u_accept, u_next, draft_probs=None, distinct=False) -> None:
+        """Accept a path and draw the token behind it (``path``, ``path_len``, ``out_tokens``)."""
+        kvmm.draft_verify(target_probs, tokens, self.parent, u_accept, u_next, self.path, self.path_len,
+                          self.out_tokens, draft_probs=draft_probs, n_nodes=self.n_nodes, distinct=distinct,
+                          err=self.state.err)
+
+    def keep(self) -> None:
+        """Settle the accepted nodes in every layer."""
+        st = self.state
+        kvmm.kv_keep_path(st.shape, -1, self.path, self.path_len, st.seq_len, st.k_pool, st.v_pool, st.block_table,
+                          st.meta, err=st.err)
+        st.seq_len.add_(self.path_len)
 
 
 class Kv4DecodeState(_StepState):
