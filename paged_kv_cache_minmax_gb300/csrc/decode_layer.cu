@@ -180,11 +180,9 @@ DecodeGrid decode_layer_grid(const kvmm_shape& s, int ph)
     return g;
 }
 
-// The tensor map of the metadata for the score items' tensor copies: a 3-D tensor of 16-bit elements,
-// {64 (one 128-byte line), 2D / 64 lines of a [min | max] row, B * L * Hkv * Pmax rows}, read in boxes of
-// {64, 2D / 64, 16 rows} with the 128-byte swizzle; rows past the end read as zeros.  The encoder is the
-// driver's, reached through the runtime.
-static cudaError_t meta_tensor_map(CUtensorMap* m, const DecodeParams& p)
+// A 3-D tensor map of 16-bit elements over a dense array.  The encoder is the driver's, reached through the runtime.
+cudaError_t tensor_map_3d(CUtensorMap* m, const void* data, uint64_t inner, uint64_t mid, uint64_t outer, uint32_t box0,
+                          uint32_t box1, CUtensorMapSwizzle swizzle, uint32_t box2)
 {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
@@ -197,16 +195,24 @@ static cudaError_t meta_tensor_map(CUtensorMap* m, const DecodeParams& p)
             encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
     if (encode == nullptr) return cudaErrorNotSupported;
-    const cuuint64_t lines = static_cast<cuuint64_t>(2 * p.D / 64);
-    const cuuint64_t rows = static_cast<cuuint64_t>(p.B) * p.L * p.Hkv * p.Pmax;
-    const cuuint64_t dims[3] = {64, lines, rows};
-    const cuuint64_t strides[2] = {128, lines * 128};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(lines), 16};
+    const cuuint64_t dims[3] = {inner, mid, outer};
+    const cuuint64_t strides[2] = {inner * 2, inner * mid * 2};
+    const cuuint32_t box[3] = {box0, box1, box2};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, p.meta, dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(data), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The tensor map of the metadata for the score items' tensor copies: {64 (one 128-byte line), 2D / 64 lines of a
+// [min | max] row, B * L * Hkv * Pmax rows}, read in boxes of {64, 2D / 64, 16 rows} with the 128-byte swizzle; rows past
+// the end read as zeros.
+static cudaError_t meta_tensor_map(CUtensorMap* m, const DecodeParams& p)
+{
+    const uint32_t lines = static_cast<uint32_t>(2 * p.D / 64);
+    const uint64_t rows = static_cast<uint64_t>(p.B) * p.L * p.Hkv * p.Pmax;
+    return tensor_map_3d(m, p.meta, 64, lines, rows, 64, lines, CU_TENSOR_MAP_SWIZZLE_128B, 16);
 }
 
 cudaError_t launch_decode_layer(DecodeParams p, int group_reduce, int ph, cudaStream_t stream)

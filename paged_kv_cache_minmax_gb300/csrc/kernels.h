@@ -334,6 +334,7 @@ inline size_t kv4_ws_bytes(int D) { return kKv4CounterBytes + size_t(kKv4MaxCtas
 
 // sparse_paged_tree_attn (tree_attn.cu)
 constexpr int kTreeMaxNodes = 64;
+constexpr int kTreeMaxCtas = 160;  // CTAs of one launch: each may leave two parts of units in the workspace
 struct TreeAttnParams {
     int32_t B, L, Hq, Hkv, G, D, T, Pmax, Kmax, layer, n_max;
     int64_t n_phys;
@@ -402,6 +403,9 @@ cudaError_t launch_meankey(const MeanParams& p, cudaStream_t stream);
 cudaError_t launch_history_record(const StabilityParams& p, cudaStream_t stream);
 cudaError_t launch_stability_rco(const StabilityParams& p, cudaStream_t stream);
 size_t stability_max_heads();  // largest L * Hkv the classification handles
+// A tensor map of 16-bit elements {inner, mid, outer}, dense, read in boxes of {box0, box1, 1} (decode_layer.cu)
+cudaError_t tensor_map_3d(CUtensorMap* m, const void* data, uint64_t inner, uint64_t mid, uint64_t outer, uint32_t box0,
+                          uint32_t box1, CUtensorMapSwizzle swizzle, uint32_t box2 = 1);
 // The phases a launch of the decode kernel runs: decode_layer runs both; page_score_topk runs the first
 // alone (score and select), sparse_paged_decode_attn the second (attend over kept selections).
 constexpr int kPhScore = 1;   // score every page of the rescored units, select their top K

@@ -1,111 +1,804 @@
 // tree_attn.cu -- attention of a tree of drafted tokens over the paged cache.
 //
-// A warp takes one query row (a node's head): its lanes hold the row's
-// channels, and it walks the pages with a running maximum and sum.
-#include "common.cuh"
+// The query rows of one (batch, KV head), nodes x heads of the group, are the
+// M axis of the tensor cores: tiles of 128 rows against blocks of 128 tokens,
+//     S = Q K^T      [128 x 128], fp32 in tensor memory
+//     P = exp2(S - m), rounded to bf16, written over S in tensor memory
+//     O += P V       [128 x D], fp32 in tensor memory
+// with m a running reference of each row: it moves, and O and the sum are
+// rescaled, only when a score passes it by 2^8, so weights stay below 2^8.
+//
+// The pages are in the form the tensor cores take: a key page [T][D] is T
+// K-major rows of Q K^T's second operand, a value page [D][T] D K-major rows
+// of P V's, each 16 tokens wide or twice that.  TMA copies them with the
+// swizzle of their rows (128 bytes for keys, 32 or 64 for values).
+//
+// A CTA's warps: two groups of four for the softmax of two streams (a thread a
+// row), one that copies, one that issues the products.  The streams alternate
+// on the tensor cores: two row tiles over the same blocks, or, with at most
+// 128 rows, one tile over every other block, joined at the end from tensor
+// memory.
+//
+// The blocks of all units are dealt evenly to one CTA an SM.  A unit that
+// falls on several CTAs leaves parts in the workspace, which a second launch
+// joins.
+#include <cstdint>
+
 #include "kernels.h"
+#include "tcgen05.cuh"
 
 namespace kvmm {
 namespace {
 
-constexpr int kTreeWarps = 8;
+constexpr int kThreads = 320;    // 8 softmax warps, the copying warp, the issuing warp
+constexpr int kTokens = 128;     // tokens of a block
+constexpr int kRing = 8;         // blocks whose masks are held (see copy_pages)
+constexpr int kNoNode = 1 << 20; // an entry that holds no node
+constexpr int kUnitsAtOnce = 2048;
+
+struct Launch {
+    TreeAttnParams p;
+    int b0, nb;      // batch entries of this launch
+    int tiles;       // row tiles of a unit: 1 or 2
+    int groups;      // units of one (batch, KV head)
+    int units;       // nb * Hkv * groups
+    int tile_rows;   // rows of a tile in the workspace
+    int2* parts;     // of each unit: its first and last CTA; first -1: it was written whole, -2: it has no block
+    float2* ml;      // [2 * CTAs][tiles][tile_rows] reference and sum
+    float* o;        // [2 * CTAs][tiles][tile_rows][D]
+};
+
+struct Unit {
+    int b, h;
+    int seq, held;         // settled tokens, nodes with a place
+    int row0, rows;        // rows of the unit among the nodes' rows
+    int listed, entries;   // pages of settled tokens, all pages
+    int blocks;
+    size_t index;          // of the (batch, layer, KV head)
+};
+
+template <int T>
+__device__ __forceinline__ Unit unit_of(const Launch& a, int w, bool tell)
+{
+    const TreeAttnParams& p = a.p;
+    Unit u;
+    const int g = w % a.groups, bh = w / a.groups;
+    u.h = bh % p.Hkv;
+    u.b = a.b0 + bh / p.Hkv;
+    u.index = (static_cast<size_t>(u.b) * p.L + p.layer) * p.Hkv + u.h;
+    const int cap = p.Pmax * T;
+    int n = p.n_nodes != nullptr ? p.n_nodes[u.b] : p.n_max;
+    int cnt = p.sel_idx != nullptr ? p.sel_cnt[u.index] : 0;
+    u.seq = p.seq_len[u.b];
+    bool bad = u.seq < 0 || u.seq > cap || n < 0 || n > p.n_max || cnt < 0 || cnt > p.Kmax;
+    u.seq = min(max(u.seq, 0), cap);
+    n = min(max(n, 0), p.n_max);
+    cnt = min(max(cnt, 0), p.Kmax);
+    u.held = min(n, cap - u.seq);
+    bad |= u.held < n;
+    if (tell && bad) report(p.err, KVMM_ERR_OUT_OF_RANGE);
+    u.row0 = g * a.tiles * 128;
+    u.rows = min(max(n * p.G - u.row0, 0), a.tiles * 128);
+    if (p.sel_idx != nullptr) {
+        u.listed = cnt;
+        u.entries = cnt + (u.held > 0 ? (u.seq + u.held - 1) / T - u.seq / T + 1 : 0);
+    } else {
+        u.listed = u.entries = (u.seq + u.held + T - 1) / T;
+    }
+    u.blocks = u.rows > 0 ? (u.entries * T + kTokens - 1) / kTokens : 0;
+    return u;
+}
+
+// what a block shows: for each of its pages the slots of settled tokens, and the node in its first slot
+struct BlockMask {
+    uint32_t settled[kTokens / 16];
+    int32_t node0[kTokens / 16];
+    int32_t whole;  // every slot is a settled token's
+    int32_t held;   // nodes of the sequence
+};
+
+struct Control {
+    uint64_t full[10], empty[10], s_full[2], p_ready[2], q_ready[2], o_done[2], meet, drain;
+    uint32_t tmem;
+    int32_t gave_up;
+    int32_t w0, off0, total;
+    int32_t sums[kThreads / 32];
+    BlockMask mask[kRing];
+    float2 ml[2][128];
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kTile = 128 * D * 2;  // a tile of queries, a block of keys or of values
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kControl = (2 + kStages) * kTile;
+    static constexpr size_t kBytes = kControl + sizeof(Control);
+};
+static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory of a CTA");
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// wait for the phase; false once any warp of the CTA has given up
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int32_t* gave_up)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t spin = 0;; ++spin) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((spin & 63u) != 63u) continue;
+        if (*gave_up != 0) return false;
+        if (global_timer_ns() - t0 > 1000000000ull) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+}
+
+// the CTA's run of blocks, piece by piece (a piece: blocks of one unit)
+struct Walk {
+    int w, off, left;  // unit, its next block, blocks of the run to come
+};
+template <int T>
+__device__ __forceinline__ bool next_piece(const Launch& a, Walk& k, Unit& u, int& begin, int& count)
+{
+    if (k.left <= 0) return false;
+    for (;; ++k.w, k.off = 0) {
+        if (k.w >= a.units) return false;
+        u = unit_of<T>(a, k.w, false);
+        if (u.blocks > k.off) break;
+    }
+    begin = k.off;
+    count = min(u.blocks - k.off, k.left);
+    k.off += count;
+    k.left -= count;
+    return true;
+}
+
+// ---- the copying warp -------------------------------------------------------------
+template <int D, int T>
+__device__ void copy_pages(const Launch& a, const CUtensorMap* kmap, const CUtensorMap* vmap, uint8_t* smem, Control& c, Walk k)
+{
+    using S = Smem<D>;
+    constexpr int kPages = kTokens / T;        // pages of a block
+    constexpr int kBlocks = 32 / kPages;       // blocks whose pages the lanes look up at once
+    constexpr uint32_t kPageBytes = T * D * 2;
+    const int lane = threadIdx.x & 31, mine = lane % kPages;
+    const TreeAttnParams& p = a.p;
+    uint8_t* ring = smem + 2 * S::kTile;
+    const uint64_t policy = l2_policy_evict_first();
+    uint32_t item = 0, nth = 0;
+    bool fine = true;
+    Unit u;
+    int begin, count;
+    while (fine && next_piece<T>(a, k, u, begin, count)) {
+        const int32_t* table = p.block_table + u.index * p.Pmax;
+        const int32_t* sel = p.sel_idx != nullptr ? p.sel_idx + u.index * p.Kmax : nullptr;
+        const int pages = (u.seq + T - 1) / T, first = u.seq / T;
+        for (int b0 = 0; fine && b0 < count; b0 += kBlocks) {
+            // the lane's page: entry e of the unit
+            const int e = (begin + b0) * kPages + lane;
+            int page = -1;
+            bool old = false, young = false;
+            if (b0 + lane / kPages < count && e < u.entries) {
+                old = e < u.listed;
+                young = sel == nullptr || !old;
+                page = !old ? first + e - u.listed : sel != nullptr ? sel[e] : e;
+                if (sel != nullptr && old && (page < 0 || page >= pages)) {
+                    report(p.err, KVMM_ERR_OUT_OF_RANGE);
+                    page = -1;
+                }
+            }
+            int32_t phys = -1;
+            if (page >= 0) {
+                phys = table[page];
+                if (phys < 0 || phys >= p.n_phys) {
+                    report(p.err, phys < 0 ? KVMM_ERR_NULL_BLOCK : KVMM_ERR_OUT_OF_RANGE);
+                    phys = -1;
+                }
+            }
+            uint32_t settled = 0;
+            int node0 = kNoNode;
+            if (phys >= 0) {
+                const int s = u.seq - page * T;  // settled slots of the page, when listed for them
+                if (old && s > 0) settled = s >= T ? 0xffffffffu >> (32 - T) : (1u << s) - 1;
+                if (young && -s < u.held && T - s > 0) node0 = -s;
+            }
+            const uint32_t some = __ballot_sync(kFullMask, phys >= 0);
+            const uint32_t all = __ballot_sync(kFullMask, settled == 0xffffffffu >> (32 - T));
+            const int blocks = min(kBlocks, count - b0);
+            for (int j = 0; j < blocks; ++j) {
+                const uint32_t lanes = (kPages == 32 ? kFullMask : (1u << kPages) - 1) << (j * kPages);
+                const bool on = lane / kPages == j;
+                const uint32_t bytes = __popc(some & lanes) * kPageBytes;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++item) {
+                    const uint32_t slot = item % S::kStages;
+                    fine = wait_for(&c.empty[slot], (item / S::kStages & 1) ^ 1, &c.gave_up);
+                    fine = __all_sync(kFullMask, fine);
+                    if (!fine) break;
+                    if (kv == 0) {
+                        // The slot was freed by the products of item 2 nth - kStages, which are issued after P V of
+                        // block nth - kRing: nobody reads that block's masks any more.
+                        BlockMask& m = c.mask[nth % kRing];
+                        if (on) {
+                            m.settled[mine] = settled;
+                            m.node0[mine] = node0;
+                        }
+                        if (lane == 0) {
+                            m.whole = (all & lanes) == lanes;
+                            m.held = u.held;
+                        }
+                        ++nth;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(&c.full[slot], bytes);
+                    __syncwarp();
+                    if (on && phys >= 0) {
+                        uint8_t* dst = ring + slot * S::kTile;
+                        if (kv == 0) {
+#pragma unroll
+                            for (int half = 0; half < D / 64; ++half)
+                                tma_load_3d_hint(dst + half * (kTokens * 128) + mine * (T * 128), kmap, half * 64, 0, phys,
+                                                 &c.full[slot], policy);
+                        } else {
+                            tma_load_3d_hint(dst + mine * kPageBytes, vmap, 0, 0, phys, &c.full[slot], policy);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!fine) break;
+            }
+        }
+    }
+    if (!fine) {  // the copies in flight land before the CTA ends
+        const uint32_t n = min(item, static_cast<uint32_t>(S::kStages));
+        for (uint32_t i = item - n; i < item; ++i)
+            mbar_wait_bounded(&c.full[i % S::kStages], i / S::kStages & 1);
+    }
+}
+
+// ---- the issuing warp -------------------------------------------------------------
+// Slots of a block's values that nothing shows are set to zero: whatever they hold, NaN included, would meet a weight of 0.
+template <int D, int T>
+__device__ __forceinline__ void clear_unseen(uint8_t* values, const BlockMask& m)
+{
+    constexpr int kPages = kTokens / T, kChunks = T / 8;
+    const int lane = threadIdx.x & 31;
+    for (int i = 0; i < kPages; ++i) {
+        uint32_t seen = m.settled[i];
+        for (int t = 0; t < T; ++t) {
+            const int j = m.node0[i] + t;
+            if (j >= 0 && j < m.held) seen |= 1u << t;
+        }
+        if (seen == 0xffffffffu >> (32 - T)) continue;
+        for (int x = lane; x < D * kChunks; x += 32) {
+            const int d = x / kChunks, ch = x % kChunks;
+            const uint32_t bits = seen >> (8 * ch) & 255u;
+            if (bits == 255u) continue;
+            const int at = T == 16 ? ch ^ (d >> 2 & 1) : ch ^ (d >> 1 & 3);
+            uint4* q = reinterpret_cast<uint4*>(values + i * (T * D * 2) + d * (T * 2) + at * 16);
+            uint4 v = *q;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                w[s] &= (bits >> (2 * s) & 1 ? 0xffffu : 0u) | (bits >> (2 * s + 1) & 1 ? 0xffff0000u : 0u);
+            *q = v;
+        }
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+}
 
 template <int D, int T>
-__global__ void __launch_bounds__(kTreeWarps * 32) tree_attn_kernel(const TreeAttnParams p)
+__device__ void issue_products(const Launch& a, uint8_t* smem, Control& c, Walk k)
 {
-    constexpr int C = D / 32;  // channels of a lane: lane, lane + 32, ..
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y, b = blockIdx.z;
+    using S = Smem<D>;
+    constexpr uint64_t rows128 = matrix_desc(128), rowsT = matrix_desc(T * 2);
+    constexpr uint32_t qk = mma_desc(128, kTokens), pv = mma_desc(128, D);
+    const int lane = threadIdx.x & 31;
+    const uint32_t ring = smem_addr(smem) + 2 * S::kTile, tmem = c.tmem;
+    const bool two = a.tiles == 2;
+    uint32_t item = 0, piece = 0, nth = 0, p_phase[2] = {0, 0};
+    bool fine = true;
+    Unit u;
+    int begin, count;
+    while (fine && next_piece<T>(a, k, u, begin, count)) {
+        fine = wait_for(&c.q_ready[0], piece & 1, &c.gave_up) && wait_for(&c.q_ready[1], piece & 1, &c.gave_up);
+        fine = __all_sync(kFullMask, fine);
+        ++piece;
+        const int steps = two ? 2 * count : count;
+        auto scores = [&](int v) {  // S = Q K^T of step v
+            const int s = v & 1, blk = two ? v >> 1 : v;
+            const uint32_t it = item + 2 * blk, slot = it % S::kStages;
+            if (!two || s == 0) fine = fine && wait_for(&c.full[slot], it / S::kStages & 1, &c.gave_up);
+            fine = __all_sync(kFullMask, fine);
+            if (!fine) return;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t q = matrix_at(rows128, smem_addr(smem) + s * S::kTile), kk = matrix_at(rows128, ring + slot * S::kTile);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t off = ((i / 4) * (128 * 128) + (i % 4) * 32) >> 4;
+                    mma_ss(tmem + s * 128, q + off, kk + off, qk, i > 0);
+                }
+                if (!two || s == 1) mma_commit(&c.empty[slot]);
+                mma_commit(&c.s_full[s]);
+            }
+            __syncwarp();
+        };
+        auto values = [&](int v) {  // O += P V of step v
+            const int s = v & 1, blk = two ? v >> 1 : v;
+            const uint32_t it = item + 2 * blk + 1, slot = it % S::kStages;
+            if (!two || s == 0) {
+                fine = fine && wait_for(&c.full[slot], it / S::kStages & 1, &c.gave_up);
+                fine = __all_sync(kFullMask, fine);
+                if (!fine) return;
+                const BlockMask& m = c.mask[(nth + blk) % kRing];
+                if (!m.whole) clear_unseen<D, T>(smem + 2 * S::kTile + slot * S::kTile, m);
+            }
+            fine = fine && wait_for(&c.p_ready[s], p_phase[s] & 1, &c.gave_up);
+            ++p_phase[s];
+            fine = __all_sync(kFullMask, fine);
+            if (!fine) return;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t vv = matrix_at(rowsT, ring + slot * S::kTile);
+                const bool later = v > 1;  // the stream has had a step of this piece
+#pragma unroll
+                for (int i = 0; i < kTokens / 16; ++i) {
+                    const uint32_t off = ((i * 16 / T) * (T * D * 2) + (i * 16 % T) * 2) >> 4;
+                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, vv + off, pv, later || i > 0);
+                }
+                if (!two || s == 1) mma_commit(&c.empty[slot]);
+                if (v + 2 >= steps) mma_commit(&c.o_done[s]);
+            }
+            __syncwarp();
+        };
+        if (fine) scores(0);
+        for (int v = 0; fine && v < steps; ++v) {
+            if (v + 1 < steps) scores(v + 1);
+            if (fine) values(v);
+        }
+        item += 2 * count;
+        nth += count;
+    }
+    if (!fine) {  // products in flight end before the CTA does
+        if (lane == 0) mma_commit(&c.drain);
+        mbar_wait_bounded(&c.drain, 0);
+    }
+}
+
+// ---- a softmax group: the 128 threads of a stream, a row each ------------------------
+// both groups arrive and wait; false once any warp of the CTA has given up
+__device__ __forceinline__ bool groups_meet(Control& c, uint32_t& phase)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&c.meet);
+    const bool fine = wait_for(&c.meet, phase & 1, &c.gave_up);
+    ++phase;
+    return __all_sync(kFullMask, fine);
+}
+
+// the group's tile of queries, rows that do not exist as zeros
+template <int D>
+__device__ __forceinline__ void load_queries(const TreeAttnParams& p, const Unit& u, int row0, uint8_t* tile)
+{
+    const int t = threadIdx.x & 127;
+#pragma unroll 4
+    for (int x = t; x < 128 * (D / 8); x += 128) {
+        const int r = x / (D / 8), ch = x % (D / 8), row = row0 + r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < u.row0 + u.rows) {
+            const int i = row / p.G, g = row - i * p.G;
+            v = reinterpret_cast<const uint4*>(
+                p.q + ((static_cast<size_t>(u.b) * p.n_max + i) * p.Hq + u.h * p.G + g) * D)[ch];
+        }
+        *reinterpret_cast<uint4*>(tile + (ch / 8) * (128 * 128) + r * 128 + ((ch % 8 ^ (r & 7)) << 4)) = v;
+    }
+    fence_proxy_async_shared();
+}
+
+__device__ __forceinline__ size_t row_of(const TreeAttnParams& p, const Unit& u, int row)
+{
+    const int i = row / p.G;
+    return (static_cast<size_t>(u.b) * p.n_max + i) * p.Hq + u.h * p.G + (row - i * p.G);
+}
+
+// 32 outputs of a row
+__device__ __forceinline__ void store_out32(kvmm_bf16* out, const float* o)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4*>(out)[i] =
+            make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                       pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+}
+
+__device__ __forceinline__ float lse_of(float m, float l, float scale_log2)
+{
+    return l > 0.f ? (m * scale_log2 + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D, int T>
+__device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
+{
+    constexpr int kPages = kTokens / T;
+    const TreeAttnParams& p = a.p;
+    const int s = threadIdx.x >> 7, r = threadIdx.x & 127, warp = r >> 5, lane = r & 31;
+    const bool two = a.tiles == 2;
+    const uint32_t mine = c.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t tS = mine + s * 128, tO = mine + 256 + s * 128;
+    const float scale = p.scale_log2, slack = 8.f / scale;
+    uint32_t s_phase = 0, o_phase = 0, met = 0, nth = 0;
+    Unit u;
+    int begin, count;
+    while (next_piece<T>(a, k, u, begin, count)) {
+        const int row0 = u.row0 + (two ? s * 128 : 0), row = row0 + r;
+        const int rows = min(max(u.row0 + u.rows - row0, 0), 128);  // of the tile
+        const bool busy = warp * 32 < rows;                          // the warp has rows
+        load_queries<D>(p, u, row0, smem + s * Smem<D>::kTile);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.q_ready[s]);
+        uint64_t bits = 0;
+        if (r < rows) {
+            const int i = row / p.G;
+            bits = p.tree_mask != nullptr ? p.tree_mask[static_cast<size_t>(u.b) * p.n_max + i] : ~0ull >> (63 - i);
+            if (u.held < 64) bits &= (1ull << u.held) - 1;
+        }
+        float ref = -INFINITY, l = 0.f;
+        const int steps = two ? count : (count - s + 1) / 2;
+        for (int v = 0; v < steps; ++v) {
+            const int blk = two ? v : 2 * v + s;
+            if (!__all_sync(kFullMask, wait_for(&c.s_full[s], s_phase & 1, &c.gave_up))) return;
+            ++s_phase;
+            tc_fence_after();
+            if (busy) {
+                uint32_t z[kTokens];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, z + 32 * i);
+                tmem_wait_ld();
+                const BlockMask& m = c.mask[(nth + blk) % kRing];
+                if (!m.whole) {
+#pragma unroll
+                    for (int i = 0; i < kPages; ++i) {
+                        const int j = m.node0[i];  // the node in the page's first slot, below 0 where it comes later
+                        uint32_t seen = m.settled[i];
+                        if (j < 64 && j > -64) seen |= static_cast<uint32_t>(j >= 0 ? bits >> j : bits << -j);
+#pragma unroll
+                        for (int t = 0; t < T; ++t)
+                            z[i * T + t] = seen >> t & 1 ? z[i * T + t] : 0xff800000u;
+                    }
+                }
+                float top[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(z[i]);
+#pragma unroll
+                for (int i = 4; i < kTokens; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(z[i]));
+                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (v == 0) {
+                    ref = most;
+                } else if (__any_sync(kFullMask, most > ref + slack)) {
+                    // (the products before this block's scores are done: O may be changed)
+                    float f = 1.f;
+                    if (most > ref + slack) {
+                        f = exp2_fast((ref - most) * scale);  // 0 where nothing was seen before
+                        ref = most;
+                        l *= f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * i, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tmem_st32(tO + 32 * i, o);
+                    }
+                }
+                const float base = ref == -INFINITY ? 0.f : ref * scale;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const float e0 = exp2_fast(fmaf(__uint_as_float(z[64 * i + 2 * x]), scale, -base));
+                        const float e1 = exp2_fast(fmaf(__uint_as_float(z[64 * i + 2 * x + 1]), scale, -base));
+                        sum[(2 * x) % 4] += e0;
+                        sum[(2 * x + 1) % 4] += e1;
+                        w[x] = pack_bf16x2(e0, e1);
+                    }
+                    tmem_st32(tS + 32 * i, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.p_ready[s]);
+        }
+        nth += count;
+        if (steps > 0) {
+            if (!__all_sync(kFullMask, wait_for(&c.o_done[s], o_phase & 1, &c.gave_up))) return;
+            ++o_phase;
+            tc_fence_after();
+        }
+        // the row's result: written whole, or left as a part
+        const bool whole = count == u.blocks;
+        const size_t part = (2 * blockIdx.x + (begin > 0 ? 0 : 1)) * a.tiles + (two ? s : 0);
+        float f0 = 1.f, f1 = 0.f;
+        int c0 = 0, c1 = D / 32;
+        const bool join = !two && count > 1;
+        if (!two) {  // both streams hold the same rows: each group joins half of the channels
+            c.ml[s][r] = make_float2(ref, l);
+            if (!groups_meet(c, met)) return;
+            const float2 other = c.ml[s ^ 1][r];
+            const float m = fmaxf(ref, other.x);
+            const float mine_f = l > 0.f ? exp2_fast((ref - m) * scale) : 0.f;
+            const float other_f = other.y > 0.f ? exp2_fast((other.x - m) * scale) : 0.f;
+            f0 = s == 0 ? mine_f : other_f;
+            f1 = s == 0 ? other_f : mine_f;
+            l = l * mine_f + other.y * other_f;
+            ref = m;
+            c0 = s * (D / 64);
+            c1 = c0 + D / 64;
+        }
+        if (busy) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const size_t at = r < rows ? row_of(p, u, row) : 0;
+            for (int i = c0; i < c1; ++i) {
+                uint32_t x[32], y[32];
+                tmem_ld32(mine + 256 + (two ? s * 128 : 0) + 32 * i, x);
+                if (join) tmem_ld32(mine + 384 + 32 * i, y);
+                tmem_wait_ld();
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    o[e] = __uint_as_float(x[e]) * f0;
+                    if (join) o[e] = fmaf(__uint_as_float(y[e]), f1, o[e]);
+                }
+                if (r < rows) {
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = l > 0.f ? o[e] * inv : 0.f;
+                        store_out32(p.out + at * D + 32 * i, o);
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(a.o + (part * a.tile_rows + r) * D + 32 * i);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+            }
+            if (r < rows && (two || s == 0)) {
+                if (!whole)
+                    a.ml[part * a.tile_rows + r] = make_float2(ref, l);
+                else if (p.lse != nullptr)
+                    p.lse[at] = lse_of(ref, l, scale);
+            }
+        }
+        tc_fence_before();
+        if (!two && !groups_meet(c, met)) return;  // the other stream's sums have been read, and its O
+        tc_fence_after();
+    }
+}
+
+// ---- the kernel ---------------------------------------------------------------------
+template <int D, int T>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_kernel(const Launch a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using S = Smem<D>;
+    Control& c = *reinterpret_cast<Control*>(smem + S::kControl);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == 9) tmem_alloc_all(&c.tmem);
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&c.full[i], 1);
+            mbar_init(&c.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c.s_full[i], 1);
+            mbar_init(&c.p_ready[i], 4);
+            mbar_init(&c.q_ready[i], 4);
+            mbar_init(&c.o_done[i], 1);
+        }
+        mbar_init(&c.meet, 8);
+        mbar_init(&c.drain, 1);
+        c.gave_up = 0;
+        c.w0 = a.units;
+        c.off0 = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
     pdl_wait_then_release();
-    const int cap = p.Pmax * T;
-    const bool tell = blockIdx.x == 0 && warp == 0 && lane == 0;
-    int seq = p.seq_len[b], n = p.n_nodes != nullptr ? p.n_nodes[b] : p.n_max;
-    if (seq < 0 || seq > cap || n < 0 || n > p.n_max) {
-        if (tell) report(p.err, KVMM_ERR_OUT_OF_RANGE);
-        seq = min(max(seq, 0), cap);
-        n = min(max(n, 0), p.n_max);
+
+    // the CTA's run of blocks: each thread counts some units, in order
+    const int per = (a.units + kThreads - 1) / kThreads;
+    int sum = 0;
+    for (int w = tid * per; w < min(a.units, (tid + 1) * per); ++w) sum += unit_of<T>(a, w, blockIdx.x == 0).blocks;
+    int before = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kFullMask, before, off);
+        if (lane >= off) before += y;
     }
-    int held = n;
-    if (seq + n > cap) {
-        if (tell) report(p.err, KVMM_ERR_OUT_OF_RANGE);
-        held = cap - seq;
+    if (lane == 31) c.sums[warp] = before;
+    __syncthreads();
+    int total = 0;
+    before -= sum;
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) before += c.sums[i];
+        total += c.sums[i];
     }
-    const int row = blockIdx.x * kTreeWarps + warp;
-    if (row >= n * p.G) return;
-    const int i = row / p.G, g = row % p.G;
-    const size_t unit = (static_cast<size_t>(b) * p.L + p.layer) * p.Hkv + h;
-    const size_t node = static_cast<size_t>(b) * p.n_max + i;
-    const size_t at = node * p.Hq + h * p.G + g;
-    uint64_t bits = p.tree_mask != nullptr ? p.tree_mask[node] : ~0ull >> (63 - i);
-    if (held < 64) bits &= (1ull << held) - 1;
-    const int pages = (seq + T - 1) / T;
-    int listed = pages, cnt = 0;
-    if (p.sel_idx != nullptr) {
-        cnt = p.sel_cnt[unit];
-        if (cnt < 0 || cnt > p.Kmax) {
-            if (tell) report(p.err, KVMM_ERR_OUT_OF_RANGE);
-            cnt = min(max(cnt, 0), p.Kmax);
+    // every CTA that takes part has a block: the parts of a unit come from consecutive CTAs
+    const long long n = min(static_cast<int>(gridDim.x), max(total, 1));
+    const int start = static_cast<int>(min(total * static_cast<long long>(blockIdx.x) / n, static_cast<long long>(total)));
+    const int end = static_cast<int>(min(total * (blockIdx.x + 1ll) / n, static_cast<long long>(total)));
+    for (int w = tid * per; w < min(a.units, (tid + 1) * per); ++w) {
+        const Unit u = unit_of<T>(a, w, false);
+        if (start < end && start >= before && start < before + u.blocks) {
+            c.w0 = w;
+            c.off0 = start - before;
         }
-        listed = cnt;
-    }
-    const int first = seq / T, node_pages = held > 0 ? (seq + held - 1) / T - first + 1 : 0;
-    float q[C], o[C], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        q[c] = __uint_as_float(static_cast<uint32_t>(p.q[at * D + lane + 32 * c]) << 16);
-        o[c] = 0.f;
-    }
-    for (int e = 0; e < listed + node_pages; ++e) {
-        const bool settled = e < listed;
-        const int page = !settled ? first + e - listed : p.sel_idx != nullptr ? p.sel_idx[unit * p.Kmax + e] : e;
-        if (settled && (page < 0 || page >= pages)) {
-            if (lane == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
-            continue;
+        if (u.blocks == 0) {
+            if (blockIdx.x == 0) a.parts[w] = make_int2(-2, 0);
+        } else if (before >= start && before < end) {  // the unit begins here; its last block's CTA
+            const long long last = ((before + u.blocks) * n - 1) / total;
+            a.parts[w] = last == blockIdx.x ? make_int2(-1, 0) : make_int2(blockIdx.x, static_cast<int>(last));
         }
-        const int32_t phys = p.block_table[unit * p.Pmax + page];
-        if (phys < 0 || phys >= p.n_phys) {
-            if (lane == 0) report(p.err, phys < 0 ? KVMM_ERR_NULL_BLOCK : KVMM_ERR_OUT_OF_RANGE);
-            continue;
-        }
-        const kvmm_bf16* k = p.k_pool + static_cast<size_t>(phys) * T * D;
-        const kvmm_bf16* v = p.v_pool + static_cast<size_t>(phys) * T * D;
-        for (int s = 0; s < T; ++s) {
-            const int t = page * T + s, j = t - seq;
-            const bool live = settled ? j < 0 : j >= 0 && j < held && (bits >> j & 1);
-            if (!live) continue;
-            float z = 0.f;
+        before += u.blocks;
+    }
+    __syncthreads();
+    tc_fence_after();
+    const Walk k{c.w0, c.off0, end - start};
+    if (warp < 8)
+        softmax_rows<D, T>(a, smem, c, k);
+    else if (warp == 8)
+        copy_pages<D, T>(a, &kmap, &vmap, smem, c, k);
+    else
+        issue_products<D, T>(a, smem, c, k);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && c.gave_up != 0) report(a.p.err, KVMM_ERR_TIMEOUT);
+    if (warp == 9) tmem_free_all(c.tmem);
+}
+
+// ---- the parts of units that fell on several CTAs, and units without a block -------------
+constexpr int kJoinWarps = 4;
+
+template <int D, int T>
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch a)
+{
+    constexpr int C = D / 32;
+    const TreeAttnParams& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait_then_release();
+    const int w = blockIdx.x;
+    const int2 parts = a.parts[w];
+    if (parts.x == -1) return;
+    const Unit u = unit_of<T>(a, w, false);
+    const int row = blockIdx.y * kJoinWarps + warp;
+    if (row >= u.rows) return;
+    const size_t at = row_of(p, u, u.row0 + row);
+    const int tile = row >> 7, r = row & 127;
+    float o[C], m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                z = fmaf(q[c], __uint_as_float(static_cast<uint32_t>(k[s * D + lane + 32 * c]) << 16), z);
+    for (int i = 0; i < C; ++i) o[i] = 0.f;
+    if (parts.x >= 0) {
+        auto part = [&](int cta) {
+            return ((2 * static_cast<size_t>(cta) + (cta == parts.x ? 1 : 0)) * a.tiles + tile) * a.tile_rows + r;
+        };
+        for (int cta = parts.x + lane; cta <= parts.y; cta += 32) m = fmaxf(m, a.ml[part(cta)].x);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(kFullMask, z, off);
-            z *= p.scale_log2;
-            const float mn = fmaxf(m, z), f = exp2f(m - mn), w = exp2f(z - mn);
-            m = mn;
-            l = fmaf(l, f, w);
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, off));
+#pragma unroll 4
+        for (int cta = parts.x; cta <= parts.y; ++cta) {
+            const size_t x = part(cta);
+            const float2 ml = a.ml[x];
+            const float f = ml.y > 0.f ? exp2_fast((ml.x - m) * p.scale_log2) : 0.f;
+            l = fmaf(ml.y, f, l);
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                o[c] = fmaf(o[c], f, w * __uint_as_float(static_cast<uint32_t>(v[(lane + 32 * c) * T + s]) << 16));
+            for (int i = 0; i < C; ++i) o[i] = fmaf(a.o[x * D + lane * C + i], f, o[i]);
         }
     }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + at * D + lane * C);
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-        p.out[at * D + lane + 32 * c] = static_cast<kvmm_bf16>(pack_bf16x2(l > 0.f ? o[c] / l : 0.f, 0.f) & 0xffffu);
-    if (p.lse != nullptr && lane == 0) p.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    for (int i = 0; i < C / 2; ++i) out[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+    if (p.lse != nullptr && lane == 0) p.lse[at] = lse_of(m, l, p.scale_log2);
+}
+
+// rows of the nodes' tiles, and how the units are cut
+struct Cut {
+    int tiles, groups, tile_rows, batches;  // batches: of one launch
+    Cut(int n_max, int G, int Hkv, int B)
+    {
+        const int rows = n_max * G;
+        tiles = rows > 128 ? 2 : 1;
+        groups = (rows + 128 * tiles - 1) / (128 * tiles);
+        tile_rows = rows < 128 ? rows : 128;
+        batches = kUnitsAtOnce / (Hkv * groups);
+        batches = batches < 1 ? 1 : batches > B ? B : batches;
+    }
+    size_t parts_bytes(int Hkv) const { return round256(sizeof(int2) * static_cast<size_t>(batches) * Hkv * groups); }
+    size_t rows() const { return static_cast<size_t>(2 * kTreeMaxCtas) * tiles * tile_rows; }
+    size_t ml_bytes() const { return round256(sizeof(float2) * rows()); }
+};
+
+template <int D, int T>
+cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    struct Device {
+        int dev = -1, sms = 0;
+    };
+    static thread_local Device known;  // per thread and kernel
+    if (known.dev != dev) {
+        e = cudaFuncSetAttribute(tree_attn_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(Smem<D>::kBytes));
+        if (e != cudaSuccess) return e;
+        e = cudaDeviceGetAttribute(&known.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        known.dev = dev;
+    }
+    CUtensorMap kmap, vmap;
+    const uint64_t n = static_cast<uint64_t>(p.n_phys < INT32_MAX ? p.n_phys : INT32_MAX);
+    e = tensor_map_3d(&kmap, p.k_pool, D, T, n, 64, T, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    e = tensor_map_3d(&vmap, p.v_pool, T, D, n, T, D, T == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B);
+    if (e != cudaSuccess) return e;
+
+    const Cut cut(p.n_max, p.G, p.Hkv, p.B);
+    Launch a{};
+    a.p = p;
+    a.tiles = cut.tiles;
+    a.groups = cut.groups;
+    a.tile_rows = cut.tile_rows;
+    char* ws = static_cast<char*>(p.workspace);
+    a.parts = reinterpret_cast<int2*>(ws);
+    a.ml = reinterpret_cast<float2*>(ws + cut.parts_bytes(p.Hkv));
+    a.o = reinterpret_cast<float*>(ws + cut.parts_bytes(p.Hkv) + cut.ml_bytes());
+    const int pages = p.sel_idx != nullptr ? p.Kmax + (p.n_max + T - 2) / T + 1 : p.Pmax;
+    const long long most = (static_cast<long long>(pages) * T + kTokens - 1) / kTokens;  // blocks of a unit
+    const int rows = p.n_max * p.G < 128 * cut.tiles ? p.n_max * p.G : 128 * cut.tiles;
+    for (a.b0 = 0; a.b0 < p.B; a.b0 += cut.batches) {
+        a.nb = p.B - a.b0 < cut.batches ? p.B - a.b0 : cut.batches;
+        a.units = a.nb * p.Hkv * cut.groups;
+        long long ctas = most * a.units;
+        if (ctas > known.sms) ctas = known.sms;
+        if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
+        e = launch_pdl(tree_attn_kernel<D, T>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Smem<D>::kBytes, stream, a,
+                       kmap, vmap);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(tree_join_kernel<D, T>, dim3(a.units, (rows + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0,
+                       stream, a);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
 
-size_t tree_ws_bytes(const kvmm_shape&, int) { return 16; }
+size_t tree_ws_bytes(const kvmm_shape& s, int n_max)
+{
+    const Cut cut(n_max, s.Hq / s.Hkv, s.Hkv, s.B);
+    return cut.parts_bytes(s.Hkv) + cut.ml_bytes() + sizeof(float) * cut.rows() * s.D;
+}
 
 cudaError_t launch_tree_attention(const TreeAttnParams& p, cudaStream_t stream)
 {
-    const dim3 grid((p.n_max * p.G + kTreeWarps - 1) / kTreeWarps, p.Hkv, p.B), block(kTreeWarps * 32);
-    if (p.D == 128)
-        return p.T == 16 ? launch_pdl(tree_attn_kernel<128, 16>, grid, block, 0, stream, p)
-                         : launch_pdl(tree_attn_kernel<128, 32>, grid, block, 0, stream, p);
-    return p.T == 16 ? launch_pdl(tree_attn_kernel<64, 16>, grid, block, 0, stream, p)
-                     : launch_pdl(tree_attn_kernel<64, 32>, grid, block, 0, stream, p);
+    if (p.D == 128) return p.T == 16 ? launch<128, 16>(p, stream) : launch<128, 32>(p, stream);
+    return p.T == 16 ? launch<64, 16>(p, stream) : launch<64, 32>(p, stream);
 }
 
 }  // namespace kvmm
