@@ -30,7 +30,7 @@
 namespace kvmm {
 namespace {
 
-constexpr int kThreads = 320;    // 8 softmax warps, the copying warp, the issuing warp
+constexpr int kThreads = 384;    // 8 softmax warps, the copying warp, the issuing warp, two that only share registers
 constexpr int kTokens = 128;     // tokens of a block
 constexpr int kRing = 8;         // blocks whose masks are held (see copy_pages)
 constexpr int kNoNode = 1 << 20; // an entry that holds no node
@@ -462,7 +462,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
                 uint32_t z[kTokens];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, z + 32 * i);
-                tmem_wait_ld();
+                tmem_wait_ld(z);
                 const BlockMask& m = c.mask[(nth + blk) % kRing];
                 if (!m.whole) {
 #pragma unroll
@@ -491,30 +491,30 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
                         ref = most;
                         l *= f;
                     }
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + i, o);
+                        tmem_wait_ld(o);
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + 32 * i, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        tmem_st32(tO + 32 * i, o);
+                        for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tmem_st16(tO + i, o);
                     }
                 }
                 const float base = ref == -INFINITY ? 0.f : ref * scale;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t w[32];
+                for (int i = 0; i < kTokens / 32; ++i) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const float e0 = exp2_fast(fmaf(__uint_as_float(z[64 * i + 2 * x]), scale, -base));
-                        const float e1 = exp2_fast(fmaf(__uint_as_float(z[64 * i + 2 * x + 1]), scale, -base));
+                    for (int x = 0; x < 16; ++x) {
+                        const float e0 = exp2_fast(fmaf(__uint_as_float(z[32 * i + 2 * x]), scale, -base));
+                        const float e1 = exp2_fast(fmaf(__uint_as_float(z[32 * i + 2 * x + 1]), scale, -base));
                         sum[(2 * x) % 4] += e0;
                         sum[(2 * x + 1) % 4] += e1;
                         w[x] = pack_bf16x2(e0, e1);
                     }
-                    tmem_st32(tS + 32 * i, w);
+                    tmem_st16(tS + 16 * i, w);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_wait_st();
@@ -555,8 +555,9 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
             for (int i = c0; i < c1; ++i) {
                 uint32_t x[32], y[32];
                 tmem_ld32(mine + 256 + (two ? s * 128 : 0) + 32 * i, x);
-                if (join) tmem_ld32(mine + 384 + 32 * i, y);
-                tmem_wait_ld();
+                tmem_ld32(mine + 384 + 32 * i, y);  // (not used unless the streams are joined)
+                tmem_wait_ld(x);
+                tmem_wait_ld(y);
                 float o[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -658,12 +659,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const Walk k{c.w0, c.off0, end - start};
-    if (warp < 8)
+    // 168 registers a thread at launch: the softmax groups take 208 (a row's 128 scores stay in registers), the others 88
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         softmax_rows<D, T>(a, smem, c, k);
-    else if (warp == 8)
-        copy_pages<D, T>(a, &kmap, &vmap, smem, c, k);
-    else
-        issue_products<D, T>(a, smem, c, k);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8)
+            copy_pages<D, T>(a, &kmap, &vmap, smem, c, k);
+        else if (warp == 9)
+            issue_products<D, T>(a, smem, c, k);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
