@@ -262,21 +262,19 @@ __device__ void copy_pages(const Launch& a, const CUtensorMap* kmap, const CUten
     }
 }
 
-// ---- the issuing warp -------------------------------------------------------------
-// Slots of a block's values that nothing shows are set to zero: whatever they hold, NaN included, would meet a weight of 0.
+// ---- values that nothing may see -------------------------------------------------------
+// Slots of a block's values that nothing shows are set to zero: whatever they hold, NaN included, would meet a weight of
+// 0.  By the 128 threads of a softmax group, before they hand over the weights.
 template <int D, int T>
-__device__ __forceinline__ void clear_unseen(uint8_t* values, const BlockMask& m)
+__device__ __noinline__ void clear_unseen(uint8_t* values, const BlockMask& m)
 {
     constexpr int kPages = kTokens / T, kChunks = T / 8;
-    const int lane = threadIdx.x & 31;
     for (int i = 0; i < kPages; ++i) {
         uint32_t seen = m.settled[i];
-        for (int t = 0; t < T; ++t) {
-            const int j = m.node0[i] + t;
-            if (j >= 0 && j < m.held) seen |= 1u << t;
-        }
+        const int from = max(m.node0[i], 0), to = min(m.node0[i] + T, m.held);  // its nodes (none: from >= to)
+        if (from < to) seen |= ((to - from >= 32 ? 0u : 1u << (to - from)) - 1u) << (from - m.node0[i]);
         if (seen == 0xffffffffu >> (32 - T)) continue;
-        for (int x = lane; x < D * kChunks; x += 32) {
+        for (int x = threadIdx.x & 127; x < D * kChunks; x += 128) {
             const int d = x / kChunks, ch = x % kChunks;
             const uint32_t bits = seen >> (8 * ch) & 255u;
             if (bits == 255u) continue;
@@ -291,84 +289,88 @@ __device__ __forceinline__ void clear_unseen(uint8_t* values, const BlockMask& m
         }
     }
     fence_proxy_async_shared();
-    __syncwarp();
 }
 
+// ---- the issuing thread -------------------------------------------------------------
+// In order: the scores of the first two steps, then, as each step's weights come, its P V and the scores of the step after
+// next.  So the step of one stream has P V and Q K^T done while the other's softmax runs.  A group's scores are complete
+// only when the P V before them is (its sums may then be rescaled), and they overwrite its weights behind that P V.
 template <int D, int T>
 __device__ void issue_products(const Launch& a, uint8_t* smem, Control& c, Walk k)
 {
     using S = Smem<D>;
     constexpr uint64_t rows128 = matrix_desc(128), rowsT = matrix_desc(T * 2);
     constexpr uint32_t qk = mma_desc(128, kTokens), pv = mma_desc(128, D);
-    const int lane = threadIdx.x & 31;
-    const uint32_t ring = smem_addr(smem) + 2 * S::kTile, tmem = c.tmem;
+    const uint32_t base = smem_addr(smem), ring = base + 2 * S::kTile, tmem = c.tmem;
     const bool two = a.tiles == 2;
-    uint32_t item = 0, piece = 0, nth = 0, p_phase[2] = {0, 0};
+    // slot and phase of the next block's keys and of the next values: every other item of the ring
+    uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;
+    auto next = [](uint32_t& slot, uint32_t& phase) {
+        slot += 2;
+        if (slot >= S::kStages) {
+            slot -= S::kStages;
+            phase ^= 1;
+        }
+    };
+    uint32_t piece = 0, p_phase = 0;  // a bit a stream
     bool fine = true;
     Unit u;
     int begin, count;
     while (fine && next_piece<T>(a, k, u, begin, count)) {
         fine = wait_for(&c.q_ready[0], piece & 1, &c.gave_up) && wait_for(&c.q_ready[1], piece & 1, &c.gave_up);
-        fine = __all_sync(kFullMask, fine);
+        tc_fence_after();
         ++piece;
         const int steps = two ? 2 * count : count;
         auto scores = [&](int v) {  // S = Q K^T of step v
-            const int s = v & 1, blk = two ? v >> 1 : v;
-            const uint32_t it = item + 2 * blk, slot = it % S::kStages;
-            if (!two || s == 0) fine = fine && wait_for(&c.full[slot], it / S::kStages & 1, &c.gave_up);
-            fine = __all_sync(kFullMask, fine);
-            if (!fine) return;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint64_t q = matrix_at(rows128, smem_addr(smem) + s * S::kTile), kk = matrix_at(rows128, ring + slot * S::kTile);
+            const uint32_t s = v & 1;
+            const bool first = !two || s == 0, last = !two || s == 1;  // of the products that take the block's keys
+            if (first && !wait_for(&c.full[k_slot], k_phase, &c.gave_up)) {
+                fine = false;
+                return;
+            }
+            const uint64_t q = matrix_at(rows128, base + s * S::kTile), kk = matrix_at(rows128, ring + k_slot * S::kTile);
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t off = ((i / 4) * (128 * 128) + (i % 4) * 32) >> 4;
-                    mma_ss(tmem + s * 128, q + off, kk + off, qk, i > 0);
-                }
-                if (!two || s == 1) mma_commit(&c.empty[slot]);
-                mma_commit(&c.s_full[s]);
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t off = ((i / 4) * (128 * 128) + (i % 4) * 32) >> 4;
+                mma_ss(tmem + s * 128, q + off, kk + off, qk, i > 0);
             }
-            __syncwarp();
+            mma_commit(&c.s_full[s]);
+            if (last) {
+                mma_commit(&c.empty[k_slot]);
+                next(k_slot, k_phase);
+            }
         };
-        auto values = [&](int v) {  // O += P V of step v
-            const int s = v & 1, blk = two ? v >> 1 : v;
-            const uint32_t it = item + 2 * blk + 1, slot = it % S::kStages;
-            if (!two || s == 0) {
-                fine = fine && wait_for(&c.full[slot], it / S::kStages & 1, &c.gave_up);
-                fine = __all_sync(kFullMask, fine);
-                if (!fine) return;
-                const BlockMask& m = c.mask[(nth + blk) % kRing];
-                if (!m.whole) clear_unseen<D, T>(smem + 2 * S::kTile + slot * S::kTile, m);
+        scores(0);
+        if (fine && steps > 1) scores(1);
+        for (int v = 0; fine && v < steps; ++v) {  // O += P V of step v
+            const uint32_t s = v & 1;
+            const bool first = !two || s == 0, last = !two || s == 1;
+            if ((first && !wait_for(&c.full[v_slot], v_phase, &c.gave_up)) ||
+                !wait_for(&c.p_ready[s], p_phase >> s & 1, &c.gave_up)) {
+                fine = false;
+                break;
             }
-            fine = fine && wait_for(&c.p_ready[s], p_phase[s] & 1, &c.gave_up);
-            ++p_phase[s];
-            fine = __all_sync(kFullMask, fine);
-            if (!fine) return;
+            p_phase ^= 1u << s;
             tc_fence_after();
-            if (lane == 0) {
-                const uint64_t vv = matrix_at(rowsT, ring + slot * S::kTile);
-                const bool later = v > 1;  // the stream has had a step of this piece
+            const uint64_t vv = matrix_at(rowsT, ring + v_slot * S::kTile);
+            mma_ts(tmem + 256 + s * 128, tmem + s * 128, vv, pv, v > 1);  // (the first of the stream's in this piece: not added)
 #pragma unroll
-                for (int i = 0; i < kTokens / 16; ++i) {
-                    const uint32_t off = ((i * 16 / T) * (T * D * 2) + (i * 16 % T) * 2) >> 4;
-                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, vv + off, pv, later || i > 0);
-                }
-                if (!two || s == 1) mma_commit(&c.empty[slot]);
-                if (v + 2 >= steps) mma_commit(&c.o_done[s]);
+            for (int i = 1; i < kTokens / 16; ++i) {
+                const uint32_t off = ((i * 16 / T) * (T * D * 2) + (i * 16 % T) * 2) >> 4;
+                mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, vv + off, pv, true);
             }
-            __syncwarp();
-        };
-        if (fine) scores(0);
-        for (int v = 0; fine && v < steps; ++v) {
-            if (v + 1 < steps) scores(v + 1);
-            if (fine) values(v);
+            if (last) {
+                mma_commit(&c.empty[v_slot]);
+                next(v_slot, v_phase);
+            }
+            if (v + 2 < steps)
+                scores(v + 2);
+            else
+                mma_commit(&c.o_done[s]);
         }
-        item += 2 * count;
-        nth += count;
     }
     if (!fine) {  // products in flight end before the CTA does
-        if (lane == 0) mma_commit(&c.drain);
+        mma_commit(&c.drain);
         mbar_wait_bounded(&c.drain, 0);
     }
 }
@@ -519,6 +521,11 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_wait_st();
             }
+            if ((!two || s == 0) && !c.mask[(nth + blk) % kRing].whole) {
+                const uint32_t item = 2 * (nth + blk) + 1, slot = item % Smem<D>::kStages;
+                if (!__all_sync(kFullMask, wait_for(&c.full[slot], item / Smem<D>::kStages & 1, &c.gave_up))) return;
+                clear_unseen<D, T>(smem + (2 + slot) * Smem<D>::kTile, c.mask[(nth + blk) % kRing]);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c.p_ready[s]);
@@ -667,8 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8)
             copy_pages<D, T>(a, &kmap, &vmap, smem, c, k);
-        else if (warp == 9)
+        else if (warp == 9 && elect_one())
             issue_products<D, T>(a, smem, c, k);
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
