@@ -43,9 +43,11 @@ struct Launch {
     int groups;      // units of one (batch, KV head)
     int units;       // nb * Hkv * groups
     int tile_rows;   // rows of a tile in the workspace
-    int2* parts;     // of each unit: its first and last CTA; first -1: it was written whole, -2: it has no block
+    int cluster;     // CTAs of a unit, one cluster; 0: the blocks of all units are dealt evenly to the CTAs
+    int by_unit;     // (dealt evenly) cut has an entry for each unit, else for each CTA
+    int4* cut;       // a unit whose blocks fall on several CTAs (x -1: none): unit, first CTA, last CTA
     float2* ml;      // [2 * CTAs][tiles][tile_rows] reference and sum
-    float* o;        // [2 * CTAs][tiles][tile_rows][D]
+    float4* o;       // [2 * CTAs][tiles][D / 4][tile_rows]
 };
 
 struct Unit {
@@ -101,7 +103,9 @@ struct Control {
     uint64_t full[10], empty[10], s_full[2], p_ready[2], q_ready[2], o_done[2], meet, drain;
     uint32_t tmem;
     int32_t gave_up;
-    int32_t w0, off0, total;
+    int32_t w0, off0, left;
+    int4 cut;
+    Unit unit;  // w0
     int32_t sums[kThreads / 32];
     BlockMask mask[kRing];
     float2 ml[2][128];
@@ -141,7 +145,8 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
 
 // the CTA's run of blocks, piece by piece (a piece: blocks of one unit)
 struct Walk {
-    int w, off, left;  // unit, its next block, blocks of the run to come
+    int w, off, left;   // unit, its next block, blocks of the run to come
+    const Unit* first;  // unit w, as long as it is the run's first
 };
 template <int T>
 __device__ __forceinline__ bool next_piece(const Launch& a, Walk& k, Unit& u, int& begin, int& count)
@@ -149,7 +154,8 @@ __device__ __forceinline__ bool next_piece(const Launch& a, Walk& k, Unit& u, in
     if (k.left <= 0) return false;
     for (;; ++k.w, k.off = 0) {
         if (k.w >= a.units) return false;
-        u = unit_of<T>(a, k.w, false);
+        u = k.first != nullptr ? *k.first : unit_of<T>(a, k.w, false);
+        k.first = nullptr;
         if (u.blocks > k.off) break;
     }
     begin = k.off;
@@ -386,29 +392,37 @@ __device__ __forceinline__ bool groups_meet(Control& c, uint32_t& phase)
     return __all_sync(kFullMask, fine);
 }
 
-// the group's tile of queries, rows that do not exist as zeros
+// row / G of a row below 512: (row / 65536 adds less than 1 / 8 to the quotient's fraction)
+__device__ __forceinline__ int node_of(const TreeAttnParams& p, int row) { return row * (65536 / p.G + 1) >> 16; }
+
+// where a row of the unit is among the nodes' heads
+__device__ __forceinline__ size_t row_of(const TreeAttnParams& p, const Unit& u, int row)
+{
+    const int i = node_of(p, row);
+    return (static_cast<size_t>(u.b) * p.n_max + i) * p.Hq + u.h * p.G + (row - i * p.G);
+}
+
+// the group's tile of queries, rows that do not exist as zeros; every load is in flight before the first store
 template <int D>
 __device__ __forceinline__ void load_queries(const TreeAttnParams& p, const Unit& u, int row0, uint8_t* tile)
 {
-    const int t = threadIdx.x & 127;
-#pragma unroll 4
-    for (int x = t; x < 128 * (D / 8); x += 128) {
-        const int r = x / (D / 8), ch = x % (D / 8), row = row0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < u.row0 + u.rows) {
-            const int i = row / p.G, g = row - i * p.G;
-            v = reinterpret_cast<const uint4*>(
-                p.q + ((static_cast<size_t>(u.b) * p.n_max + i) * p.Hq + u.h * p.G + g) * D)[ch];
-        }
-        *reinterpret_cast<uint4*>(tile + (ch / 8) * (128 * 128) + r * 128 + ((ch % 8 ^ (r & 7)) << 4)) = v;
+    constexpr int kLoads = D / 8;
+    const int t = threadIdx.x & 127, ch = t % (D / 8), r0 = t / (D / 8), end = u.row0 + u.rows;
+    const kvmm_bf16* q = p.q + (static_cast<size_t>(u.b) * p.n_max * p.Hq + u.h * p.G) * D + ch * 8;
+    const int magic = 65536 / p.G + 1;
+    uint4 v[kLoads];
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+        const int row = row0 + r0 + x * (1024 / D), i = row * magic >> 16;
+        v[x] = make_uint4(0, 0, 0, 0);
+        if (row < end) v[x] = *reinterpret_cast<const uint4*>(q + (i * p.Hq + (row - i * p.G)) * D);
+    }
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+        const int r = r0 + x * (1024 / D);
+        *reinterpret_cast<uint4*>(tile + (ch / 8) * (128 * 128) + r * 128 + ((ch % 8 ^ (r & 7)) << 4)) = v[x];
     }
     fence_proxy_async_shared();
-}
-
-__device__ __forceinline__ size_t row_of(const TreeAttnParams& p, const Unit& u, int row)
-{
-    const int i = row / p.G;
-    return (static_cast<size_t>(u.b) * p.n_max + i) * p.Hq + u.h * p.G + (row - i * p.G);
 }
 
 // 32 outputs of a row
@@ -420,6 +434,10 @@ __device__ __forceinline__ void store_out32(kvmm_bf16* out, const float* o)
             make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
                        pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
 }
+
+// a quad of a row's sums in shared memory (see join_cluster)
+template <int D>
+__device__ __forceinline__ int quad_at(int row, int quad) { return row * (D / 4) + (quad ^ (row & (D / 4 - 1))); }
 
 __device__ __forceinline__ float lse_of(float m, float l, float scale_log2)
 {
@@ -449,7 +467,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
         if (lane == 0) mbar_arrive(&c.q_ready[s]);
         uint64_t bits = 0;
         if (r < rows) {
-            const int i = row / p.G;
+            const int i = node_of(p, row);
             bits = p.tree_mask != nullptr ? p.tree_mask[static_cast<size_t>(u.b) * p.n_max + i] : ~0ull >> (63 - i);
             if (u.held < 64) bits &= (1ull << u.held) - 1;
         }
@@ -537,7 +555,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
             tc_fence_after();
         }
         // the row's result: written whole, or left as a part
-        const bool whole = count == u.blocks;
+        const bool whole = count == u.blocks && a.cluster == 0;
         const size_t part = (2 * blockIdx.x + (begin > 0 ? 0 : 1)) * a.tiles + (two ? s : 0);
         float f0 = 1.f, f1 = 0.f;
         int c0 = 0, c1 = D / 32;
@@ -556,6 +574,8 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
             c0 = s * (D / 64);
             c1 = c0 + D / 64;
         }
+        // (a cluster's CTA has one piece: behind the meeting the ring is free, and its sums go there)
+        if (two && a.cluster > 0 && !groups_meet(c, met)) return;
         if (busy) {
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const size_t at = r < rows ? row_of(p, u, row) : 0;
@@ -576,15 +596,24 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = l > 0.f ? o[e] * inv : 0.f;
                         store_out32(p.out + at * D + 32 * i, o);
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(a.o + (part * a.tile_rows + r) * D + 32 * i);
+                    } else if (a.cluster > 0) {
+                        float4* dst = reinterpret_cast<float4*>(smem + 2 * Smem<D>::kTile);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e)
+                            dst[quad_at<D>(two ? s * 128 + r : r, 8 * i + e)] =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else {
+                        float4* dst = a.o + (part * (D / 4) + 8 * i) * a.tile_rows + r;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e * a.tile_rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
             }
             if (r < rows && (two || s == 0)) {
-                if (!whole)
+                if (a.cluster > 0)
+                    reinterpret_cast<float2*>(smem + 2 * Smem<D>::kTile + a.tiles * 128 * D * 4)[two ? s * 128 + r : r] =
+                        make_float2(ref, l);
+                else if (!whole)
                     a.ml[part * a.tile_rows + r] = make_float2(ref, l);
                 else if (p.lse != nullptr)
                     p.lse[at] = lse_of(ref, l, scale);
@@ -596,6 +625,130 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
     }
 }
 
+// a unit to which nothing is shown: its selection is empty and its nodes have no place
+__device__ __noinline__ void write_nothing(const TreeAttnParams& p, const Unit& u)
+{
+    for (int row = u.row0; row < u.row0 + u.rows; ++row) {
+        const size_t at = row_of(p, u, row);
+        for (int x = 0; x < p.D / 8; ++x) reinterpret_cast<uint4*>(p.out + at * p.D)[x] = make_uint4(0, 0, 0, 0);
+        if (p.lse != nullptr) p.lse[at] = -INFINITY;
+    }
+}
+
+// The CTA's run of blocks where they are dealt evenly: each thread counts some units, in order.
+template <int T>
+__device__ __forceinline__ void deal_blocks(const Launch& a, Control& c)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (a.units + kThreads - 1) / kThreads;
+    int sum = 0;
+    Unit u;
+    for (int w = tid * per; w < min(a.units, (tid + 1) * per); ++w) {
+        u = unit_of<T>(a, w, blockIdx.x == 0);
+        sum += u.blocks;
+    }
+    int before = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kFullMask, before, off);
+        if (lane >= off) before += y;
+    }
+    if (lane == 31) c.sums[warp] = before;
+    __syncthreads();
+    int total = 0;
+    before -= sum;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+        const int x = c.sums[i];
+        if (i < warp) before += x;
+        total += x;
+    }
+    // Every CTA that takes part has a block: the parts of a unit come from consecutive CTAs.  CTA i begins at block
+    // total * i / n, rounded down.
+    const int n = min(static_cast<int>(gridDim.x), max(total, 1)), each = total / n, rest = total - each * n;
+    const int cta = min(static_cast<int>(blockIdx.x), n);
+    const int start = each * cta + rest * cta / n;
+    const int end = cta == n ? start : each * (cta + 1) + rest * (cta + 1) / n;
+    for (int w = tid * per; w < min(a.units, (tid + 1) * per); ++w) {
+        if (per > 1) u = unit_of<T>(a, w, false);
+        if (start < end && start >= before && start < before + u.blocks) {
+            c.w0 = w;
+            c.off0 = start - before;
+            c.left = end - start;
+            c.unit = u;
+        }
+        if (u.blocks == 0) {
+            if (u.rows > 0 && blockIdx.x == 0) write_nothing(a.p, u);
+        } else if (before >= start && before < end && before + u.blocks > end) {
+            // the unit begins here and goes on, up to the CTA of its last block
+            c.cut = make_int4(w, cta, static_cast<int>((static_cast<long long>(before + u.blocks) * n - 1) / total), 0);
+        }
+        if (a.by_unit && (u.blocks == 0 ? blockIdx.x == 0 : before >= start && before < end))
+            a.cut[w] = u.blocks != 0 && before + u.blocks > end ? c.cut : make_int4(-1, 0, 0, 0);
+        before += u.blocks;
+    }
+    if (a.by_unit) return;
+    __syncthreads();
+    if (tid == 0) a.cut[blockIdx.x] = c.cut;
+}
+
+// ---- a cluster a unit: its CTAs' sums, joined through distributed shared memory -----------
+// A CTA's sums lie where its ring of blocks was: rows of D / 4 quads, a row's quads swapped by its number so that both a
+// thread a row and a thread a quad reach all banks; behind them reference and sum of each row.
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t local, uint32_t rank)
+{
+    uint32_t remote;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(remote)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 ld_cluster_v2(uint32_t local, uint32_t rank)
+{
+    uint32_t remote;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
+    return v;
+}
+
+template <int D>
+__device__ __forceinline__ void join_cluster(const Launch& a, const Unit& u, uint8_t* smem)
+{
+    const TreeAttnParams& p = a.p;
+    const uint32_t sums = smem_addr(smem) + 2 * Smem<D>::kTile, ml = sums + a.tiles * 128 * D * 4;
+    for (int x = cluster_ctarank() * 256 + threadIdx.x; x < u.rows * (D / 4); x += a.cluster * 256) {
+        const int row = x / (D / 4), quad = x % (D / 4);
+        float m = -INFINITY;
+#pragma unroll 4
+        for (int k = 0; k < a.cluster; ++k) m = fmaxf(m, ld_cluster_v2(ml + row * 8, k).x);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < a.cluster; ++k) {
+            const float2 y = ld_cluster_v2(ml + row * 8, k);
+            const float4 v = ld_cluster_v4(sums + quad_at<D>(row, quad) * 16, k);
+            if (y.y > 0.f) {  // (a CTA without a block has left no sums)
+                const float f = exp2_fast((y.x - m) * p.scale_log2);
+                l = fmaf(y.y, f, l);
+                o.x = fmaf(v.x, f, o.x);
+                o.y = fmaf(v.y, f, o.y);
+                o.z = fmaf(v.z, f, o.z);
+                o.w = fmaf(v.w, f, o.w);
+            }
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const size_t at = row_of(p, u, u.row0 + row);
+        reinterpret_cast<uint2*>(p.out + at * D)[quad] =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (p.lse != nullptr && quad == 0) p.lse[at] = lse_of(m, l, p.scale_log2);
+    }
+}
+
 // ---- the kernel ---------------------------------------------------------------------
 template <int D, int T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -604,8 +757,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     using S = Smem<D>;
     Control& c = *reinterpret_cast<Control*>(smem + S::kControl);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     if (warp == 9) tmem_alloc_all(&c.tmem);
+    if (tid == 256) {  // (the copying warp's: the maps are there before its first copy)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+    }
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&c.full[i], 1);
@@ -622,50 +779,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.gave_up = 0;
         c.w0 = a.units;
         c.off0 = 0;
+        c.left = 0;
+        c.cut = make_int4(-1, 0, 0, 0);
         fence_barrier_init();
     }
     tc_fence_before();
     pdl_wait_then_release();
 
-    // the CTA's run of blocks: each thread counts some units, in order
-    const int per = (a.units + kThreads - 1) / kThreads;
-    int sum = 0;
-    for (int w = tid * per; w < min(a.units, (tid + 1) * per); ++w) sum += unit_of<T>(a, w, blockIdx.x == 0).blocks;
-    int before = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(kFullMask, before, off);
-        if (lane >= off) before += y;
-    }
-    if (lane == 31) c.sums[warp] = before;
-    __syncthreads();
-    int total = 0;
-    before -= sum;
-    for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) before += c.sums[i];
-        total += c.sums[i];
-    }
-    // every CTA that takes part has a block: the parts of a unit come from consecutive CTAs
-    const long long n = min(static_cast<int>(gridDim.x), max(total, 1));
-    const int start = static_cast<int>(min(total * static_cast<long long>(blockIdx.x) / n, static_cast<long long>(total)));
-    const int end = static_cast<int>(min(total * (blockIdx.x + 1ll) / n, static_cast<long long>(total)));
-    for (int w = tid * per; w < min(a.units, (tid + 1) * per); ++w) {
-        const Unit u = unit_of<T>(a, w, false);
-        if (start < end && start >= before && start < before + u.blocks) {
-            c.w0 = w;
-            c.off0 = start - before;
-        }
-        if (u.blocks == 0) {
-            if (blockIdx.x == 0) a.parts[w] = make_int2(-2, 0);
-        } else if (before >= start && before < end) {  // the unit begins here; its last block's CTA
-            const long long last = ((before + u.blocks) * n - 1) / total;
-            a.parts[w] = last == blockIdx.x ? make_int2(-1, 0) : make_int2(blockIdx.x, static_cast<int>(last));
-        }
-        before += u.blocks;
+    if (a.cluster == 0) {
+        deal_blocks<T>(a, c);
+    } else if (tid == 0) {
+        c.w0 = blockIdx.x / a.cluster;
+        const int rank = cluster_ctarank();
+        c.unit = unit_of<T>(a, c.w0, rank == 0);
+        c.off0 = c.unit.blocks * rank / a.cluster;
+        c.left = c.unit.blocks * (rank + 1) / a.cluster - c.off0;
     }
     __syncthreads();
     tc_fence_after();
-    const Walk k{c.w0, c.off0, end - start};
+    const Walk k{c.w0, c.off0, c.left, &c.unit};
     // 168 registers a thread at launch: the softmax groups take 208 (a row's 128 scores stay in registers), the others 88
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -681,53 +813,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (a.cluster > 0) {
+        if (c.left == 0 && tid < a.tiles * 128)  // nothing was summed here
+            reinterpret_cast<float2*>(smem + 2 * S::kTile + a.tiles * 128 * D * 4)[tid] = make_float2(-INFINITY, 0.f);
+        cluster_sync();
+        if (warp < 8) join_cluster<D>(a, c.unit, smem);  // (the warps that have the registers)
+        cluster_sync();
+    }
     if (tid == 0 && c.gave_up != 0) report(a.p.err, KVMM_ERR_TIMEOUT);
     if (warp == 9) tmem_free_all(c.tmem);
 }
 
-// ---- the parts of units that fell on several CTAs, and units without a block -------------
-constexpr int kJoinWarps = 4;
+// ---- the parts of units that fell on several CTAs --------------------------------------
+// A block takes 32 rows of a unit, a lane a row.  With many parts a unit (SLICES = 4) the warps
+// share them, two channel quads a block; with few, a warp takes D / 32 quads over all parts.
+constexpr int kJoinWarps = 8;
 
-template <int D, int T>
+template <int D, int T, int SLICES>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch a)
 {
-    constexpr int C = D / 32;
+    constexpr int Q = SLICES == 1 ? D / 32 : 1;  // quads of a warp
+    __shared__ float4 other[SLICES][kJoinWarps / SLICES][32];
     const TreeAttnParams& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slice = SLICES == 1 ? 0 : warp % SLICES, quad0 = SLICES == 1 ? warp * Q : blockIdx.z * 2 + warp / SLICES;
     pdl_wait_then_release();
-    const int w = blockIdx.x;
-    const int2 parts = a.parts[w];
-    if (parts.x == -1) return;
-    const Unit u = unit_of<T>(a, w, false);
-    const int row = blockIdx.y * kJoinWarps + warp;
-    if (row >= u.rows) return;
-    const size_t at = row_of(p, u, u.row0 + row);
-    const int tile = row >> 7, r = row & 127;
-    float o[C], m = -INFINITY, l = 0.f;
+    const int4 cut = a.cut[blockIdx.x];
+    if (cut.x < 0) return;
+    const Unit u = unit_of<T>(a, cut.x, false);
+    const int row = blockIdx.y * 32 + lane, first = cut.y, last = cut.z;
+    if (blockIdx.y * 32 >= u.rows) return;
+    const int tile = row >> 7, r = min(row & 127, a.tile_rows - 1);  // (a lane without a row reads another's)
+    auto part = [&](int cta) { return static_cast<size_t>(2 * cta + (cta == first ? 1 : 0)) * a.tiles + tile; };
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int cta = first; cta <= last; ++cta) m = fmaxf(m, a.ml[part(cta) * a.tile_rows + r].x);
+    float4 o[Q];
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.f;
-    if (parts.x >= 0) {
-        auto part = [&](int cta) {
-            return ((2 * static_cast<size_t>(cta) + (cta == parts.x ? 1 : 0)) * a.tiles + tile) * a.tile_rows + r;
-        };
-        for (int cta = parts.x + lane; cta <= parts.y; cta += 32) m = fmaxf(m, a.ml[part(cta)].x);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, off));
+    for (int i = 0; i < Q; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
 #pragma unroll 4
-        for (int cta = parts.x; cta <= parts.y; ++cta) {
-            const size_t x = part(cta);
-            const float2 ml = a.ml[x];
-            const float f = ml.y > 0.f ? exp2_fast((ml.x - m) * p.scale_log2) : 0.f;
-            l = fmaf(ml.y, f, l);
+    for (int cta = first; cta <= last; ++cta) {
+        const float2 ml = a.ml[part(cta) * a.tile_rows + r];
+        const float f = ml.y > 0.f ? exp2_fast((ml.x - m) * p.scale_log2) : 0.f;
+        l = fmaf(ml.y, f, l);
+        if (SLICES > 1 && (cta - first) % SLICES != slice) continue;
+        const float4* x = a.o + (part(cta) * (D / 4) + quad0) * a.tile_rows + r;
 #pragma unroll
-            for (int i = 0; i < C; ++i) o[i] = fmaf(a.o[x * D + lane * C + i], f, o[i]);
+        for (int i = 0; i < Q; ++i) {
+            const float4 y = x[i * a.tile_rows];
+            o[i].x = fmaf(y.x, f, o[i].x);
+            o[i].y = fmaf(y.y, f, o[i].y);
+            o[i].z = fmaf(y.z, f, o[i].z);
+            o[i].w = fmaf(y.w, f, o[i].w);
         }
     }
+    if (SLICES > 1) {
+        other[slice][warp / SLICES][lane] = o[0];
+        __syncthreads();
+        if (slice != 0) return;
+        for (int i = 1; i < SLICES; ++i) {
+            const float4 y = other[i][warp / SLICES][lane];
+            o[0] = make_float4(o[0].x + y.x, o[0].y + y.y, o[0].z + y.z, o[0].w + y.w);
+        }
+    }
+    if (row >= u.rows) return;
+    const size_t at = row_of(p, u, u.row0 + row);
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + at * D + lane * C);
+    uint2* out = reinterpret_cast<uint2*>(p.out + at * D) + quad0;
 #pragma unroll
-    for (int i = 0; i < C / 2; ++i) out[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-    if (p.lse != nullptr && lane == 0) p.lse[at] = lse_of(m, l, p.scale_log2);
+    for (int i = 0; i < Q; ++i)
+        out[i] = make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
+    if (p.lse != nullptr && quad0 == 0) p.lse[at] = lse_of(m, l, p.scale_log2);
 }
 
 // rows of the nodes' tiles, and how the units are cut
@@ -742,10 +899,34 @@ struct Cut {
         batches = kUnitsAtOnce / (Hkv * groups);
         batches = batches < 1 ? 1 : batches > B ? B : batches;
     }
-    size_t parts_bytes(int Hkv) const { return round256(sizeof(int2) * static_cast<size_t>(batches) * Hkv * groups); }
+    static constexpr size_t kCutBytes = (sizeof(int4) * kTreeMaxCtas + 255) / 256 * 256;
     size_t rows() const { return static_cast<size_t>(2 * kTreeMaxCtas) * tiles * tile_rows; }
     size_t ml_bytes() const { return round256(sizeof(float2) * rows()); }
 };
+
+constexpr int kShort = 12;
+
+// clusters of c CTAs of this kernel that the device holds at once
+int clusters_at_once(void (*kernel)(Launch, CUtensorMap, CUtensorMap), size_t smem, int c)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c, 1, 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return -1;
+    }
+    return n > 0 ? n : -1;
+}
 
 template <int D, int T>
 cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
@@ -755,9 +936,13 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     struct Device {
         int dev = -1, sms = 0;
+        int held[17] = {};  // clusters of c CTAs held at once; 0: not asked yet, -1: none
     };
     static thread_local Device known;  // per thread and kernel
     if (known.dev != dev) {
+        known = Device{};
+        e = cudaFuncSetAttribute(tree_attn_kernel<D, T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
         e = cudaFuncSetAttribute(tree_attn_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(Smem<D>::kBytes));
         if (e != cudaSuccess) return e;
@@ -779,23 +964,46 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
     a.groups = cut.groups;
     a.tile_rows = cut.tile_rows;
     char* ws = static_cast<char*>(p.workspace);
-    a.parts = reinterpret_cast<int2*>(ws);
-    a.ml = reinterpret_cast<float2*>(ws + cut.parts_bytes(p.Hkv));
-    a.o = reinterpret_cast<float*>(ws + cut.parts_bytes(p.Hkv) + cut.ml_bytes());
+    a.cut = reinterpret_cast<int4*>(ws);
+    a.ml = reinterpret_cast<float2*>(ws + Cut::kCutBytes);
+    a.o = reinterpret_cast<float4*>(ws + Cut::kCutBytes + cut.ml_bytes());
     const int pages = p.sel_idx != nullptr ? p.Kmax + (p.n_max + T - 2) / T + 1 : p.Pmax;
     const long long most = (static_cast<long long>(pages) * T + kTokens - 1) / kTokens;  // blocks of a unit
     const int rows = p.n_max * p.G < 128 * cut.tiles ? p.n_max * p.G : 128 * cut.tiles;
     for (a.b0 = 0; a.b0 < p.B; a.b0 += cut.batches) {
         a.nb = p.B - a.b0 < cut.batches ? p.B - a.b0 : cut.batches;
         a.units = a.nb * p.Hkv * cut.groups;
+        // A cluster a unit, of the most CTAs whose clusters all run at once, where no CTA then takes more than kShort
+        // blocks: no second launch, and no CTA looks through all units for its own.
+        int c = 0;
+        if (a.units <= known.sms) {
+            for (c = 1; c < 16 && c < most && a.units * (c + 1) <= known.sms;) {
+                int& held = known.held[c + 1];
+                if (held == 0) held = clusters_at_once(tree_attn_kernel<D, T>, Smem<D>::kBytes, c + 1);
+                if (held < a.units) break;
+                ++c;
+            }
+        }
+        a.cluster = c > 0 && (most + c - 1) / c <= kShort ? c : 0;
+        if (a.cluster > 0) {
+            e = launch_pdl_cluster(tree_attn_kernel<D, T>, dim3(static_cast<unsigned>(a.units * c)), dim3(kThreads),
+                                   Smem<D>::kBytes, stream, static_cast<unsigned>(c), a, kmap, vmap);
+            if (e != cudaSuccess) return e;
+            continue;
+        }
         long long ctas = most * a.units;
         if (ctas > known.sms) ctas = known.sms;
         if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
+        a.by_unit = a.units <= ctas;
         e = launch_pdl(tree_attn_kernel<D, T>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Smem<D>::kBytes, stream, a,
                        kmap, vmap);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(tree_join_kernel<D, T>, dim3(a.units, (rows + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0,
-                       stream, a);
+        if (ctas == 1) continue;  // nothing is cut
+        const unsigned at = static_cast<unsigned>(a.by_unit ? a.units : ctas), groups32 = (rows + 31) / 32;
+        if (ctas > 4ll * a.units)
+            e = launch_pdl(tree_join_kernel<D, T, 4>, dim3(at, groups32, D / 8), dim3(kJoinWarps * 32), 0, stream, a);
+        else
+            e = launch_pdl(tree_join_kernel<D, T, 1>, dim3(at, groups32), dim3(kJoinWarps * 32), 0, stream, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -806,7 +1014,7 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
 size_t tree_ws_bytes(const kvmm_shape& s, int n_max)
 {
     const Cut cut(n_max, s.Hq / s.Hkv, s.Hkv, s.B);
-    return cut.parts_bytes(s.Hkv) + cut.ml_bytes() + sizeof(float) * cut.rows() * s.D;
+    return Cut::kCutBytes + cut.ml_bytes() + sizeof(float) * cut.rows() * s.D;
 }
 
 cudaError_t launch_tree_attention(const TreeAttnParams& p, cudaStream_t stream)
