@@ -8,16 +8,21 @@
 // residual is stored: an entry's is found again from p, q and the factors of
 // the children rejected before it at the same node.
 //
-// One CTA takes one sequence.  Each warp owns a run of entries, so that the
-// drawn token is found from the warps' sums and one warp's second look.
+// A cluster of CTAs takes one sequence.  One lane of each CTA walks the tree (all
+// alike; fp64 runs at two lanes a clock); where a sum over the row is needed the
+// CTAs share the row, a run of entries for each warp, and exchange their sums
+// through distributed shared memory.  The sums of the last pass lead to the drawn
+// token: the CTA, the warp, then one look at that warp's run again.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace kvmm {
 namespace {
 
-constexpr int kVerThreads = 1024;
+constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kVerCluster = 16;
+constexpr int kStep = 128;  // entries a warp takes at once, four a lane
 constexpr long long kWhole = 1ll << 53;
 
 // floor(x * 2^53) of x clamped to [0, 512] (NaN: 0)
@@ -54,9 +59,25 @@ __device__ __forceinline__ long long residual(const Row& r, float p, float q, in
     return w;
 }
 
-__device__ __forceinline__ long long residual_at(const Row& r, int x)
+// entries x .. x + 3 of a row of V, 0 behind its end
+__device__ __forceinline__ float4 entries4(const float* row, long long x, int V)
 {
-    return residual(r, r.p[x], r.q != nullptr ? r.q[x] : 0.f, x);
+    if (x + 4 <= V && (reinterpret_cast<uintptr_t>(row) & 15) == 0) return __ldg(reinterpret_cast<const float4*>(row + x));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (x < V) v.x = __ldg(row + x);
+    if (x + 1 < V) v.y = __ldg(row + x + 1);
+    if (x + 2 < V) v.z = __ldg(row + x + 2);
+    if (x + 3 < V) v.w = __ldg(row + x + 3);
+    return v;
+}
+
+// the residuals of a lane's four entries
+__device__ __forceinline__ void residual4(const Row& r, const float4& p, const float4& q, int x, long long (&w)[4])
+{
+    w[0] = residual(r, p.x, q.x, x);
+    w[1] = residual(r, p.y, q.y, x + 1);
+    w[2] = residual(r, p.z, q.z, x + 2);
+    w[3] = residual(r, p.w, q.w, x + 3);
 }
 
 __device__ __forceinline__ long long warp_sum(long long v)
@@ -66,143 +87,218 @@ __device__ __forceinline__ long long warp_sum(long long v)
     return v;
 }
 
-// the sum of a row's residual; every warp's part stays in part[]
-__device__ long long row_sum(const Row& r, int V, int run, long long* part)
+struct Shared {
+    int token[kTreeMaxNodes], path[kTreeMaxNodes], gone[kTreeMaxNodes];
+    float u[kTreeMaxNodes], factor[kTreeMaxNodes];
+    float p[kTreeMaxNodes], q[kTreeMaxNodes];          // a node's token in its parent's rows
+    unsigned long long children[kTreeMaxNodes];        // bits
+    long long part[kVerWarps];                         // the warps' sums of a pass
+    long long totals[2][kVerCluster];                  // the CTAs', by the pass's parity
+    int cur, rejected, len, ask;                       // ask: a sum is wanted for the walk
+};
+
+__device__ __forceinline__ void st_cluster_s64(long long* local, uint32_t rank, long long v)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long first = static_cast<long long>(warp) * run;
-    const int end = static_cast<int>(min(first + run, static_cast<long long>(V)));
-    long long s = 0;
-    for (long long x = first + lane; x < end; x += 32) s += residual_at(r, static_cast<int>(x));
-    s = warp_sum(s);
-    __syncthreads();
-    if (lane == 0) part[warp] = s;
-    __syncthreads();
-    s = part[lane];
-    return warp_sum(s);
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
+    asm volatile("st.shared::cluster.s64 [%0], %1;" ::"r"(remote), "l"(v) : "memory");
 }
 
-__global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyParams p)
+// The sum of a row's residual over all CTAs of the cluster; the warps' and the CTAs' parts stay in part and totals.
+// A CTA writes totals of the pass after next only behind the next pass's barrier, when all have read these.
+__device__ __forceinline__ long long row_sum(const Row& r, int V, int run, int ctas, int parity, Shared& sh)
 {
-    __shared__ int token[kTreeMaxNodes], parent[kTreeMaxNodes], path[kTreeMaxNodes], gone[kTreeMaxNodes];
-    __shared__ float u[kTreeMaxNodes], factor[kTreeMaxNodes];
-    __shared__ long long part[kVerWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_ctarank();
+    const long long first = static_cast<long long>(rank * kVerWarps + warp) * run;
+    const long long end = min(first + run, static_cast<long long>(V));
+    long long s = 0;
+#pragma unroll 4
+    for (long long x = first + 4 * lane; x < end; x += kStep) {
+        const float4 p = entries4(r.p, x, V);
+        const float4 q = r.q != nullptr ? entries4(r.q, x, V) : make_float4(0.f, 0.f, 0.f, 0.f);
+        long long w[4];
+        residual4(r, p, q, static_cast<int>(x), w);
+        s += (w[0] + w[1]) + (w[2] + w[3]);
+    }
+    s = warp_sum(s);
+    if (lane == 0) sh.part[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        s = warp_sum(lane < kVerWarps ? sh.part[lane] : 0);
+        if (lane < ctas) st_cluster_s64(&sh.totals[parity][rank], lane, s);
+    }
+    cluster_sync();
+    s = 0;
+    for (int k = 0; k < ctas; ++k) s += sh.totals[parity][k];
+    return s;
+}
+
+__global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyParams p, int ctas, int run)
+{
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = cluster_ctarank();
+    const int b = blockIdx.x / ctas;
     const size_t at = static_cast<size_t>(b) * p.n_max;
+    if (tid < kTreeMaxNodes) sh.children[tid] = 0;
+    cluster_arrive();
     pdl_wait_then_release();
     int n = p.n_nodes != nullptr ? p.n_nodes[b] : p.n_max;
     if (n < 0 || n > p.n_max) {
-        if (tid == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
+        if (tid == 0 && rank == 0) report(p.err, KVMM_ERR_OUT_OF_RANGE);
         n = n < 0 ? 0 : p.n_max;
     }
-    if (tid < n) {
-        int t = p.tokens[at + tid], from = p.parent[at + tid];
-        if (tid == 0) {
-            from = -1;
-        } else if (t < 0 || t >= p.V || from < 0 || from >= tid) {
-            report(p.err, KVMM_ERR_OUT_OF_RANGE);
-            t = 0;
-            from = -1;
-        }
-        token[tid] = t;
-        parent[tid] = from;
-        u[tid] = p.u_accept[at + tid];
+    if (n == 0) {  // (the whole cluster leaves)
+        if (rank == 0 && tid < p.n_max) p.path[at + tid] = p.out_tokens[at + tid] = -1;
+        if (rank == 0 && tid == 0) p.path_len[b] = 0;
+        cluster_wait();
+        return;
     }
     __syncthreads();
-    const int run = ((p.V + kVerWarps - 1) / kVerWarps + 31) & ~31;
-    int len = 0, drawn = -1;
-    if (n > 0) {
-        int cur = 0;
-        len = 1;
-        if (tid == 0) path[0] = 0;
-        Row r{p.target + at * p.target_stride, p.draft != nullptr ? p.draft + at * p.draft_stride : nullptr, 0, factor,
-              gone};
-        long long W = kWhole;
-        double Q = 1.0;
-        for (int i = 1; i < n; ++i) {
-            if (parent[i] != cur) continue;
-            const int x = token[i];
-            const long long w = residual_at(r, x);
-            long long c = W;
-            float f = 0.f, q = 0.f;
-            if (r.q != nullptr) {
-                q = r.q[x];
-                if (W > 0 && Q > 0.0) f = static_cast<float>(static_cast<double>(W) * 0x1p-53 / Q);
-                c = weight_of(__fmul_rn(q, f));
-            }
-            if (static_cast<double>(u[i]) * static_cast<double>(c) < static_cast<double>(w)) {
-                cur = i;
-                if (tid == 0) path[len] = i;
-                ++len;
-                r.p = p.target + (at + i) * p.target_stride;
-                if (r.q != nullptr) r.q = p.draft + (at + i) * p.draft_stride;
-                r.rejected = 0;
-                W = kWhole;
-                Q = 1.0;
-                continue;
-            }
-            __syncthreads();  // the lists are read above
-            if (tid == 0) {
-                factor[r.rejected] = f;
-                gone[r.rejected] = x;
-            }
-            __syncthreads();
-            ++r.rejected;
-            if (r.q != nullptr) {
-                W = row_sum(r, p.V, run, part);
-                if (p.distinct) Q -= static_cast<double>(q);
-            } else {
-                W = W > w ? W - w : 0;
+    if (tid < n) {
+        const int t = p.tokens[at + tid], from = p.parent[at + tid];
+        sh.token[tid] = t;
+        sh.u[tid] = p.u_accept[at + tid];
+        if (tid > 0) {
+            if (t >= 0 && t < p.V && from >= 0 && from < tid) {
+                sh.p[tid] = p.target[(at + from) * p.target_stride + t];
+                sh.q[tid] = p.draft != nullptr ? p.draft[(at + from) * p.draft_stride + t] : 0.f;
+                atomicOr(&sh.children[from], 1ull << tid);
+            } else if (rank == 0) {
+                report(p.err, KVMM_ERR_OUT_OF_RANGE);
             }
         }
-        long long sum = row_sum(r, p.V, run, part);
-        if (sum == 0) {  // nothing is left: the row itself
-            r.rejected = 0;
-            sum = row_sum(r, p.V, run, part);
-        }
-        long long goal = static_cast<long long>(static_cast<double>(p.u_next[b]) * static_cast<double>(sum));
-        goal = min(goal, sum - 1);
-        // the warp whose run holds the goal, then its entry
-        long long before = 0;
-        int owner = 0;
-        for (; owner < kVerWarps - 1 && before + part[owner] <= goal; ++owner) before += part[owner];
-        if (warp == owner) {
-            drawn = p.V - 1;
-            const long long first = static_cast<long long>(owner) * run;
-            for (long long x0 = first; x0 < p.V && x0 < first + run; x0 += 32) {
-                const int x = static_cast<int>(x0) + lane;
-                long long w = x < p.V && x0 + lane < first + run ? residual_at(r, x) : 0;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const long long y = __shfl_up_sync(kFullMask, w, off);
-                    if (lane >= off) w += y;
+    }
+    if (tid == 0) {
+        sh.cur = sh.rejected = 0;
+        sh.path[0] = 0;
+        sh.len = 1;
+    }
+    __syncthreads();
+    cluster_wait();  // every CTA of the cluster has begun: its shared memory may be written
+
+    Row r{nullptr, nullptr, 0, sh.factor, sh.gone};
+    unsigned long long left = sh.children[0];  // children to be tried (thread 0's)
+    long long W = kWhole;
+    double Q = 1.0;
+    int parity = 0;
+    for (;;) {
+        if (tid == 0) {
+            sh.ask = 0;
+            while (left != 0) {
+                const int i = __ffsll(static_cast<long long>(left)) - 1, x = sh.token[i];
+                left &= left - 1;
+                r.q = p.draft;
+                r.rejected = sh.rejected;
+                const long long w = residual(r, sh.p[i], sh.q[i], x);
+                long long c = W;
+                float f = 0.f;
+                if (p.draft != nullptr) {
+                    if (W > 0 && Q > 0.0) f = static_cast<float>(static_cast<double>(W) * 0x1p-53 / Q);
+                    c = weight_of(__fmul_rn(sh.q[i], f));
                 }
-                const uint32_t over = __ballot_sync(kFullMask, before + w > goal);
-                if (over) {
-                    drawn = min(p.V - 1, static_cast<int>(x0) + __ffs(over) - 1);
-                    break;
+                if (static_cast<double>(sh.u[i]) * static_cast<double>(c) < static_cast<double>(w)) {
+                    sh.cur = i;
+                    sh.path[sh.len++] = i;
+                    sh.rejected = 0;
+                    left = sh.children[i];
+                    W = kWhole;
+                    Q = 1.0;
+                    continue;
                 }
-                before += __shfl_sync(kFullMask, w, 31);
+                sh.factor[sh.rejected] = f;
+                sh.gone[sh.rejected] = x;
+                ++sh.rejected;
+                if (p.draft == nullptr) {
+                    W = W > w ? W - w : 0;
+                    continue;
+                }
+                if (p.distinct) Q -= static_cast<double>(sh.q[i]);
+                sh.ask = left != 0;
+                break;
             }
-            if (lane == 0) gone[0] = drawn;
         }
         __syncthreads();
-        drawn = gone[0];
+        const bool more = sh.ask != 0;
+        r.p = p.target + (at + sh.cur) * p.target_stride;
+        r.rejected = sh.rejected;
+        r.q = p.draft != nullptr && r.rejected > 0 ? p.draft + (at + sh.cur) * p.draft_stride : nullptr;
+        W = row_sum(r, p.V, run, ctas, parity, sh);  // (its barriers stand between the walk's reads and writes)
+        parity ^= 1;
+        if (!more) break;
     }
-    __syncthreads();
-    if (tid < p.n_max) {
-        p.path[at + tid] = tid < len ? path[tid] : -1;
-        p.out_tokens[at + tid] = tid + 1 < len ? token[path[tid + 1]] : tid + 1 == len ? drawn : -1;
+    if (W == 0 && r.rejected > 0) {  // nothing is left: the row itself
+        r.rejected = 0;
+        r.q = nullptr;
+        W = row_sum(r, p.V, run, ctas, parity, sh);
+        parity ^= 1;
     }
-    if (tid == 0) p.path_len[b] = len;
+    long long goal = static_cast<long long>(static_cast<double>(p.u_next[b]) * static_cast<double>(W));
+    goal = min(goal, W - 1);
+    // the CTA whose entries hold the goal, its warp, then the entry
+    long long before = 0;
+    int owner = 0;
+    for (; owner < ctas - 1 && before + sh.totals[parity ^ 1][owner] <= goal; ++owner) before += sh.totals[parity ^ 1][owner];
+    if (owner != rank) return;
+    for (owner = 0; owner < kVerWarps - 1 && before + sh.part[owner] <= goal; ++owner) before += sh.part[owner];
+    if (warp != owner) return;
+    const long long first = static_cast<long long>(rank * kVerWarps + warp) * run;
+    int drawn = p.V - 1;
+    for (long long x = first + 4 * lane; x - 4 * lane < min(first + run, static_cast<long long>(p.V)); x += kStep) {
+        const float4 pp = entries4(r.p, x, p.V);
+        const float4 qq = r.q != nullptr ? entries4(r.q, x, p.V) : make_float4(0.f, 0.f, 0.f, 0.f);
+        long long w[4];
+        residual4(r, pp, qq, static_cast<int>(x), w);
+        const long long mine = (w[0] + w[1]) + (w[2] + w[3]);
+        long long upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(kFullMask, upto, off);
+            if (lane >= off) upto += y;
+        }
+        const uint32_t over = __ballot_sync(kFullMask, before + upto > goal);
+        if (over != 0) {
+            long long c = before + upto - mine;
+            int k = 0;
+            for (; k < 3; ++k) {
+                c += w[k];
+                if (c > goal) break;
+            }
+            drawn = min(static_cast<int>(x) + k, p.V - 1);
+            drawn = __shfl_sync(kFullMask, drawn, __ffs(over) - 1);
+            break;
+        }
+        before += __shfl_sync(kFullMask, upto, 31);
+    }
+    const int len = sh.len;
+    for (int i = lane; i < p.n_max; i += 32) {
+        p.path[at + i] = i < len ? sh.path[i] : -1;
+        p.out_tokens[at + i] = i + 1 < len ? sh.token[sh.path[i + 1]] : i + 1 == len ? drawn : -1;
+    }
+    if (lane == 0) p.path_len[b] = len;
 }
 
 }  // namespace
 
 cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t stream)
 {
-    return launch_pdl(draft_verify_kernel, dim3(p.B), dim3(kVerThreads), 0, stream, p);
+    // As many CTAs a sequence as keep four on every SM busy, each with a step of entries for every warp at least.
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static thread_local int known = -1, sms = 0;
+    if (known != dev) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(draft_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        known = dev;
+    }
+    int ctas = 1;
+    while (ctas < kVerCluster && 2ll * ctas * p.B <= 4ll * sms && static_cast<long long>(ctas) * kVerWarps * kStep < p.V) ctas *= 2;
+    const long long warps = static_cast<long long>(ctas) * kVerWarps;
+    const int run = static_cast<int>((p.V + warps * kStep - 1) / (warps * kStep)) * kStep;
+    return launch_pdl_cluster(draft_verify_kernel, dim3(static_cast<unsigned>(p.B) * ctas), dim3(kVerThreads), 0, stream,
+                              static_cast<unsigned>(ctas), p, ctas, run);
 }
 
 }  // namespace kvmm
