@@ -25,16 +25,13 @@ constexpr int kVerCluster = 16;
 constexpr int kStep = 128;  // entries a warp takes at once, four a lane
 constexpr long long kWhole = 1ll << 53;
 
-// floor(x * 2^53) of x clamped to [0, 512] (NaN: 0)
+// floor(x * 2^53) of x clamped to [0, 512] (NaN: 0).  x = m * 2^(e - 150), m with its hidden bit: m * 2^39 shifted right
+// by 136 - e.  (e = 0, a zero or what is far below 2^-53, shifts everything out.)
 __device__ __forceinline__ long long weight_of(float x)
 {
-    const uint32_t u = __float_as_uint(x);
-    if (!(x > 0.f)) return 0;
-    if (x >= 512.f) return 1ll << 62;
-    const int e = static_cast<int>(u >> 23);  // x = m * 2^(e - 150), m with its hidden bit
-    const unsigned long long m = (u & 0x7fffffu) | 0x800000u;
-    if (e >= 97) return static_cast<long long>(m << (e - 97));
-    return e > 97 - 24 ? static_cast<long long>(m >> (97 - e)) : 0;
+    const uint32_t u = __float_as_uint(fminf(fmaxf(x, 0.f), 512.f));
+    const unsigned long long m = static_cast<unsigned long long>((u << 7) & 0x3fffffffu | 0x40000000u) << 32;
+    return static_cast<long long>(m >> min(136u - (u >> 23), 63u));
 }
 
 struct Row {  // the residual at a node
@@ -74,10 +71,27 @@ __device__ __forceinline__ float4 entries4(const float* row, long long x, int V)
 // the residuals of a lane's four entries
 __device__ __forceinline__ void residual4(const Row& r, const float4& p, const float4& q, int x, long long (&w)[4])
 {
-    w[0] = residual(r, p.x, q.x, x);
-    w[1] = residual(r, p.y, q.y, x + 1);
-    w[2] = residual(r, p.z, q.z, x + 2);
-    w[3] = residual(r, p.w, q.w, x + 3);
+    w[0] = weight_of(p.x);
+    w[1] = weight_of(p.y);
+    w[2] = weight_of(p.z);
+    w[3] = weight_of(p.w);
+    if (r.q != nullptr) {
+#pragma unroll 1
+        for (int k = 0; k < r.rejected; ++k) {
+            const float f = r.f[k];
+            w[0] = max(w[0] - weight_of(__fmul_rn(q.x, f)), 0ll);
+            w[1] = max(w[1] - weight_of(__fmul_rn(q.y, f)), 0ll);
+            w[2] = max(w[2] - weight_of(__fmul_rn(q.z, f)), 0ll);
+            w[3] = max(w[3] - weight_of(__fmul_rn(q.w, f)), 0ll);
+        }
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < r.rejected; ++k) {
+            const int at = r.gone[k] - x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = at == e ? 0 : w[e];
+        }
+    }
 }
 
 __device__ __forceinline__ long long warp_sum(long long v)
@@ -111,14 +125,26 @@ __device__ __forceinline__ long long row_sum(const Row& r, int V, int run, int c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_ctarank();
     const long long first = static_cast<long long>(rank * kVerWarps + warp) * run;
     const long long end = min(first + run, static_cast<long long>(V));
+    constexpr int kAhead = 4;  // steps whose loads are in flight
     long long s = 0;
-#pragma unroll 4
-    for (long long x = first + 4 * lane; x < end; x += kStep) {
-        const float4 p = entries4(r.p, x, V);
-        const float4 q = r.q != nullptr ? entries4(r.q, x, V) : make_float4(0.f, 0.f, 0.f, 0.f);
-        long long w[4];
-        residual4(r, p, q, static_cast<int>(x), w);
-        s += (w[0] + w[1]) + (w[2] + w[3]);
+#pragma unroll 1
+    for (long long x0 = first + 4 * lane; x0 < end; x0 += kAhead * kStep) {
+        float4 p[kAhead], q[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const long long x = x0 + i * kStep;
+            p[i] = q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < end) {
+                p[i] = entries4(r.p, x, V);
+                if (r.q != nullptr) q[i] = entries4(r.q, x, V);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            long long w[4];
+            residual4(r, p[i], q[i], static_cast<int>(x0) + i * kStep, w);
+            s += (w[0] + w[1]) + (w[2] + w[3]);
+        }
     }
     s = warp_sum(s);
     if (lane == 0) sh.part[warp] = s;
