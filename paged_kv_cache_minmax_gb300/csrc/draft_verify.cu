@@ -19,7 +19,7 @@
 namespace kvmm {
 namespace {
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerCluster = 16;
 constexpr int kStep = 128;  // entries a warp takes at once, four a lane
@@ -32,6 +32,20 @@ __device__ __forceinline__ long long weight_of(float x)
     const uint32_t u = __float_as_uint(fminf(fmaxf(x, 0.f), 512.f));
     const unsigned long long m = static_cast<unsigned long long>((u << 7) & 0x3fffffffu | 0x40000000u) << 32;
     return static_cast<long long>(m >> min(136u - (u >> 23), 63u));
+}
+
+// floor(x * 2^53) of 0 <= x < 2 in three digits: additions that round towards zero leave floor(x * 2^21), floor(r * 2^43)
+// of the rest and floor(r * 2^53) of that in the low bits of their results.  (Each rest is exact.)  fp32 additions run at
+// twice the rate of the integer pipe's shifts and logic.
+constexpr float kDigit1 = 4.f, kDigit2 = 0x1p-20f, kDigit3 = 0x1p-30f;
+struct Digits {
+    int d1, d2, d3;  // with the bits of kDigit1 .. 3 added
+};
+__device__ __forceinline__ Digits digits_of(float x)
+{
+    const float t1 = __fadd_rz(x, kDigit1), r1 = x - (t1 - kDigit1);
+    const float t2 = __fadd_rz(r1, kDigit2), r2 = r1 - (t2 - kDigit2);
+    return {__float_as_int(t1), __float_as_int(t2), __float_as_int(__fadd_rz(r2, kDigit3))};
 }
 
 struct Row {  // the residual at a node
@@ -127,22 +141,56 @@ __device__ __forceinline__ long long row_sum(const Row& r, int V, int run, int c
     const long long end = min(first + run, static_cast<long long>(V));
     constexpr int kAhead = 4;  // steps whose loads are in flight
     long long s = 0;
+    // One pass for what is met most, a row as it is and a row less the draft's once: P - Q where p > q and nothing where
+    // not, which is P less the weight of min(p, q), as floor() ascends.  19 instructions an entry, most of them fp32,
+    // against 46 with every residual in 64 bits: the pass was bound by the integer pipe.
+    const bool plain = r.rejected == 0 || r.q == nullptr || r.rejected == 1;
+    uint32_t odd = 0;  // an exponent of 2 or more, or a sign: no probability, the general pass is right for it
+    if (plain) {
+        const float f = r.q != nullptr ? r.f[0] : 0.f;
 #pragma unroll 1
-    for (long long x0 = first + 4 * lane; x0 < end; x0 += kAhead * kStep) {
-        float4 p[kAhead], q[kAhead];
+        for (long long x0 = first + 4 * lane; x0 < end; x0 += kAhead * kStep) {
+            float4 p[kAhead], q[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const long long x = x0 + i * kStep;
-            p[i] = q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x < end) {
-                p[i] = entries4(r.p, x, V);
-                if (r.q != nullptr) q[i] = entries4(r.q, x, V);
+            for (int i = 0; i < kAhead; ++i) {
+                const long long x = x0 + i * kStep;
+                p[i] = q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x < end) {
+                    p[i] = entries4(r.p, x, V);
+                    if (r.q != nullptr) q[i] = entries4(r.q, x, V);
+                }
             }
-        }
+            int d1 = 0, d2 = 0, d3 = 0;  // 16 entries' digits of 22 bits at most
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+            for (int i = 0; i < kAhead; ++i) {
+                const float pp[4] = {p[i].x, p[i].y, p[i].z, p[i].w}, qq[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    odd |= __float_as_uint(pp[k]);
+                    const Digits a = digits_of(pp[k]), b = digits_of(fminf(__fmul_rn(qq[k], f), pp[k]));
+                    d1 += a.d1 - b.d1;
+                    d2 += a.d2 - b.d2;
+                    d3 += a.d3 - b.d3;
+                }
+            }
+            s += (static_cast<long long>(d1) << 32) + (static_cast<long long>(d2) << 10) + d3;
+        }
+        if (r.q == nullptr)  // less the rejected candidates, each once
+            for (int k = lane; k < r.rejected; k += 32) {
+                const int x = r.gone[k];
+                bool again = x < first || x >= end;
+                for (int e = 0; e < k; ++e) again |= r.gone[e] == x;
+                if (!again) s -= weight_of(r.p[x]);
+            }
+    }
+    if (!plain || __any_sync(kFullMask, (odd >> 30) != 0)) {
+        s = 0;
+#pragma unroll 1
+        for (long long x = first + 4 * lane; x < end; x += kStep) {
+            const float4 p = entries4(r.p, x, V);
+            const float4 q = r.q != nullptr ? entries4(r.q, x, V) : make_float4(0.f, 0.f, 0.f, 0.f);
             long long w[4];
-            residual4(r, p[i], q[i], static_cast<int>(x0) + i * kStep, w);
+            residual4(r, p, q, static_cast<int>(x), w);
             s += (w[0] + w[1]) + (w[2] + w[3]);
         }
     }
@@ -159,7 +207,7 @@ __device__ __forceinline__ long long row_sum(const Row& r, int V, int run, int c
     return s;
 }
 
-__global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyParams p, int ctas, int run)
+__global__ void __launch_bounds__(kVerThreads, 4) draft_verify_kernel(const VerifyParams p, int ctas, int run)
 {
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = cluster_ctarank();
@@ -219,7 +267,10 @@ __global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyP
                 long long c = W;
                 float f = 0.f;
                 if (p.draft != nullptr) {
-                    if (W > 0 && Q > 0.0) f = static_cast<float>(static_cast<double>(W) * 0x1p-53 / Q);
+                    if (W == kWhole && Q == 1.0)
+                        f = 1.f;  // (as the division gives)
+                    else if (W > 0 && Q > 0.0)
+                        f = static_cast<float>(static_cast<double>(W) * 0x1p-53 / Q);
                     c = weight_of(__fmul_rn(sh.q[i], f));
                 }
                 if (static_cast<double>(sh.u[i]) * static_cast<double>(c) < static_cast<double>(w)) {
@@ -307,7 +358,8 @@ __global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyP
 
 cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t stream)
 {
-    // As many CTAs a sequence as keep four on every SM busy, each with a step of entries for every warp at least.
+    // As many CTAs a sequence as all run at once (64 registers a thread: four an SM), each with a step of entries for every
+    // warp at least.
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
