@@ -1129,7 +1129,7 @@ kvmm_status kv_keep_path(const kvmm_shape* shape, int32_t layer, const int32_t* 
     if (st != KVMM_OK) return st;
     const kvmm_shape& s = *shape;
     if (layer < -1 || layer >= s.L || n_max < 1) return KVMM_INVALID_ARG;
-    if (n_max > kvmm::kTreeMaxNodes || static_cast<int64_t>(s.L) * s.Hkv > INT32_MAX) return KVMM_UNSUPPORTED_SHAPE;
+    if (n_max > kvmm::kTreeMaxNodes || static_cast<int64_t>(s.L) * s.Hkv > INT32_MAX / 4) return KVMM_UNSUPPORTED_SHAPE;
     if (!req4(path) || !req4(path_len) || !req4(seq_len) || !req(k_pool) || !req(v_pool) || !req4(block_table) ||
         !opt(meta) || !opt4(err))
         return KVMM_INVALID_ARG;
