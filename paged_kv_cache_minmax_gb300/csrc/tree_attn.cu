@@ -40,12 +40,12 @@ struct Launch {
     TreeAttnParams p;
     int b0, nb;      // batch entries of this launch
     int tiles;       // row tiles of a unit: 1 or 2
-    int groups;      // units of one (batch, KV head)
+    int groups;      // units of one (batch, KV head): 1 or 2
     int units;       // nb * Hkv * groups
     int tile_rows;   // rows of a tile in the workspace
     int cluster;     // CTAs of a unit, one cluster; 0: the blocks of all units are dealt evenly to the CTAs
     int by_unit;     // (dealt evenly) cut has an entry for each unit, else for each CTA
-    int4* cut;       // a unit whose blocks fall on several CTAs (x -1: none): unit, first CTA, last CTA
+    int4* cut;       // a unit whose blocks fall on several CTAs (x -1: none): unit, first CTA, last CTA, rows
     float2* ml;      // [2 * CTAs][tiles][tile_rows] reference and sum
     float4* o;       // [2 * CTAs][tiles][D / 4][tile_rows]
 };
@@ -64,9 +64,10 @@ __device__ __forceinline__ Unit unit_of(const Launch& a, int w, bool tell)
 {
     const TreeAttnParams& p = a.p;
     Unit u;
-    const int g = w % a.groups, bh = w / a.groups;
-    u.h = bh % p.Hkv;
-    u.b = a.b0 + bh / p.Hkv;
+    const int g = w & (a.groups - 1), bh = w >> (a.groups - 1);  // (one or two groups)
+    u.b = bh / p.Hkv;
+    u.h = bh - u.b * p.Hkv;
+    u.b += a.b0;
     u.index = (static_cast<size_t>(u.b) * p.L + p.layer) * p.Hkv + u.h;
     const int cap = p.Pmax * T;
     int n = p.n_nodes != nullptr ? p.n_nodes[u.b] : p.n_max;
@@ -681,7 +682,7 @@ __device__ __forceinline__ void deal_blocks(const Launch& a, Control& c)
             if (u.rows > 0 && blockIdx.x == 0) write_nothing(a.p, u);
         } else if (before >= start && before < end && before + u.blocks > end) {
             // the unit begins here and goes on, up to the CTA of its last block
-            c.cut = make_int4(w, cta, static_cast<int>((static_cast<long long>(before + u.blocks) * n - 1) / total), 0);
+            c.cut = make_int4(w, cta, static_cast<int>((static_cast<long long>(before + u.blocks) * n - 1) / total), u.rows);
         }
         if (a.by_unit && (u.blocks == 0 ? blockIdx.x == 0 : before >= start && before < end))
             a.cut[w] = u.blocks != 0 && before + u.blocks > end ? c.cut : make_int4(-1, 0, 0, 0);
@@ -825,24 +826,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- the parts of units that fell on several CTAs --------------------------------------
-// A block takes 32 rows of a unit, a lane a row.  With many parts a unit (SLICES = 4) the warps
-// share them, two channel quads a block; with few, a warp takes D / 32 quads over all parts.
+// A block takes 32 rows of a unit, a lane a row.  With many parts a unit (SLICES = 4) its warps share them, and the block
+// takes 32 channels; with few, each warp takes D / 8 channels over all parts.
 constexpr int kJoinWarps = 8;
 
-template <int D, int T, int SLICES>
+template <int D, int SLICES>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch a)
 {
-    constexpr int Q = SLICES == 1 ? D / 32 : 1;  // quads of a warp
-    __shared__ float4 other[SLICES][kJoinWarps / SLICES][32];
+    constexpr int Q = SLICES == 1 ? D / 32 : 4;  // quads of a warp
+    __shared__ float4 other[SLICES > 1 ? kJoinWarps : 1][Q][32];
+    __shared__ float sums[kJoinWarps][32];
     const TreeAttnParams& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slice = SLICES == 1 ? 0 : warp % SLICES, quad0 = SLICES == 1 ? warp * Q : blockIdx.z * 2 + warp / SLICES;
+    const int slice = warp % SLICES, quad0 = (blockIdx.z * (kJoinWarps / SLICES) + warp / SLICES) * Q;
     pdl_wait_then_release();
     const int4 cut = a.cut[blockIdx.x];
-    if (cut.x < 0) return;
-    const Unit u = unit_of<T>(a, cut.x, false);
-    const int row = blockIdx.y * 32 + lane, first = cut.y, last = cut.z;
-    if (blockIdx.y * 32 >= u.rows) return;
+    const int row = blockIdx.y * 32 + lane, first = cut.y, last = cut.z, rows = cut.w;
+    if (cut.x < 0 || blockIdx.y * 32 >= rows) return;
     const int tile = row >> 7, r = min(row & 127, a.tile_rows - 1);  // (a lane without a row reads another's)
     auto part = [&](int cta) { return static_cast<size_t>(2 * cta + (cta == first ? 1 : 0)) * a.tiles + tile; };
     float m = -INFINITY;
@@ -853,32 +853,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch
     for (int i = 0; i < Q; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll 4
-    for (int cta = first; cta <= last; ++cta) {
+    for (int cta = first + slice; cta <= last; cta += SLICES) {
         const float2 ml = a.ml[part(cta) * a.tile_rows + r];
+        const float4* x = a.o + (part(cta) * (D / 4) + quad0) * a.tile_rows + r;
+        float4 y[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) y[i] = x[i * a.tile_rows];
         const float f = ml.y > 0.f ? exp2_fast((ml.x - m) * p.scale_log2) : 0.f;
         l = fmaf(ml.y, f, l);
-        if (SLICES > 1 && (cta - first) % SLICES != slice) continue;
-        const float4* x = a.o + (part(cta) * (D / 4) + quad0) * a.tile_rows + r;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            const float4 y = x[i * a.tile_rows];
-            o[i].x = fmaf(y.x, f, o[i].x);
-            o[i].y = fmaf(y.y, f, o[i].y);
-            o[i].z = fmaf(y.z, f, o[i].z);
-            o[i].w = fmaf(y.w, f, o[i].w);
+            o[i].x = fmaf(y[i].x, f, o[i].x);
+            o[i].y = fmaf(y[i].y, f, o[i].y);
+            o[i].z = fmaf(y[i].z, f, o[i].z);
+            o[i].w = fmaf(y[i].w, f, o[i].w);
         }
     }
     if (SLICES > 1) {
-        other[slice][warp / SLICES][lane] = o[0];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) other[warp][i][lane] = o[i];
+        sums[warp][lane] = l;
         __syncthreads();
         if (slice != 0) return;
-        for (int i = 1; i < SLICES; ++i) {
-            const float4 y = other[i][warp / SLICES][lane];
-            o[0] = make_float4(o[0].x + y.x, o[0].y + y.y, o[0].z + y.z, o[0].w + y.w);
+#pragma unroll
+        for (int k = 1; k < SLICES; ++k) {
+            l += sums[warp + k][lane];
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const float4 y = other[warp + k][i][lane];
+                o[i] = make_float4(o[i].x + y.x, o[i].y + y.y, o[i].z + y.z, o[i].w + y.w);
+            }
         }
     }
-    if (row >= u.rows) return;
-    const size_t at = row_of(p, u, u.row0 + row);
+    if (row >= rows) return;
+    const int bh = cut.x >> (a.groups - 1), b = bh / p.Hkv, g = cut.x & (a.groups - 1);
+    Unit u;
+    u.b = a.b0 + b;
+    u.h = bh - b * p.Hkv;
+    const size_t at = row_of(p, u, g * a.tiles * 128 + row);
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint2* out = reinterpret_cast<uint2*>(p.out + at * D) + quad0;
 #pragma unroll
@@ -1001,9 +1013,9 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
         if (ctas == 1) continue;  // nothing is cut
         const unsigned at = static_cast<unsigned>(a.by_unit ? a.units : ctas), groups32 = (rows + 31) / 32;
         if (ctas > 4ll * a.units)
-            e = launch_pdl(tree_join_kernel<D, T, 4>, dim3(at, groups32, D / 8), dim3(kJoinWarps * 32), 0, stream, a);
+            e = launch_pdl(tree_join_kernel<D, 4>, dim3(at, groups32, D / 32), dim3(kJoinWarps * 32), 0, stream, a);
         else
-            e = launch_pdl(tree_join_kernel<D, T, 1>, dim3(at, groups32), dim3(kJoinWarps * 32), 0, stream, a);
+            e = launch_pdl(tree_join_kernel<D, 1>, dim3(at, groups32), dim3(kJoinWarps * 32), 0, stream, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
