@@ -724,23 +724,37 @@ __device__ __forceinline__ void join_cluster(const Launch& a, const Unit& u, uin
     const uint32_t sums = smem_addr(smem) + 2 * Smem<D>::kTile, ml = sums + a.tiles * 128 * D * 4;
     for (int x = cluster_ctarank() * 256 + threadIdx.x; x < u.rows * (D / 4); x += a.cluster * 256) {
         const int row = x / (D / 4), quad = x % (D / 4);
-        float m = -INFINITY;
-#pragma unroll 4
-        for (int k = 0; k < a.cluster; ++k) m = fmaxf(m, ld_cluster_v2(ml + row * 8, k).x);
+        float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < a.cluster; ++k) {
-            const float2 y = ld_cluster_v2(ml + row * 8, k);
-            const float4 v = ld_cluster_v4(sums + quad_at<D>(row, quad) * 16, k);
-            if (y.y > 0.f) {  // (a CTA without a block has left no sums)
-                const float f = exp2_fast((y.x - m) * p.scale_log2);
-                l = fmaf(y.y, f, l);
-                o.x = fmaf(v.x, f, o.x);
-                o.y = fmaf(v.y, f, o.y);
-                o.z = fmaf(v.z, f, o.z);
-                o.w = fmaf(v.w, f, o.w);
+#pragma unroll 1
+        for (int k0 = 0; k0 < a.cluster; k0 += 8) {  // eight CTAs' loads in flight
+            float2 ml_k[8];
+            float4 o_k[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                ml_k[k] = make_float2(-INFINITY, 0.f);
+                if (k0 + k < a.cluster) {
+                    ml_k[k] = ld_cluster_v2(ml + row * 8, k0 + k);
+                    o_k[k] = ld_cluster_v4(sums + quad_at<D>(row, quad) * 16, k0 + k);
+                }
             }
+            float mn = m;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml_k[k].x);
+            const float f0 = l > 0.f ? exp2_fast((m - mn) * p.scale_log2) : 0.f;
+            m = mn;
+            l *= f0;
+            o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (ml_k[k].y > 0.f) {  // (a CTA without a block has left no sums)
+                    const float f = exp2_fast((ml_k[k].x - m) * p.scale_log2);
+                    l = fmaf(ml_k[k].y, f, l);
+                    o.x = fmaf(o_k[k].x, f, o.x);
+                    o.y = fmaf(o_k[k].y, f, o.y);
+                    o.z = fmaf(o_k[k].z, f, o.z);
+                    o.w = fmaf(o_k[k].w, f, o.w);
+                }
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const size_t at = row_of(p, u, u.row0 + row);
@@ -917,6 +931,7 @@ struct Cut {
 };
 
 constexpr int kShort = 12;
+constexpr int kMaxCluster = 16;
 
 // clusters of c CTAs of this kernel that the device holds at once
 int clusters_at_once(void (*kernel)(Launch, CUtensorMap, CUtensorMap), size_t smem, int c)
@@ -989,7 +1004,7 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
         // blocks: no second launch, and no CTA looks through all units for its own.
         int c = 0;
         if (a.units <= known.sms) {
-            for (c = 1; c < 16 && c < most && a.units * (c + 1) <= known.sms;) {
+            for (c = 1; c < kMaxCluster && c < most && a.units * (c + 1) <= known.sms;) {
                 int& held = known.held[c + 1];
                 if (held == 0) held = clusters_at_once(tree_attn_kernel<D, T>, Smem<D>::kBytes, c + 1);
                 if (held < a.units) break;
