@@ -416,7 +416,7 @@ __device__ __forceinline__ void load_queries(const TreeAttnParams& p, const Unit
     for (int x = 0; x < kLoads; ++x) {
         const int row = row0 + r0 + x * (1024 / D), i = row * magic >> 16;
         v[x] = make_uint4(0, 0, 0, 0);
-        if (row < end) v[x] = *reinterpret_cast<const uint4*>(q + (i * p.Hq + (row - i * p.G)) * D);
+        if (row < end) v[x] = *reinterpret_cast<const uint4*>(q + (static_cast<size_t>(i) * p.Hq + (row - i * p.G)) * D);
     }
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
@@ -442,7 +442,7 @@ __device__ __forceinline__ int quad_at(int row, int quad) { return row * (D / 4)
 
 __device__ __forceinline__ float lse_of(float m, float l, float scale_log2)
 {
-    return l > 0.f ? (m * scale_log2 + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    return l != 0.f ? (m * scale_log2 + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int D, int T>
@@ -556,7 +556,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
             tc_fence_after();
         }
         // the row's result: written whole, or left as a part
-        const bool whole = count == u.blocks && a.cluster == 0;
+        const bool whole = count == u.blocks && a.cluster <= 1;
         const size_t part = (2 * blockIdx.x + (begin > 0 ? 0 : 1)) * a.tiles + (two ? s : 0);
         float f0 = 1.f, f1 = 0.f;
         int c0 = 0, c1 = D / 32;
@@ -566,19 +566,19 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
             if (!groups_meet(c, met)) return;
             const float2 other = c.ml[s ^ 1][r];
             const float m = fmaxf(ref, other.x);
-            const float mine_f = l > 0.f ? exp2_fast((ref - m) * scale) : 0.f;
-            const float other_f = other.y > 0.f ? exp2_fast((other.x - m) * scale) : 0.f;
+            const float mine_f = l != 0.f ? exp2_fast((ref - m) * scale) : 0.f;
+            const float other_f = other.y != 0.f ? exp2_fast((other.x - m) * scale) : 0.f;
             f0 = s == 0 ? mine_f : other_f;
             f1 = s == 0 ? other_f : mine_f;
-            l = l * mine_f + other.y * other_f;
+            l = l * mine_f + other.y * other_f;  // (a sum is 0 only where nothing was seen: NaN goes through)
             ref = m;
             c0 = s * (D / 64);
             c1 = c0 + D / 64;
         }
         // (a cluster's CTA has one piece: behind the meeting the ring is free, and its sums go there)
-        if (two && a.cluster > 0 && !groups_meet(c, met)) return;
+        if (two && a.cluster > 1 && !groups_meet(c, met)) return;
         if (busy) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l != 0.f ? 1.f / l : 0.f;
             const size_t at = r < rows ? row_of(p, u, row) : 0;
             for (int i = c0; i < c1; ++i) {
                 uint32_t x[32], y[32];
@@ -595,9 +595,9 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
                 if (r < rows) {
                     if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = l > 0.f ? o[e] * inv : 0.f;
+                        for (int e = 0; e < 32; ++e) o[e] = l != 0.f ? o[e] * inv : 0.f;
                         store_out32(p.out + at * D + 32 * i, o);
-                    } else if (a.cluster > 0) {
+                    } else if (a.cluster > 1) {
                         float4* dst = reinterpret_cast<float4*>(smem + 2 * Smem<D>::kTile);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -611,7 +611,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
                 }
             }
             if (r < rows && (two || s == 0)) {
-                if (a.cluster > 0)
+                if (a.cluster > 1)
                     reinterpret_cast<float2*>(smem + 2 * Smem<D>::kTile + a.tiles * 128 * D * 4)[two ? s * 128 + r : r] =
                         make_float2(ref, l);
                 else if (!whole)
@@ -741,13 +741,13 @@ __device__ __forceinline__ void join_cluster(const Launch& a, const Unit& u, uin
             float mn = m;
 #pragma unroll
             for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml_k[k].x);
-            const float f0 = l > 0.f ? exp2_fast((m - mn) * p.scale_log2) : 0.f;
+            const float f0 = l != 0.f ? exp2_fast((m - mn) * p.scale_log2) : 0.f;
             m = mn;
             l *= f0;
             o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (ml_k[k].y > 0.f) {  // (a CTA without a block has left no sums)
+                if (ml_k[k].y != 0.f) {  // (a CTA without a block has left no sums)
                     const float f = exp2_fast((ml_k[k].x - m) * p.scale_log2);
                     l = fmaf(ml_k[k].y, f, l);
                     o.x = fmaf(o_k[k].x, f, o.x);
@@ -756,7 +756,7 @@ __device__ __forceinline__ void join_cluster(const Launch& a, const Unit& u, uin
                     o.w = fmaf(o_k[k].w, f, o.w);
                 }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
         const size_t at = row_of(p, u, u.row0 + row);
         reinterpret_cast<uint2*>(p.out + at * D)[quad] =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -809,6 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.unit = unit_of<T>(a, c.w0, rank == 0);
         c.off0 = c.unit.blocks * rank / a.cluster;
         c.left = c.unit.blocks * (rank + 1) / a.cluster - c.off0;
+        if (a.cluster == 1 && c.unit.blocks == 0 && c.unit.rows > 0) write_nothing(a.p, c.unit);
     }
     __syncthreads();
     tc_fence_after();
@@ -828,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (a.cluster > 0) {
+    if (a.cluster > 1) {
         if (c.left == 0 && tid < a.tiles * 128)  // nothing was summed here
             reinterpret_cast<float2*>(smem + 2 * S::kTile + a.tiles * 128 * D * 4)[tid] = make_float2(-INFINITY, 0.f);
         cluster_sync();
@@ -873,7 +874,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch
         float4 y[Q];
 #pragma unroll
         for (int i = 0; i < Q; ++i) y[i] = x[i * a.tile_rows];
-        const float f = ml.y > 0.f ? exp2_fast((ml.x - m) * p.scale_log2) : 0.f;
+        const float f = ml.y != 0.f ? exp2_fast((ml.x - m) * p.scale_log2) : 0.f;
         l = fmaf(ml.y, f, l);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch
     u.b = a.b0 + b;
     u.h = bh - b * p.Hkv;
     const size_t at = row_of(p, u, g * a.tiles * 128 + row);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     uint2* out = reinterpret_cast<uint2*>(p.out + at * D) + quad0;
 #pragma unroll
     for (int i = 0; i < Q; ++i)
@@ -930,7 +931,7 @@ struct Cut {
     size_t ml_bytes() const { return round256(sizeof(float2) * rows()); }
 };
 
-constexpr int kShort = 12;
+constexpr int kShort = 17;  // blocks x tiles of a CTA up to which a cluster takes a unit, over every page
 constexpr int kMaxCluster = 16;
 
 // clusters of c CTAs of this kernel that the device holds at once
@@ -1000,8 +1001,13 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
     for (a.b0 = 0; a.b0 < p.B; a.b0 += cut.batches) {
         a.nb = p.B - a.b0 < cut.batches ? p.B - a.b0 : cut.batches;
         a.units = a.nb * p.Hkv * cut.groups;
-        // A cluster a unit, of the most CTAs whose clusters all run at once, where no CTA then takes more than kShort
-        // blocks: no second launch, and no CTA looks through all units for its own.
+        // A cluster a unit, of the most CTAs whose clusters all run at once, where no CTA then takes many blocks: no second
+        // launch, and no CTA looks through all units for its own.  One sequence of 8 KV heads, 4 query heads each, trees of
+        // 8: 13.9 us against 19.1 for 4K tokens, 24.1 against 26.9 for 16K, 31.6 against 32.7 for 24K, 38.0 against 37.3
+        // for 32K (17 blocks a CTA), four sequences of 8K (17 blocks) 32.8 against 38.1; trees of 64 (two tiles, a block twice the work) 25.6 against 26.4 for 8K, 33.2 against
+        // 31.7 for 16K (8 blocks).  Selections are mostly as long as Kmax, so no cluster waits for a longer one: eight
+        // sequences, 300 pages a head (20 blocks a CTA) 38.7 against 44.2; ragged sequences of up to 16K (128 blocks)
+        // 154 against 133.
         int c = 0;
         if (a.units <= known.sms) {
             for (c = 1; c < kMaxCluster && c < most && a.units * (c + 1) <= known.sms;) {
@@ -1011,7 +1017,7 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
                 ++c;
             }
         }
-        a.cluster = c > 0 && (most + c - 1) / c <= kShort ? c : 0;
+        a.cluster = c > 0 && (most + c - 1) / c * cut.tiles <= (p.sel_idx != nullptr ? 2 * kShort : kShort) ? c : 0;
         if (a.cluster > 0) {
             e = launch_pdl_cluster(tree_attn_kernel<D, T>, dim3(static_cast<unsigned>(a.units * c)), dim3(kThreads),
                                    Smem<D>::kBytes, stream, static_cast<unsigned>(c), a, kmap, vmap);

@@ -359,6 +359,51 @@ def test_pool_beyond_32_bit_offsets():
     c.check()
 
 
+@pytest.mark.parametrize("n,G", [(6, 4), (40, 8), (64, 8)])
+@pytest.mark.parametrize("K", [0, 12])
+@pytest.mark.parametrize("lens", [[500], [500, 3, 0, 129, 900], [60] * 37])
+def test_short_sequences_of_a_long_table(lens, n, G, K):
+    """A table for far longer sequences: the blocks are dealt to the SMs where a table of their length has clusters."""
+    for Pmax in (None, 6000):
+        c = Case(lens, [n] * len(lens), n, Hkv=2, G=G, D=64, K=K, seed=40, Pmax=Pmax)
+        if K and Pmax:  # and selections far shorter than their list may be
+            wide = torch.zeros(c.B, 1, 2, 4000, dtype=torch.int32, device="cuda")
+            wide[..., :K] = c.sel
+            c.sel, c.shape.Kmax = wide, 4000
+        c.call()
+        c.check()
+
+
+def test_more_units_than_one_launch_takes():
+    c = Case([(5 * b) % 90 for b in range(300)], [1 + b % 3 for b in range(300)], 3, Hkv=8, G=1, D=64, seed=41, Pmax=7)
+    c.call()
+    c.check()
+
+
+def test_a_batch_of_nothing_but_empty_rows():
+    """Selections of no page and nodes without a place: zeros and -inf, whichever way the units are taken."""
+    for Pmax, B in ((16, 1), (16, 90), (2000, 3)):
+        c = Case([Pmax * 16] * B, [3] * B, 3, Hkv=2, G=4, D=64, seed=42, Pmax=Pmax, K=2)
+        c.cnt.zero_()
+        c.call()
+        torch.cuda.synchronize()
+        assert int(c.err) == kvmm.ERR_OUT_OF_RANGE
+        assert (c.out == 0).all() and torch.isneginf(c.lse).all()
+
+
+def test_nan_in_a_query_stays_in_its_row():
+    for lens in ([300], [40000]):
+        c = Case(lens, [5], 5, Hkv=1, G=4, D=64, seed=43)
+        c.call()
+        want = c.out.clone()
+        c.q[0, 2, 1, 7] = math.nan
+        c.call()
+        torch.cuda.synchronize()
+        assert c.out[0, 2, 1].isnan().all() and c.lse[0, 2, 1].isnan()
+        want[0, 2, 1] = c.out[0, 2, 1] = 0
+        assert torch.equal(want, c.out)
+
+
 def test_refusals():
     c = Case([20], [4], 4, Hkv=1, seed=1)
     for kw, what in ((dict(tree_mask=c.mask[:, :3]), "tree_mask"), (dict(lse=c.lse[:, :3]), "lse"),
