@@ -14,14 +14,25 @@
 // swizzle of their rows (128 bytes for keys, 32 or 64 for values).
 //
 // A CTA's warps: two groups of four for the softmax of two streams (a thread a
-// row), one that copies, one that issues the products.  The streams alternate
-// on the tensor cores: two row tiles over the same blocks, or, with at most
-// 128 rows, one tile over every other block, joined at the end from tensor
-// memory.
+// row), one that copies, one whose elected thread issues the products.  The
+// streams alternate on the tensor cores: two row tiles over the same blocks, or,
+// with at most 128 rows, one tile over every other block, joined at the end from
+// tensor memory.  128 rows are the tensor cores' own tile; fewer rows leave part
+// of it unused, which costs nothing as long as the memory is the bound: a block
+// (64 KB with 128 channels) takes 2,800 cycles at a copy's rate, its products
+// about 1,500 a tile, its softmax 1,450 (128 exponentials a row at 16 a clock and
+// SM).  Two tiles take 3,000 of products, so the largest trees are bound by them.
 //
-// The blocks of all units are dealt evenly to one CTA an SM.  A unit that
-// falls on several CTAs leaves parts in the workspace, which a second launch
-// joins.
+// Short units take a cluster of CTAs each, joined through distributed shared
+// memory.  Otherwise the blocks of all units are dealt evenly to one CTA an SM,
+// whatever the sequences' lengths; a unit that falls on several CTAs leaves parts
+// in the workspace, which a second launch joins.
+//
+// Times (us in a row; the floor is the bytes at a copy's rate): one 128K sequence,
+// 8 KV heads, 64 nodes x 4 heads 110 (79; 137 GFLOP, 1,250 TFLOP/s); 16 ragged
+// sequences of up to 16K tokens, pages of 32, 13 nodes x 5 heads 133 (116); eight
+// sequences, 128 selected pages, 16 nodes 25.2 (10.3); one of 4K 14.5 (2.5), which is
+// latency: lengths, table entry, first block 4.5, products and softmax 2.5, join 4.
 #include <cstdint>
 
 #include "kernels.h"
