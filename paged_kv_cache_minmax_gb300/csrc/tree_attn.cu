@@ -109,6 +109,7 @@ struct BlockMask {
     int32_t node0[kTokens / 16];
     int32_t whole;  // every slot is a settled token's
     int32_t held;   // nodes of the sequence
+    int32_t pages;  // up to the last that was copied (1 at least): what lies behind is not multiplied
 };
 
 struct Control {
@@ -250,6 +251,7 @@ __device__ void copy_pages(const Launch& a, const CUtensorMap* kmap, const CUten
                         if (lane == 0) {
                             m.whole = (all & lanes) == lanes;
                             m.held = u.held;
+                            m.pages = max(32 - __clz((some & lanes) >> (j * kPages)), 1);
                         }
                         ++nth;
                     }
@@ -286,8 +288,8 @@ __device__ void copy_pages(const Launch& a, const CUtensorMap* kmap, const CUten
 template <int D, int T>
 __device__ __noinline__ void clear_unseen(uint8_t* values, const BlockMask& m)
 {
-    constexpr int kPages = kTokens / T, kChunks = T / 8;
-    for (int i = 0; i < kPages; ++i) {
+    constexpr int kChunks = T / 8;
+    for (int i = 0; i < m.pages; ++i) {
         uint32_t seen = m.settled[i];
         const int from = max(m.node0[i], 0), to = min(m.node0[i] + T, m.held);  // its nodes (none: from >= to)
         if (from < to) seen |= ((to - from >= 32 ? 0u : 1u << (to - from)) - 1u) << (from - m.node0[i]);
@@ -330,7 +332,7 @@ __device__ void issue_products(const Launch& a, uint8_t* smem, Control& c, Walk 
             phase ^= 1;
         }
     };
-    uint32_t piece = 0, p_phase = 0;  // a bit a stream
+    uint32_t piece = 0, nth = 0, p_phase = 0;  // (a bit a stream)
     bool fine = true;
     Unit u;
     int begin, count;
@@ -372,10 +374,11 @@ __device__ void issue_products(const Launch& a, uint8_t* smem, Control& c, Walk 
             tc_fence_after();
             const uint64_t vv = matrix_at(rowsT, ring + v_slot * S::kTile);
             mma_ts(tmem + 256 + s * 128, tmem + s * 128, vv, pv, v > 1);  // (the first of the stream's in this piece: not added)
+            const int sixteens = c.mask[(nth + (two ? v >> 1 : v)) % kRing].pages * (T / 16);
 #pragma unroll
             for (int i = 1; i < kTokens / 16; ++i) {
                 const uint32_t off = ((i * 16 / T) * (T * D * 2) + (i * 16 % T) * 2) >> 4;
-                mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, vv + off, pv, true);
+                if (i < sixteens) mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, vv + off, pv, true);
             }
             if (last) {
                 mma_commit(&c.empty[v_slot]);
@@ -386,6 +389,7 @@ __device__ void issue_products(const Launch& a, uint8_t* smem, Control& c, Walk 
             else
                 mma_commit(&c.o_done[s]);
         }
+        nth += count;
     }
     if (!fine) {  // products in flight end before the CTA does
         mma_commit(&c.drain);
@@ -733,7 +737,8 @@ __device__ __forceinline__ void join_cluster(const Launch& a, const Unit& u, uin
 {
     const TreeAttnParams& p = a.p;
     const uint32_t sums = smem_addr(smem) + 2 * Smem<D>::kTile, ml = sums + a.tiles * 128 * D * 4;
-    for (int x = cluster_ctarank() * 256 + threadIdx.x; x < u.rows * (D / 4); x += a.cluster * 256) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int x = (warp * a.cluster + cluster_ctarank()) * 32 + lane; x < u.rows * (D / 4); x += a.cluster * 256) {
         const int row = x / (D / 4), quad = x % (D / 4);
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -818,8 +823,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.w0 = blockIdx.x / a.cluster;
         const int rank = cluster_ctarank();
         c.unit = unit_of<T>(a, c.w0, rank == 0);
-        c.off0 = c.unit.blocks * rank / a.cluster;
-        c.left = c.unit.blocks * (rank + 1) / a.cluster - c.off0;
+        // (rounded up: the last CTA, whose last block has masks, does not get the odd blocks too)
+        c.off0 = (c.unit.blocks * rank + a.cluster - 1) / a.cluster;
+        c.left = (c.unit.blocks * (rank + 1) + a.cluster - 1) / a.cluster - c.off0;
         if (a.cluster == 1 && c.unit.blocks == 0 && c.unit.rows > 0) write_nothing(a.p, c.unit);
     }
     __syncthreads();
