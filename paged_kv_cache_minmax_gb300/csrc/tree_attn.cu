@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch
 {
     constexpr int Q = SLICES == 1 ? D / 32 : 4;  // quads of a warp
     __shared__ float4 other[SLICES > 1 ? kJoinWarps : 1][Q][32];
-    __shared__ float sums[kJoinWarps][32];
+    __shared__ float2 sums[kJoinWarps][32];
     const TreeAttnParams& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slice = warp % SLICES, quad0 = (blockIdx.z * (kJoinWarps / SLICES) + warp / SLICES) * Q;
@@ -875,45 +875,74 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch
     const int4 cut = a.cut[blockIdx.x];
     const int row = blockIdx.y * 32 + lane, first = cut.y, last = cut.z, rows = cut.w;
     if (cut.x < 0 || blockIdx.y * 32 >= rows) return;
-    const int tile = row >> 7, r = min(row & 127, a.tile_rows - 1);  // (a lane without a row reads another's)
+    const int tile = row >> 7, r = min(row & 127, a.tile_rows - 1);  // (a lane without a row reads what lies there)
     auto part = [&](int cta) { return static_cast<size_t>(2 * cta + (cta == first ? 1 : 0)) * a.tiles + tile; };
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int cta = first; cta <= last; ++cta) m = fmaxf(m, a.ml[part(cta) * a.tile_rows + r].x);
+    constexpr int kAhead = Q > 2 ? 2 : 4;  // parts whose loads are in flight
+    float m = -INFINITY, l = 0.f;
     float4 o[Q];
 #pragma unroll
     for (int i = 0; i < Q; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int cta = first + slice; cta <= last; cta += SLICES) {
-        const float2 ml = a.ml[part(cta) * a.tile_rows + r];
-        const float4* x = a.o + (part(cta) * (D / 4) + quad0) * a.tile_rows + r;
-        float4 y[Q];
+#pragma unroll 1
+    for (int cta0 = first + slice; cta0 <= last; cta0 += kAhead * SLICES) {
+        float2 ml[kAhead];
+        float4 y[kAhead][Q];
 #pragma unroll
-        for (int i = 0; i < Q; ++i) y[i] = x[i * a.tile_rows];
-        const float f = ml.y != 0.f ? exp2_fast((ml.x - m) * p.scale_log2) : 0.f;
-        l = fmaf(ml.y, f, l);
+        for (int k = 0; k < kAhead; ++k) {
+            const int cta = cta0 + k * SLICES;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (cta <= last) {
+                ml[k] = a.ml[part(cta) * a.tile_rows + r];
+                const float4* x = a.o + (part(cta) * (D / 4) + quad0) * a.tile_rows + r;
 #pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            o[i].x = fmaf(y[i].x, f, o[i].x);
-            o[i].y = fmaf(y[i].y, f, o[i].y);
-            o[i].z = fmaf(y[i].z, f, o[i].z);
-            o[i].w = fmaf(y[i].w, f, o[i].w);
+                for (int i = 0; i < Q; ++i) y[k][i] = x[i * a.tile_rows];
+            }
+        }
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) mn = fmaxf(mn, ml[k].x);
+        const float f0 = l != 0.f ? exp2_fast((m - mn) * p.scale_log2) : 0.f;
+        m = mn;
+        l *= f0;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) o[i] = make_float4(o[i].x * f0, o[i].y * f0, o[i].z * f0, o[i].w * f0);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (ml[k].y == 0.f) continue;
+            const float f = exp2_fast((ml[k].x - m) * p.scale_log2);
+            l = fmaf(ml[k].y, f, l);
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                o[i].x = fmaf(y[k][i].x, f, o[i].x);
+                o[i].y = fmaf(y[k][i].y, f, o[i].y);
+                o[i].z = fmaf(y[k][i].z, f, o[i].z);
+                o[i].w = fmaf(y[k][i].w, f, o[i].w);
+            }
         }
     }
     if (SLICES > 1) {
 #pragma unroll
         for (int i = 0; i < Q; ++i) other[warp][i][lane] = o[i];
-        sums[warp][lane] = l;
+        sums[warp][lane] = make_float2(m, l);
         __syncthreads();
         if (slice != 0) return;
+        float most = m;
+#pragma unroll
+        for (int k = 1; k < SLICES; ++k) most = fmaxf(most, sums[warp + k][lane].x);
+        const float f0 = l != 0.f ? exp2_fast((m - most) * p.scale_log2) : 0.f;
+        m = most;
+        l *= f0;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) o[i] = make_float4(o[i].x * f0, o[i].y * f0, o[i].z * f0, o[i].w * f0);
 #pragma unroll
         for (int k = 1; k < SLICES; ++k) {
-            l += sums[warp + k][lane];
+            const float2 ml = sums[warp + k][lane];
+            if (ml.y == 0.f) continue;
+            const float f = exp2_fast((ml.x - m) * p.scale_log2);
+            l = fmaf(ml.y, f, l);
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
                 const float4 y = other[warp + k][i][lane];
-                o[i] = make_float4(o[i].x + y.x, o[i].y + y.y, o[i].z + y.z, o[i].w + y.w);
+                o[i] = make_float4(fmaf(y.x, f, o[i].x), fmaf(y.y, f, o[i].y), fmaf(y.z, f, o[i].z), fmaf(y.w, f, o[i].w));
             }
         }
     }
