@@ -31,6 +31,7 @@ constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerCluster = 16;
 constexpr int kStep = 128;  // entries a warp takes at once, four a lane
+constexpr int kAhead = 4;   // steps whose loads are in flight
 constexpr long long kWhole = 1ll << 53;
 
 // floor(x * 2^53) of x clamped to [0, 512] (NaN: 0).  x = m * 2^(e - 150), m with its hidden bit: m * 2^39 shifted right
@@ -128,6 +129,7 @@ struct Shared {
     float u[kTreeMaxNodes], factor[kTreeMaxNodes];
     float p[kTreeMaxNodes], q[kTreeMaxNodes];          // a node's token in its parent's rows
     unsigned long long children[kTreeMaxNodes];        // bits
+    int first[kTreeMaxNodes];                          // whether a node is accepted where it is its parent's first to be tried
     long long part[kVerWarps];                         // the warps' sums of a pass
     long long totals[2][kVerCluster];                  // the CTAs', by the pass's parity
     int cur, rejected, len, ask;                       // ask: a sum is wanted for the walk
@@ -147,7 +149,6 @@ __device__ __forceinline__ long long row_sum(const Row& r, int V, int run, int c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_ctarank();
     const long long first = static_cast<long long>(rank * kVerWarps + warp) * run;
     const long long end = min(first + run, static_cast<long long>(V));
-    constexpr int kAhead = 4;  // steps whose loads are in flight
     long long s = 0;
     // One pass for what is met most, a row as it is and a row less the draft's once: P - Q where p > q and nothing where
     // not, which is P less the weight of min(p, q), as floor() ascends.  19 instructions an entry, most of them fp32,
@@ -242,8 +243,12 @@ __global__ void __launch_bounds__(kVerThreads, 4) draft_verify_kernel(const Veri
         sh.u[tid] = p.u_accept[at + tid];
         if (tid > 0) {
             if (t >= 0 && t < p.V && from >= 0 && from < tid) {
-                sh.p[tid] = p.target[(at + from) * p.target_stride + t];
-                sh.q[tid] = p.draft != nullptr ? p.draft[(at + from) * p.draft_stride + t] : 0.f;
+                const float pt = p.target[(at + from) * p.target_stride + t];
+                const float qt = p.draft != nullptr ? p.draft[(at + from) * p.draft_stride + t] : 0.f;
+                const long long c = p.draft != nullptr ? weight_of(qt) : kWhole;
+                sh.p[tid] = pt;
+                sh.q[tid] = qt;
+                sh.first[tid] = static_cast<double>(sh.u[tid]) * static_cast<double>(c) < static_cast<double>(weight_of(pt));
                 atomicOr(&sh.children[from], 1ull << tid);
             } else if (rank == 0) {
                 report(p.err, KVMM_ERR_OUT_OF_RANGE);
@@ -269,19 +274,24 @@ __global__ void __launch_bounds__(kVerThreads, 4) draft_verify_kernel(const Veri
             while (left != 0) {
                 const int i = __ffsll(static_cast<long long>(left)) - 1, x = sh.token[i];
                 left &= left - 1;
-                r.q = p.draft;
-                r.rejected = sh.rejected;
-                const long long w = residual(r, sh.p[i], sh.q[i], x);
-                long long c = W;
-                float f = 0.f;
-                if (p.draft != nullptr) {
-                    if (W == kWhole && Q == 1.0)
-                        f = 1.f;  // (as the division gives)
-                    else if (W > 0 && Q > 0.0)
-                        f = static_cast<float>(static_cast<double>(W) * 0x1p-53 / Q);
-                    c = weight_of(__fmul_rn(sh.q[i], f));
+                long long w = 0;
+                float f = 1.f;  // (of a first child: W / 2^53 and Q are 1)
+                bool accepted;
+                if (sh.rejected == 0) {
+                    accepted = sh.first[i] != 0;
+                    w = weight_of(sh.p[i]);
+                } else {
+                    r.q = p.draft;
+                    r.rejected = sh.rejected;
+                    w = residual(r, sh.p[i], sh.q[i], x);
+                    long long c = W;
+                    if (p.draft != nullptr) {
+                        f = W > 0 && Q > 0.0 ? static_cast<float>(static_cast<double>(W) * 0x1p-53 / Q) : 0.f;
+                        c = weight_of(__fmul_rn(sh.q[i], f));
+                    }
+                    accepted = static_cast<double>(sh.u[i]) * static_cast<double>(c) < static_cast<double>(w);
                 }
-                if (static_cast<double>(sh.u[i]) * static_cast<double>(c) < static_cast<double>(w)) {
+                if (accepted) {
                     sh.cur = i;
                     sh.path[sh.len++] = i;
                     sh.rejected = 0;
@@ -327,33 +337,46 @@ __global__ void __launch_bounds__(kVerThreads, 4) draft_verify_kernel(const Veri
     for (owner = 0; owner < kVerWarps - 1 && before + sh.part[owner] <= goal; ++owner) before += sh.part[owner];
     if (warp != owner) return;
     const long long first = static_cast<long long>(rank * kVerWarps + warp) * run;
-    int drawn = p.V - 1;
-    for (long long x = first + 4 * lane; x - 4 * lane < min(first + run, static_cast<long long>(p.V)); x += kStep) {
-        const float4 pp = entries4(r.p, x, p.V);
-        const float4 qq = r.q != nullptr ? entries4(r.q, x, p.V) : make_float4(0.f, 0.f, 0.f, 0.f);
-        long long w[4];
-        residual4(r, pp, qq, static_cast<int>(x), w);
-        const long long mine = (w[0] + w[1]) + (w[2] + w[3]);
-        long long upto = mine;
+    const long long end = min(first + run, static_cast<long long>(p.V));
+    int drawn = -1;
+#pragma unroll 1
+    for (long long x0 = first + 4 * lane; x0 - 4 * lane < end && drawn < 0; x0 += kAhead * kStep) {
+        float4 pp[kAhead], qq[kAhead];
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(kFullMask, upto, off);
-            if (lane >= off) upto += y;
-        }
-        const uint32_t over = __ballot_sync(kFullMask, before + upto > goal);
-        if (over != 0) {
-            long long c = before + upto - mine;
-            int k = 0;
-            for (; k < 3; ++k) {
-                c += w[k];
-                if (c > goal) break;
+        for (int i = 0; i < kAhead; ++i) {
+            const long long x = x0 + i * kStep;
+            pp[i] = qq[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < end) {
+                pp[i] = entries4(r.p, x, p.V);
+                if (r.q != nullptr) qq[i] = entries4(r.q, x, p.V);
             }
-            drawn = min(static_cast<int>(x) + k, p.V - 1);
-            drawn = __shfl_sync(kFullMask, drawn, __ffs(over) - 1);
-            break;
         }
-        before += __shfl_sync(kFullMask, upto, 31);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int x = static_cast<int>(x0) + i * kStep;
+            long long w[4];
+            residual4(r, pp[i], qq[i], x, w);
+            const long long mine = (w[0] + w[1]) + (w[2] + w[3]);
+            long long upto = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(kFullMask, upto, off);
+                if (lane >= off) upto += y;
+            }
+            const uint32_t over = __ballot_sync(kFullMask, before + upto > goal);
+            if (over != 0 && drawn < 0) {
+                long long c = before + upto - mine;
+                int k = 0;
+                for (; k < 3; ++k) {
+                    c += w[k];
+                    if (c > goal) break;
+                }
+                drawn = __shfl_sync(kFullMask, min(x + k, p.V - 1), __ffs(over) - 1);
+            }
+            before += __shfl_sync(kFullMask, upto, 31);
+        }
     }
+    if (drawn < 0) drawn = p.V - 1;
     const int len = sh.len;
     for (int i = lane; i < p.n_max; i += 32) {
         p.path[at + i] = i < len ? sh.path[i] : -1;
