@@ -21,6 +21,8 @@
 // about 3 each; one chain of four, 32,000 tokens 7.1 (0.04).  The large case is
 // bound by the instructions of its pass, the small ones by the chain of loads (the
 // nodes, their probabilities, the row) and the cluster's barriers.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -132,6 +134,10 @@ struct Shared {
     int first[kTreeMaxNodes];                          // whether a node is accepted where it is its parent's first to be tried
     long long part[kVerWarps];                         // the warps' sums of a pass
     long long totals[2][kVerCluster];                  // the CTAs', by the pass's parity
+    long long before;                                  // the drawn token's: what lies before its warp's run
+    long long goal;
+    int owner;                                         // its warp, -1: in another CTA
+    float u_next;
     int cur, rejected, len, ask;                       // ask: a sum is wanted for the walk
 };
 
@@ -157,33 +163,46 @@ __device__ __forceinline__ long long row_sum(const Row& r, int V, int run, int c
     uint32_t odd = 0;  // an exponent of 2 or more, or a sign: no probability, the general pass is right for it
     if (plain) {
         const float f = r.q != nullptr ? r.f[0] : 0.f;
+        // steps of both rows, or twice as many of one, in flight
+        auto steps = [&](auto both) {
+            constexpr bool kBoth = decltype(both)::value;
+            constexpr int kN = kBoth ? kAhead : 2 * kAhead;
 #pragma unroll 1
-        for (long long x0 = first + 4 * lane; x0 < end; x0 += kAhead * kStep) {
-            float4 p[kAhead], q[kAhead];
+            for (long long x0 = first + 4 * lane; x0 < end; x0 += kN * kStep) {
+                float4 p[kN], q[kBoth ? kN : 1];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const long long x = x0 + i * kStep;
-                p[i] = q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (x < end) {
-                    p[i] = entries4(r.p, x, V);
-                    if (r.q != nullptr) q[i] = entries4(r.q, x, V);
+                for (int i = 0; i < kN; ++i) {
+                    const long long x = x0 + i * kStep;
+                    p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (kBoth) q[i] = p[i];
+                    if (x < end) {
+                        p[i] = entries4(r.p, x, V);
+                        if (kBoth) q[i] = entries4(r.q, x, V);
+                    }
                 }
-            }
-            int d1 = 0, d2 = 0, d3 = 0;  // 16 entries' digits of 22 bits at most
+                int d1 = 0, d2 = 0, d3 = 0;  // 16 entries' digits of 22 bits, or 32 entries', less those of a zero
+                const Digits zero = digits_of(0.f);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const float pp[4] = {p[i].x, p[i].y, p[i].z, p[i].w}, qq[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                for (int i = 0; i < kN; ++i) {
+                    const float pp[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
+                    const float4 c = kBoth ? q[kBoth ? i : 0] : p[i];
+                    const float qq[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    odd |= __float_as_uint(pp[k]);
-                    const Digits a = digits_of(pp[k]), b = digits_of(fminf(__fmul_rn(qq[k], f), pp[k]));
-                    d1 += a.d1 - b.d1;
-                    d2 += a.d2 - b.d2;
-                    d3 += a.d3 - b.d3;
+                    for (int k = 0; k < 4; ++k) {
+                        odd |= __float_as_uint(pp[k]);
+                        const Digits a = digits_of(pp[k]), b = kBoth ? digits_of(fminf(__fmul_rn(qq[k], f), pp[k])) : zero;
+                        d1 += a.d1 - b.d1;
+                        d2 += a.d2 - b.d2;
+                        d3 += a.d3 - b.d3;
+                    }
                 }
+                s += (static_cast<long long>(d1) << 32) + (static_cast<long long>(d2) << 10) + d3;
             }
-            s += (static_cast<long long>(d1) << 32) + (static_cast<long long>(d2) << 10) + d3;
-        }
+        };
+        if (r.q != nullptr)
+            steps(std::true_type{});
+        else
+            steps(std::false_type{});
         if (r.q == nullptr)  // less the rejected candidates, each once
             for (int k = lane; k < r.rejected; k += 32) {
                 const int x = r.gone[k];
@@ -257,6 +276,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) draft_verify_kernel(const Veri
     }
     if (tid == 0) {
         sh.cur = sh.rejected = 0;
+        sh.u_next = p.u_next[b];
         sh.path[0] = 0;
         sh.len = 1;
     }
@@ -327,15 +347,21 @@ __global__ void __launch_bounds__(kVerThreads, 4) draft_verify_kernel(const Veri
         W = row_sum(r, p.V, run, ctas, parity, sh);
         parity ^= 1;
     }
-    long long goal = static_cast<long long>(static_cast<double>(p.u_next[b]) * static_cast<double>(W));
-    goal = min(goal, W - 1);
-    // the CTA whose entries hold the goal, its warp, then the entry
-    long long before = 0;
-    int owner = 0;
-    for (; owner < ctas - 1 && before + sh.totals[parity ^ 1][owner] <= goal; ++owner) before += sh.totals[parity ^ 1][owner];
-    if (owner != rank) return;
-    for (owner = 0; owner < kVerWarps - 1 && before + sh.part[owner] <= goal; ++owner) before += sh.part[owner];
-    if (warp != owner) return;
+    if (tid == 0) {  // the CTA whose entries hold the goal, and its warp
+        const long long goal = min(static_cast<long long>(static_cast<double>(sh.u_next) * static_cast<double>(W)), W - 1);
+        const long long* totals = sh.totals[parity ^ 1];
+        long long before = 0;
+        int cta = 0, owner = 0;
+        for (; cta < ctas - 1 && before + totals[cta] <= goal; ++cta) before += totals[cta];
+        for (; cta == rank && owner < kVerWarps - 1 && before + sh.part[owner] <= goal; ++owner) before += sh.part[owner];
+        sh.goal = goal;
+        sh.before = before;
+        sh.owner = cta == rank ? owner : -1;
+    }
+    __syncthreads();
+    if (warp != sh.owner) return;
+    const long long goal = sh.goal;
+    long long before = sh.before;
     const long long first = static_cast<long long>(rank * kVerWarps + warp) * run;
     const long long end = min(first + run, static_cast<long long>(p.V));
     int drawn = -1;
