@@ -15,9 +15,9 @@
 // token: the CTA, the warp, then one look at that warp's run again.
 //
 // Times (us in a row; the floor is the rows drawn from at a copy's rate): chains of
-// seven for 64 sequences, 131,072 tokens 24.8 (9.9); trees of 24 certain candidates
-// for 16 12.3 (1.2); trees of 16 drawn without replacement for 8, 100,003 tokens
-// 15.1 (0.9): a pass over the row for every rejected child that has a sibling left,
+// seven for 64 sequences, 131,072 tokens 23.5 (9.9); trees of 24 certain candidates
+// for 16 10.8 (1.2); trees of 16 drawn without replacement for 8, 100,003 tokens
+// 14.4 (0.9): a pass over the row for every rejected child that has a sibling left,
 // about 3 each; one chain of four, 32,000 tokens 7.1 (0.04).  The large case is
 // bound by the instructions of its pass, the small ones by the chain of loads (the
 // nodes, their probabilities, the row) and the cluster's barriers.

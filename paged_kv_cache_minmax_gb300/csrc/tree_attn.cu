@@ -29,10 +29,10 @@
 // in the workspace, which a second launch joins.
 //
 // Times (us in a row; the floor is the bytes at a copy's rate): one 128K sequence,
-// 8 KV heads, 64 nodes x 4 heads 110 (79; 137 GFLOP, 1,250 TFLOP/s); 16 ragged
-// sequences of up to 16K tokens, pages of 32, 13 nodes x 5 heads 133 (116); eight
-// sequences, 128 selected pages, 16 nodes 25.2 (10.3); one of 4K 14.5 (2.5), which is
-// latency: lengths, table entry, first block 4.5, products and softmax 2.5, join 4.
+// 8 KV heads, 64 nodes x 4 heads 108 (79; 137 GFLOP, 1,270 TFLOP/s); 16 ragged
+// sequences of up to 16K tokens, pages of 32, 13 nodes x 5 heads 130 (116); eight
+// sequences, 128 selected pages, 16 nodes 24.0 (10.3); one of 4K 12.5 (2.5), which is
+// latency: lengths, table entry, first block 3.7, products and softmax 4, join 3.
 #include <cstdint>
 
 #include "kernels.h"
@@ -977,7 +977,7 @@ struct Cut {
     size_t ml_bytes() const { return round256(sizeof(float2) * rows()); }
 };
 
-constexpr int kShort = 17;  // blocks x tiles of a CTA up to which a cluster takes a unit, over every page
+constexpr int kShort = 128;  // blocks x tiles of a unit up to which a cluster takes it
 constexpr int kMaxCluster = 16;
 
 // clusters of c CTAs of this kernel that the device holds at once
@@ -1047,13 +1047,13 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
     for (a.b0 = 0; a.b0 < p.B; a.b0 += cut.batches) {
         a.nb = p.B - a.b0 < cut.batches ? p.B - a.b0 : cut.batches;
         a.units = a.nb * p.Hkv * cut.groups;
-        // A cluster a unit, of the most CTAs whose clusters all run at once, where no CTA then takes many blocks: no second
-        // launch, and no CTA looks through all units for its own.  One sequence of 8 KV heads, 4 query heads each, trees of
-        // 8: 13.9 us against 19.1 for 4K tokens, 24.1 against 26.9 for 16K, 31.6 against 32.7 for 24K, 38.0 against 37.3
-        // for 32K (17 blocks a CTA), four sequences of 8K (17 blocks) 32.8 against 38.1; trees of 64 (two tiles, a block twice the work) 25.6 against 26.4 for 8K, 33.2 against
-        // 31.7 for 16K (8 blocks).  Selections are mostly as long as Kmax, so no cluster waits for a longer one: eight
-        // sequences, 300 pages a head (20 blocks a CTA) 38.7 against 44.2; ragged sequences of up to 16K (128 blocks)
-        // 154 against 133.
+        // A cluster a unit, of the most CTAs whose clusters all run at once, where units are short: no second launch, and
+        // no CTA looks through all units for its own.  Beyond that the SMs that whole clusters leave empty, and waiting for
+        // the longest of ragged sequences, cost more.  Clusters against dealing, 8 KV heads of 4 query heads, trees of 8
+        // (us): one sequence of 4K tokens 12.0, 14.6, of 12K 20.0, 20.5, of 24K (193 blocks) 30.0, 28.0; two of 8K 21.8,
+        // 24.1, of 16K 36.3, 33.3; four of 8K 31.2, 33.8; sixteen of 2K 30.2, 35.0; sixteen ragged ones of up to 16K, 13
+        // nodes x 5 heads 147, 128.  Two tiles, trees of 64: two of 4K 24.5, 27.3, four of 8K (65 blocks) 42.9, 47.2, but
+        // one of 1K, whose 16 CTAs have most to join, 16.4, 14.6.
         int c = 0;
         if (a.units <= known.sms) {
             for (c = 1; c < kMaxCluster && c < most && a.units * (c + 1) <= known.sms;) {
@@ -1063,7 +1063,7 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
                 ++c;
             }
         }
-        a.cluster = c > 0 && (most + c - 1) / c * cut.tiles <= (p.sel_idx != nullptr ? 2 * kShort : kShort) ? c : 0;
+        a.cluster = c > 0 && most * cut.tiles <= kShort && c * cut.tiles <= 24 ? c : 0;
         if (a.cluster > 0) {
             e = launch_pdl_cluster(tree_attn_kernel<D, T>, dim3(static_cast<unsigned>(a.units * c)), dim3(kThreads),
                                    Smem<D>::kBytes, stream, static_cast<unsigned>(c), a, kmap, vmap);
