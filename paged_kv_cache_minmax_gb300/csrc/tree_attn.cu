@@ -1047,23 +1047,23 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
     for (a.b0 = 0; a.b0 < p.B; a.b0 += cut.batches) {
         a.nb = p.B - a.b0 < cut.batches ? p.B - a.b0 : cut.batches;
         a.units = a.nb * p.Hkv * cut.groups;
-        // A cluster a unit, of the most CTAs whose clusters all run at once, where units are short: no second launch, and
+        // A cluster a unit, of the most CTAs whose clusters all run at once (7 of 16, 8 of 12, 15 of 9), where units are short: no second launch, and
         // no CTA looks through all units for its own.  Beyond that the SMs that whole clusters leave empty, and waiting for
         // the longest of ragged sequences, cost more.  Clusters against dealing, 8 KV heads of 4 query heads, trees of 8
         // (us): one sequence of 4K tokens 12.0, 14.6, of 12K 20.0, 20.5, of 24K (193 blocks) 30.0, 28.0; two of 8K 21.8,
         // 24.1, of 16K 36.3, 33.3; four of 8K 31.2, 33.8; sixteen of 2K 30.2, 35.0; sixteen ragged ones of up to 16K, 13
         // nodes x 5 heads 147, 128.  Two tiles, trees of 64: two of 4K 24.5, 27.3, four of 8K (65 blocks) 42.9, 47.2, but
-        // one of 1K, whose 16 CTAs have most to join, 16.4, 14.6.
+        // one of 1K, whose clusters of 12 CTAs have most to join, 16.4, 14.6.
         int c = 0;
         if (a.units <= known.sms) {
-            for (c = 1; c < kMaxCluster && c < most && a.units * (c + 1) <= known.sms;) {
-                int& held = known.held[c + 1];
-                if (held == 0) held = clusters_at_once(tree_attn_kernel<D, T>, Smem<D>::kBytes, c + 1);
-                if (held < a.units) break;
-                ++c;
+            c = 1;
+            for (int k = 2; k <= kMaxCluster && k <= most && a.units * k <= known.sms; ++k) {
+                int& held = known.held[k];
+                if (held == 0) held = clusters_at_once(tree_attn_kernel<D, T>, Smem<D>::kBytes, k);
+                if (held >= a.units) c = k;
             }
         }
-        a.cluster = c > 0 && most * cut.tiles <= kShort && c * cut.tiles <= 24 ? c : 0;
+        a.cluster = c > 0 && most * cut.tiles <= kShort && c * cut.tiles <= 20 ? c : 0;
         if (a.cluster > 0) {
             e = launch_pdl_cluster(tree_attn_kernel<D, T>, dim3(static_cast<unsigned>(a.units * c)), dim3(kThreads),
                                    Smem<D>::kBytes, stream, static_cast<unsigned>(c), a, kmap, vmap);
