@@ -31,7 +31,7 @@
 // Times (us in a row; the floor is the bytes at a copy's rate): one 128K sequence,
 // 8 KV heads, 64 nodes x 4 heads 108 (79; 137 GFLOP, 1,270 TFLOP/s); 16 ragged
 // sequences of up to 16K tokens, pages of 32, 13 nodes x 5 heads 130 (116); eight
-// sequences, 128 selected pages, 16 nodes 24.0 (10.3); one of 4K 12.5 (2.5), which is
+// sequences, 128 selected pages, 16 nodes 22.9 (10.3); one of 4K 12.5 (2.5), which is
 // latency: lengths, table entry, first block 3.7, products and softmax 4, join 3.
 #include <cstdint>
 
@@ -732,52 +732,80 @@ __device__ __forceinline__ float2 ld_cluster_v2(uint32_t local, uint32_t rank)
     return v;
 }
 
-template <int D>
-__device__ __forceinline__ void join_cluster(const Launch& a, const Unit& u, uint8_t* smem)
+// K CTAs' and I quads' loads in flight: a remote one takes some 700 cycles.  (Pairs of CTAs have several quads a thread: two at
+// once took eight sequences of 128 pages a head from 23.9 to 22.9 us, four spill.)
+template <int D, int K, int I>
+__device__ __forceinline__ void join_quads(const Launch& a, const Unit& u, uint8_t* smem)
 {
     const TreeAttnParams& p = a.p;
     const uint32_t sums = smem_addr(smem) + 2 * Smem<D>::kTile, ml = sums + a.tiles * 128 * D * 4;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int x = (warp * a.cluster + cluster_ctarank()) * 32 + lane; x < u.rows * (D / 4); x += a.cluster * 256) {
-        const int row = x / (D / 4), quad = x % (D / 4);
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int k0 = 0; k0 < a.cluster; k0 += 8) {  // eight CTAs' loads in flight
-            float2 ml_k[8];
-            float4 o_k[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, step = a.cluster * 256, all = u.rows * (D / 4);
+    for (int x0 = (warp * a.cluster + cluster_ctarank()) * 32 + lane; x0 < all; x0 += I * step) {
+        float m[I], l[I];
+        float4 o[I];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                ml_k[k] = make_float2(-INFINITY, 0.f);
-                if (k0 + k < a.cluster) {
-                    ml_k[k] = ld_cluster_v2(ml + row * 8, k0 + k);
-                    o_k[k] = ld_cluster_v4(sums + quad_at<D>(row, quad) * 16, k0 + k);
+        for (int i = 0; i < I; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int k0 = 0; k0 < a.cluster; k0 += K) {
+            float2 ml_k[I][K];
+            float4 o_k[I][K];
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                const int x = x0 + i * step, row = x / (D / 4), quad = x % (D / 4);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    ml_k[i][k] = make_float2(-INFINITY, 0.f);
+                    if (k0 + k < a.cluster && x < all) {
+                        ml_k[i][k] = ld_cluster_v2(ml + row * 8, k0 + k);
+                        o_k[i][k] = ld_cluster_v4(sums + quad_at<D>(row, quad) * 16, k0 + k);
+                    }
                 }
             }
-            float mn = m;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml_k[k].x);
-            const float f0 = l != 0.f ? exp2_fast((m - mn) * p.scale_log2) : 0.f;
-            m = mn;
-            l *= f0;
-            o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+            for (int i = 0; i < I; ++i) {
+                float mn = m[i];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (ml_k[k].y != 0.f) {  // (a CTA without a block has left no sums)
-                    const float f = exp2_fast((ml_k[k].x - m) * p.scale_log2);
-                    l = fmaf(ml_k[k].y, f, l);
-                    o.x = fmaf(o_k[k].x, f, o.x);
-                    o.y = fmaf(o_k[k].y, f, o.y);
-                    o.z = fmaf(o_k[k].z, f, o.z);
-                    o.w = fmaf(o_k[k].w, f, o.w);
-                }
+                for (int k = 0; k < K; ++k) mn = fmaxf(mn, ml_k[i][k].x);
+                const float f0 = l[i] != 0.f ? exp2_fast((m[i] - mn) * p.scale_log2) : 0.f;
+                m[i] = mn;
+                l[i] *= f0;
+                o[i] = make_float4(o[i].x * f0, o[i].y * f0, o[i].z * f0, o[i].w * f0);
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (ml_k[i][k].y != 0.f) {  // (a CTA without a block has left no sums)
+                        const float f = exp2_fast((ml_k[i][k].x - mn) * p.scale_log2);
+                        l[i] = fmaf(ml_k[i][k].y, f, l[i]);
+                        o[i].x = fmaf(o_k[i][k].x, f, o[i].x);
+                        o[i].y = fmaf(o_k[i][k].y, f, o[i].y);
+                        o[i].z = fmaf(o_k[i][k].z, f, o[i].z);
+                        o[i].w = fmaf(o_k[i][k].w, f, o[i].w);
+                    }
+            }
         }
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        const size_t at = row_of(p, u, u.row0 + row);
-        reinterpret_cast<uint2*>(p.out + at * D)[quad] =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (p.lse != nullptr && quad == 0) p.lse[at] = lse_of(m, l, p.scale_log2);
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int x = x0 + i * step, row = x / (D / 4), quad = x % (D / 4);
+            if (x >= all) continue;
+            const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
+            const size_t at = row_of(p, u, u.row0 + row);
+            reinterpret_cast<uint2*>(p.out + at * D)[quad] =
+                make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
+            if (p.lse != nullptr && quad == 0) p.lse[at] = lse_of(m[i], l[i], p.scale_log2);
+        }
     }
+}
+
+template <int D>
+__device__ __forceinline__ void join_cluster(const Launch& a, const Unit& u, uint8_t* smem)
+{
+    if (a.cluster <= 2)
+        join_quads<D, 2, 2>(a, u, smem);
+    else
+        join_quads<D, 8, 1>(a, u, smem);
 }
 
 // ---- the kernel ---------------------------------------------------------------------

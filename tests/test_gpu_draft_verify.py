@@ -195,6 +195,12 @@ def test_odd_probabilities_do_no_harm():
     assert (c.len >= 1).all() and (last >= 0).all() and (last < 1000).all()
 
 
+def test_more_sequences_than_run_at_once():
+    c = Case(700, 4, 300, "distinct", 2, seed=19)
+    c.call()
+    c.check()
+
+
 def test_stream_and_graph():
     c = Case(6, 8, 5000, "distinct", 3, seed=18)
     side = torch.cuda.Stream()
