@@ -158,10 +158,13 @@ class TreeDecode:
     which do not include node 0.  A step is ``begin``, ``layer_step`` for every layer, ``verify`` with the target's
     probabilities, ``keep``; ``out_tokens[:, path_len - 1]`` are the next roots.
 
-    ``parent`` [B, n_max] int32 gives the trees (see ``kvmm.draft_verify``); they may be replaced with ``set_trees``."""
+    ``parent`` [B, n_max] int32 gives the trees (see ``kvmm.draft_verify``); they may be replaced with ``set_trees``, which
+    steps that are captured in a graph follow."""
 
     def __init__(self, state: DecodeState, parent: torch.Tensor, rope: kvmm.Rope | None = None):
         s = state.shape
+        if parent.dim() != 2 or parent.shape[0] != s.B:
+            raise ValueError(f"parent must be [{s.B}, n], got {list(parent.shape)}")
         n = parent.shape[1]
         dev = state.seq_len.device
         i32 = dict(dtype=torch.int32, device=dev)
@@ -174,16 +177,21 @@ class TreeDecode:
         self.path_len = torch.zeros(s.B, **i32)
         self.n_nodes, self.tok_end = torch.full((s.B,), n, **i32), torch.zeros(s.B, **i32)
         self.positions = torch.zeros(s.B, n, **i32)
+        self.parent, self.depth = torch.zeros(s.B, n, **i32), torch.zeros(s.B, n, **i32)
+        self.mask = torch.zeros(s.B, n, dtype=torch.int64, device=dev)
         self.workspace = kvmm.alloc_tree_workspace(s, n, device=dev)
         self.rope = None if rope is None else kvmm.Rope(rope.table, rope.dim, bool(rope.c.interleaved), self.positions)
         self.set_trees(parent)
 
     def set_trees(self, parent: torch.Tensor) -> None:
-        """The trees of the following steps."""
-        self.parent = parent.to(torch.int32).contiguous()
-        self.mask = kvmm.tree_masks(self.parent)
-        j = torch.arange(self.n_max, device=parent.device)
-        self.depth = ((self.mask.unsqueeze(-1) >> j) & 1).sum(-1).sub_(1).to(torch.int32)
+        """The trees of the following steps, ``parent`` [B, n_max] copied.  What a captured step reads stays in its place:
+        its replays take the trees set last."""
+        if parent.shape != self.parent.shape:
+            raise ValueError(f"parent must be {list(self.parent.shape)}, got {list(parent.shape)}")
+        self.parent.copy_(parent)
+        self.mask.copy_(kvmm.tree_masks(self.parent))
+        j = torch.arange(self.n_max, device=self.mask.device)
+        self.depth.copy_(((self.mask.unsqueeze(-1) >> j) & 1).sum(-1).sub_(1))
 
     def begin(self, n_nodes: torch.Tensor | None = None) -> None:
         """Start a step; ``n_nodes`` [B] int32: the nodes of each tree that exist (default: all)."""
