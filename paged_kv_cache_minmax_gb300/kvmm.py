@@ -734,11 +734,12 @@ def alloc_tree_workspace(shape: Shape, n_max: int, device="cuda") -> torch.Tenso
 
 def tree_masks(parent: torch.Tensor) -> torch.Tensor:
     """The tree_mask [B, n] (int64, bit j of node i: i sees j) in which every node sees itself and its ancestors, from
-    parent [B, n] (node 0 is the root; parent[:, i] < i).  A launch for each node: for trees that are kept."""
+    parent [B, n] (node 0 is the root; parent[:, i] < i; a node with a parent that is no earlier one sees itself alone, or
+    with a parent below 0 the root too).  A few launches for each node: for trees that are kept."""
     if parent.dim() != 2 or not 1 <= parent.shape[1] <= 64:
         raise ValueError(f"parent must be [B, n] with 1 <= n <= 64, got {tuple(parent.shape)}")
     n = parent.shape[1]
-    up = parent.long().clamp(min=0)
+    up = parent.long().clamp(0, n - 1)  # (a node that is not reached yet has no bits)
     bits = torch.zeros(parent.shape, dtype=torch.int64, device=parent.device)
     for i in range(n):
         own = 1 << i if i < 63 else -(1 << 63)

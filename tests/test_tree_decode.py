@@ -65,3 +65,15 @@ def test_trees_of_another_shape_are_refused(shape):
 def test_a_state_of_another_batch_is_refused(parent):
     with pytest.raises(ValueError, match="parent"):
         trees(parent)
+
+
+@pytest.mark.parametrize("wrong", [N, N + 1, 99, (1 << 31) - 1, 3, 2, -7, -(1 << 31)])
+def test_impossible_parents_index_nothing(wrong):
+    """A parent that is no earlier node: the node sees itself alone (below 0: itself and the root); the others are as
+    they were.  (draft_verify reports it.)"""
+    parent = [[-1, 0, wrong, 1], [-1, 0, 1, 2]]
+    t = trees(parent)
+    alone = 0b100 if wrong > 0 else 0b101
+    assert t.mask.tolist() == [[0b1, 0b11, alone, 0b1011], [0b1, 0b11, 0b111, 0b1111]]
+    assert t.depth.tolist() == [[0, 1, 0 if wrong > 0 else 1, 2], [0, 1, 2, 3]]
+    assert torch.equal(kvmm.tree_masks(torch.tensor(parent)), t.mask)
