@@ -398,12 +398,15 @@ __device__ void issue_products(const Launch& a, uint8_t* smem, Control& c, Walk 
 }
 
 // ---- a softmax group: the 128 threads of a stream, a row each ------------------------
-// both groups arrive and wait; false once any warp of the CTA has given up
+// Both groups arrive and wait; false once any warp of the CTA has given up.  What either has seen done in tensor memory
+// (its stream's products, its own loads and stores) is done for both behind it.
 __device__ __forceinline__ bool groups_meet(Control& c, uint32_t& phase)
 {
+    tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&c.meet);
     const bool fine = wait_for(&c.meet, phase & 1, &c.gave_up);
+    tc_fence_after();
     ++phase;
     return __all_sync(kFullMask, fine);
 }
@@ -635,9 +638,8 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
                     p.lse[at] = lse_of(ref, l, scale);
             }
         }
-        tc_fence_before();
-        if (!two && !groups_meet(c, met)) return;  // the other stream's sums have been read, and its O
-        tc_fence_after();
+        // (behind it the other stream's sums have been read, and its O)
+        if (!two && !groups_meet(c, met)) return;
     }
 }
 
