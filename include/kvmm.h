@@ -733,8 +733,8 @@ kvmm_status sparse_paged_decode_attn_kv4(const kvmm_shape* shape, int32_t layer,
  *              shows it node j (its own bit counts like any other).  NULL: a
  *              chain, node i sees the nodes 0 .. i.  Bits from n_nodes[b] on
  *              do not matter.
- * Scores, softmax and sums are fp32; a weight is rounded to bf16 where it
- * meets the bf16 values.  sm_scale <= 0 means 1/sqrt(D).  A row to which
+ * Scores, softmax and sums are fp32; a weight meets the bf16 values as two
+ * bf16 halves, 2^-16 of it left out.  sm_scale <= 0 means 1/sqrt(D).  A row to which
  * nothing is shown yields out = 0 and lse = -inf.  Rows of nodes that do not
  * exist are neither read nor written.  A page that has to be read and whose
  * table entry is null or out of range sets its error bit and contributes
