@@ -53,6 +53,12 @@ constexpr int kTokens = 128;     // tokens of a block
 constexpr int kRing = 8;         // blocks whose masks are held (see copy_pages)
 constexpr int kNoNode = 1 << 20; // an entry that holds no node
 constexpr int kUnitsAtOnce = 2048;
+constexpr int kShort = 128;      // blocks x tiles of a unit up to which a cluster takes it
+// Steps of a stream whose products tensor memory sums.  Its additions round toward zero, 16 a step: over 64 steps of sums that
+// grow steadily the result is low by up to 2^-14 (half of 1,024 x 2^-23).  Then the sums go to the workspace, where they are
+// added to the nearest.  (Without: 2^20 tokens of positive values in one CTA 2.3e-3 low, more than half of what rounding to
+// bf16 may do.)
+constexpr int kRun = kShort / 2;
 
 struct Launch {
     TreeAttnParams p;
@@ -66,6 +72,7 @@ struct Launch {
     int4* cut;       // a unit whose blocks fall on several CTAs (x -1: none): unit, first CTA, last CTA, rows
     float2* ml;      // [2 * CTAs][tiles][tile_rows] reference and sum
     float4* o;       // [2 * CTAs][tiles][D / 4][tile_rows]
+    float4* run;     // [CTAs][2 streams][D / 4][tile_rows] sums of a stream's steps before the last kRun
 };
 
 struct Unit {
@@ -386,7 +393,7 @@ __device__ void issue_products(const Launch& a, uint8_t* smem, Control& c, Walk 
             for (int i = 0; i < kTokens / 16; ++i) {
                 const uint32_t off = ((i * 16 / T) * (T * D * 2) + (i * 16 % T) * 2) >> 4;
                 if (i < sixteens) {
-                    mma_ts(o, w + i * 8, vv + off, pv, i > 0 || v > 1);  // (the first of the stream's in this piece: not added)
+                    mma_ts(o, w + i * 8, vv + off, pv, i > 0 || (v >> 1) % kRun != 0);  // (the first of a run: not added)
                     mma_ts(o, w + 64 + i * 8, vv + off, pv, true);
                 }
             }
@@ -473,6 +480,38 @@ __device__ __forceinline__ float lse_of(float m, float l, float scale_log2)
     return l != 0.f ? (m * scale_log2 + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// A row's sums of a run, kRun steps: added to those of the runs before it, which are in units of 2^(before - ref) (the first
+// run's are put down), or, at the end of a piece (LAST), those added to the last run's in tensor memory.
+template <int D, bool LAST>
+__device__ __noinline__ void carry_run(const Launch& a, uint32_t tO, float4* run, float2* kept, float ref, bool first, bool row)
+{
+    const float before = first || !row ? -INFINITY : kept->x;
+    const float f = before == -INFINITY ? 0.f : exp2_fast((before - ref) * a.p.scale_log2);
+#pragma unroll 1
+    for (int i = 0; i < D / 4; i += 4) {
+        uint32_t o[16];
+        tmem_ld16(tO + 4 * i, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!row) continue;
+            float4 x = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                   __uint_as_float(o[4 * e + 3]));
+            float4* y = run + (i + e) * a.tile_rows;
+            if (!first) x = make_float4(fmaf(y->x, f, x.x), fmaf(y->y, f, x.y), fmaf(y->z, f, x.z), fmaf(y->w, f, x.w));
+            if (!LAST) *y = x;
+            o[4 * e] = __float_as_uint(x.x);
+            o[4 * e + 1] = __float_as_uint(x.y);
+            o[4 * e + 2] = __float_as_uint(x.z);
+            o[4 * e + 3] = __float_as_uint(x.w);
+        }
+        __syncwarp();
+        if (LAST) tmem_st16(tO + 4 * i, o);
+    }
+    if (LAST) tmem_wait_st();
+    if (!LAST && row) kept->x = ref;
+}
+
 template <int D, int T>
 __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
 {
@@ -483,6 +522,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
     const uint32_t mine = c.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const uint32_t tS = mine + s * 128, tO = mine + 256 + s * 128;
     const float scale = p.scale_log2, slack = 8.f / scale;
+    float4* const run = a.run + static_cast<size_t>(2 * blockIdx.x + s) * (D / 4) * a.tile_rows + r;  // (not used in short units)
     uint32_t s_phase = 0, o_phase = 0, met = 0, nth = 0;
     Unit u;
     int begin, count;
@@ -507,6 +547,8 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
             if (!__all_sync(kFullMask, wait_for(&c.s_full[s], s_phase & 1, &c.gave_up))) return;
             ++s_phase;
             tc_fence_after();
+            // (the products before this block's scores are done; the meeting's place in shared memory is free until then)
+            if (busy && v != 0 && v % kRun == 0) carry_run<D, false>(a, tO, run, &c.ml[s][r], ref, v == kRun, r < rows);
             if (busy) {
                 uint32_t z[kTokens];
 #pragma unroll
@@ -584,6 +626,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
             if (!__all_sync(kFullMask, wait_for(&c.o_done[s], o_phase & 1, &c.gave_up))) return;
             ++o_phase;
             tc_fence_after();
+            if (busy && steps > kRun) carry_run<D, true>(a, tO, run, &c.ml[s][r], ref, false, r < rows);
         }
         // the row's result: written whole, or left as a part
         const bool whole = count == u.blocks && a.cluster <= 1;
@@ -1002,10 +1045,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Launch
     if (p.lse != nullptr && quad0 == 0) p.lse[at] = lse_of(m, l, p.scale_log2);
 }
 
+// most pages of a unit: all, or the selected ones and those that nodes reach
+long long pages_of(int Pmax, int Kmax, int n_max, int T, bool selected)
+{
+    return selected ? static_cast<long long>(Kmax) + (n_max + T - 2) / T + 1 : Pmax;
+}
+
+long long blocks_of(long long pages, int T) { return (pages * T + kTokens - 1) / kTokens; }
+
 // rows of the nodes' tiles, and how the units are cut
 struct Cut {
     int tiles, groups, tile_rows, batches;  // batches: of one launch
-    Cut(int n_max, int G, int Hkv, int B)
+    bool runs;  // a stream may have more than kRun steps
+    Cut(int n_max, int G, int Hkv, int B, int T, int Pmax, int Kmax)
     {
         const int rows = n_max * G;
         tiles = rows > 128 ? 2 : 1;
@@ -1013,13 +1065,16 @@ struct Cut {
         tile_rows = rows < 128 ? rows : 128;
         batches = kUnitsAtOnce / (Hkv * groups);
         batches = batches < 1 ? 1 : batches > B ? B : batches;
+        const long long all = pages_of(Pmax, Kmax, n_max, T, false), some = pages_of(Pmax, Kmax, n_max, T, true);
+        runs = blocks_of(all > some ? all : some, T) * tiles > 2 * kRun;
     }
     static constexpr size_t kCutBytes = (sizeof(int4) * kTreeMaxCtas + 255) / 256 * 256;
     size_t rows() const { return static_cast<size_t>(2 * kTreeMaxCtas) * tiles * tile_rows; }
     size_t ml_bytes() const { return round256(sizeof(float2) * rows()); }
+    size_t o_bytes(int D) const { return sizeof(float) * rows() * D; }
+    size_t run_bytes(int D) const { return runs ? sizeof(float) * 2 * kTreeMaxCtas * tile_rows * D : 0; }
 };
 
-constexpr int kShort = 128;  // blocks x tiles of a unit up to which a cluster takes it
 constexpr int kMaxCluster = 16;
 
 // clusters of c CTAs of this kernel that the device holds at once
@@ -1073,7 +1128,7 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
     e = tensor_map_3d(&vmap, p.v_pool, T, D, n, T, D, T == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
 
-    const Cut cut(p.n_max, p.G, p.Hkv, p.B);
+    const Cut cut(p.n_max, p.G, p.Hkv, p.B, T, p.Pmax, p.Kmax);
     Launch a{};
     a.p = p;
     a.tiles = cut.tiles;
@@ -1083,8 +1138,8 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
     a.cut = reinterpret_cast<int4*>(ws);
     a.ml = reinterpret_cast<float2*>(ws + Cut::kCutBytes);
     a.o = reinterpret_cast<float4*>(ws + Cut::kCutBytes + cut.ml_bytes());
-    const int pages = p.sel_idx != nullptr ? p.Kmax + (p.n_max + T - 2) / T + 1 : p.Pmax;
-    const long long most = (static_cast<long long>(pages) * T + kTokens - 1) / kTokens;  // blocks of a unit
+    a.run = cut.runs ? a.o + cut.o_bytes(D) / sizeof(float4) : nullptr;
+    const long long most = blocks_of(pages_of(p.Pmax, p.Kmax, p.n_max, T, p.sel_idx != nullptr), T);  // blocks of a unit
     const int rows = p.n_max * p.G < 128 * cut.tiles ? p.n_max * p.G : 128 * cut.tiles;
     for (a.b0 = 0; a.b0 < p.B; a.b0 += cut.batches) {
         a.nb = p.B - a.b0 < cut.batches ? p.B - a.b0 : cut.batches;
@@ -1134,8 +1189,8 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
 
 size_t tree_ws_bytes(const kvmm_shape& s, int n_max)
 {
-    const Cut cut(n_max, s.Hq / s.Hkv, s.Hkv, s.B);
-    return Cut::kCutBytes + cut.ml_bytes() + sizeof(float) * cut.rows() * s.D;
+    const Cut cut(n_max, s.Hq / s.Hkv, s.Hkv, s.B, s.T, s.Pmax, s.Kmax);
+    return Cut::kCutBytes + cut.ml_bytes() + cut.o_bytes(s.D) + cut.run_bytes(s.D);
 }
 
 cudaError_t launch_tree_attention(const TreeAttnParams& p, cudaStream_t stream)
