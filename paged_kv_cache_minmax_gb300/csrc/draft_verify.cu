@@ -160,7 +160,7 @@ __device__ __forceinline__ long long row_sum(const Row& r, int V, int run, int c
     // not, which is P less the weight of min(p, q), as floor() ascends.  19 instructions an entry, most of them fp32,
     // against 46 with every residual in 64 bits: the pass was bound by the integer pipe.
     const bool plain = r.rejected == 0 || r.q == nullptr || r.rejected == 1;
-    uint32_t odd = 0;  // an exponent of 2 or more, or a sign: no probability, the general pass is right for it
+    uint32_t odd = 0;  // of any p or q f an exponent of 2 or more, or a sign: no probability, the general pass is right for it
     if (plain) {
         const float f = r.q != nullptr ? r.f[0] : 0.f;
         // steps of both rows, or twice as many of one, in flight
@@ -185,12 +185,13 @@ __device__ __forceinline__ long long row_sum(const Row& r, int V, int run, int c
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
                     const float pp[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
-                    const float4 c = kBoth ? q[kBoth ? i : 0] : p[i];
-                    const float qq[4] = {c.x, c.y, c.z, c.w};
+                    const float4 y = kBoth ? q[kBoth ? i : 0] : p[i];
+                    const float qq[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        odd |= __float_as_uint(pp[k]);
-                        const Digits a = digits_of(pp[k]), b = kBoth ? digits_of(fminf(__fmul_rn(qq[k], f), pp[k])) : zero;
+                        const float c = kBoth ? __fmul_rn(qq[k], f) : 0.f;
+                        odd |= __float_as_uint(pp[k]) | __float_as_uint(c);
+                        const Digits a = digits_of(pp[k]), b = kBoth ? digits_of(fminf(c, pp[k])) : zero;
                         d1 += a.d1 - b.d1;
                         d2 += a.d2 - b.d2;
                         d3 += a.d3 - b.d3;
