@@ -88,14 +88,14 @@ __device__ __forceinline__ bool make_plan(const KeepParams& p, int window, int b
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int j = lane + 32 * k, node = k ? a1 : a0, come = s0 + node, go = s0 + j;
-        bool move = j < m && node != j;
-        if (move && first * T + come >= cap) {
+        bool kept = j < m;  // (a row that stays needs its place too)
+        if (kept && first * T + come >= cap) {
             beyond = true;
-            move = false;
+            kept = false;
         }
-        const uint32_t pages = move ? 1u << (come / T) | 1u << (go / T) : 0;
+        const uint32_t pages = kept ? 1u << (come / T) | 1u << (go / T) : 0;
         need |= __reduce_or_sync(kFullMask, pages);
-        move &= (there & pages) == pages;
+        const bool move = kept && node != j && (there & pages) == pages;
         values |= __reduce_or_sync(kFullMask, move ? pages : 0);
         dest |= __reduce_or_sync(kFullMask, move ? 1u << (go / T) : 0);
         from |= __reduce_or_sync(kFullMask, move && node < 32 ? 1u << node : 0);
