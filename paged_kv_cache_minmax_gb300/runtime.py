@@ -225,11 +225,11 @@ class TreeDecode:
                           err=self.state.err)
 
     def keep(self) -> None:
-        """Settle the accepted nodes in every layer."""
+        """Settle the accepted nodes in every layer (those with a place in the table: the others are told)."""
         st = self.state
         kvmm.kv_keep_path(st.shape, -1, self.path, self.path_len, st.seq_len, st.k_pool, st.v_pool, st.block_table,
                           st.meta, err=st.err)
-        st.seq_len.add_(self.path_len)
+        st.seq_len.add_(self.path_len).clamp_(max=st.shape.Pmax * st.shape.T)
 
 
 class Kv4DecodeState(_StepState):

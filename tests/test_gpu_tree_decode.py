@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from paged_kv_cache_minmax_gb300 import kvmm
 from paged_kv_cache_minmax_gb300.runtime import TreeDecode
 from tests.test_gpu_tree_step import build, rows
 
@@ -43,3 +44,22 @@ def test_replaced_trees_reach_a_captured_step():
             assert torch.equal(getattr(trees[0], a), getattr(trees[1], a)), a
         assert torch.equal(st.seq_len, ref.seq_len) and torch.equal(st.meta, ref.meta)
     assert st.read_err() == 0 and ref.read_err() == 0
+
+
+def test_a_table_that_is_full():
+    """Accepted nodes beyond the table's end are told, and the settled tokens stop at its end."""
+    st, rope, g = build(B=B)
+    cap = 24 * 16
+    tree = TreeDecode(st, torch.tensor([[-1, 0, 1, 2, 3]] * B, dtype=torch.int32, device="cuda"))
+    st.seq_len.copy_(torch.tensor([cap - 2, 100], dtype=torch.int32))
+    target = torch.zeros(B, N, V, device="cuda")
+    target[:, :, 3] = 1  # every node's token is the target's
+    one = torch.full((B, N), 3, dtype=torch.int32, device="cuda")
+    for want in ([cap, 105], [cap, 110]):
+        tree.begin()
+        for l in range(L):
+            tree.layer_step(l, rows(g, B, N, HQ, D), rows(g, B, N, HKV, D), rows(g, B, N, HKV, D), every_page=True)
+        tree.verify(target, one, torch.zeros(B, N, device="cuda"), torch.zeros(B, device="cuda"))
+        tree.keep()
+        assert tree.path_len.tolist() == [N, N] and st.seq_len.tolist() == want
+    assert st.read_err() == kvmm.ERR_OUT_OF_RANGE
