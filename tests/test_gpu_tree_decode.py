@@ -1,9 +1,11 @@
 """TreeDecode on the GPU: what its steps do beyond the calls they are made of."""
+import numpy as np
 import pytest
 import torch
 
 from paged_kv_cache_minmax_gb300 import kvmm
 from paged_kv_cache_minmax_gb300.runtime import TreeDecode
+from tests import tree_plain
 from tests.test_gpu_tree_step import build, rows
 
 pytestmark = pytest.mark.gpu
@@ -44,6 +46,62 @@ def test_replaced_trees_reach_a_captured_step():
             assert torch.equal(getattr(trees[0], a), getattr(trees[1], a)), a
         assert torch.equal(st.seq_len, ref.seq_len) and torch.equal(st.meta, ref.meta)
     assert st.read_err() == 0 and ref.read_err() == 0
+
+
+@pytest.mark.parametrize("mask", [None, [[1, 0], [0, 1]], [[0, 0], [0, 0]]])
+def test_pages_are_selected_by_the_roots_queries(mask):
+    """A step over selected pages: rescored units hold the root's own best pages, the others those of the step before; every
+    node attends over exactly these and over its ancestors."""
+    K, T, n = 6, 16, N
+    st, rope, g = build(B=B, K=K)
+    parent = [[-1, 0, 0, 1, 2], [-1, 0, 1, 1, 0]]
+    tree = TreeDecode(st, torch.tensor(parent, dtype=torch.int32, device="cuda"), rope)
+    end = torch.tensor([250, 170], dtype=torch.int32, device="cuda")
+    for l in range(L):
+        k, v = rows(g, B, 250, HKV, D), rows(g, B, 250, HKV, D)
+        kvmm.kv_append_rope(st.shape, l, None, k, v, torch.zeros_like(end), end, st.k_pool, st.v_pool, st.block_table, st.meta,
+                            rope=rope, err=st.err)
+    st.seq_len.copy_(end)
+    rescore = None if mask is None else torch.tensor(mask, dtype=torch.uint8, device="cuda")
+    for step in range(2):
+        tree.begin()
+        was = st.sel_idx.clone()
+        for l in range(L):
+            tree.layer_step(l, rows(g, B, n, HQ, D), rows(g, B, n, HKV, D), rows(g, B, n, HKV, D),
+                            rescore_mask=rescore if step else None)
+        torch.cuda.synchronize()
+        meta, sel, cnt = st.meta.double().cpu().numpy(), st.sel_idx.cpu().numpy(), st.sel_cnt.cpu().numpy()
+        k_pool, v_pool = st.k_pool.double().cpu().numpy(), st.v_pool.double().cpu().numpy()
+        table, bits, G = st.block_table.cpu().numpy(), tree_plain.masks(parent), HQ // HKV
+        for b in range(B):
+            seq = int(end[b])
+            pages = -(-seq // T)
+            for l in range(L):
+                q = tree.q_turned[l, b].double().cpu().numpy()
+                for h in range(HKV):
+                    got = sel[b, l, h, :cnt[b, l, h]]
+                    assert cnt[b, l, h] == K and len(set(got)) == K and got.max() < pages
+                    if step and mask is not None and not mask[l][h]:
+                        assert (got == was[b, l, h].cpu().numpy()).all()
+                    else:
+                        lo, hi = meta[b, l, h, :pages, 0], meta[b, l, h, :pages, 1]
+                        score = sum(np.maximum(q[0, h * G + i] * lo, q[0, h * G + i] * hi).sum(-1) for i in range(G))
+                        rest = np.setdiff1d(np.arange(pages), got)
+                        # scores of G * D products in fp32
+                        slack = G * D * 2.0 ** -23 * np.abs(score).max()
+                        assert score[got].min() >= score[rest].max() - slack
+                    tok = np.arange(seq + n)
+                    old = (tok < seq) & np.isin(tok // T, got)
+                    shown = np.stack([old | ((tok >= seq) & ((int(bits[b, i]) >> np.maximum(tok - seq, 0)) & 1 == 1)) for i in range(n)])
+                    at = table[b, l, h, tok // T]
+                    rows_q = q[:, h * G:(h + 1) * G].reshape(n * G, D)
+                    o, lse, weighted, size = tree_plain.attend(rows_q, k_pool[at, tok % T], v_pool[at, :, tok % T],
+                                                               shown.repeat(G, 0), D ** -0.5)
+                    out = tree.out[l, b, :, h * G:(h + 1) * G].double().cpu().numpy().reshape(n * G, D)
+                    assert (np.abs(out - o) <= tree_plain.out_bound(o, weighted, size, D, seq + n)).all()
+                    off = np.abs(tree.lse[l, b, :, h * G:(h + 1) * G].double().cpu().numpy().reshape(-1) - lse)
+                    assert (off <= tree_plain.lse_bound(lse, size, D, seq + n)).all()
+    assert st.read_err() == 0
 
 
 def test_a_table_that_is_full():
