@@ -743,9 +743,10 @@ kvmm_status sparse_paged_decode_attn_kv4(const kvmm_shape* shape, int32_t layer,
  * KVMM_ERR_OUT_OF_RANGE and are clamped, and nodes whose token would lie
  * beyond Pmax*T set it and are not attended.  What a page holds in slots that
  * no settled token and no node has is not looked at.  Selections list each
- * page once.  A node's value row has to be finite even where only some rows
- * see it: it meets a weight of 0 in the others.  A NaN in a query makes its
- * row's results NaN.
+ * page once.  A key or value of a node that is NaN or infinite leaves the
+ * rows that do not see the node alone; those that do hold NaN in that value's
+ * channel (for a key, as its scores give).  A NaN in a query makes its row's
+ * results NaN.
  * workspace: kvmm_tree_workspace_size(shape, n_max) bytes, 16-byte aligned;
  * nothing in it matters between calls.  The workspace size is 0 for an
  * unsupported shape or n_max.

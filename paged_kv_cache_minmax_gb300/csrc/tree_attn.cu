@@ -128,6 +128,7 @@ struct BlockMask {
 
 struct Control {
     uint64_t full[10], empty[10], s_full[2], p_ready[2], q_ready[2], o_done[2], meet, drain;
+    unsigned long long spoilt[2];  // nodes that have a value that is not finite, by the piece's parity
     uint32_t tmem;
     int32_t gave_up;
     int32_t w0, off0, left;
@@ -298,20 +299,23 @@ __device__ void copy_pages(const Launch& a, const CUtensorMap* kmap, const CUten
 
 // ---- values that nothing may see -------------------------------------------------------
 // Slots of a block's values that nothing shows are set to zero: whatever they hold, NaN included, would meet a weight of
-// 0.  By the 128 threads of a softmax group, before they hand over the weights.
+// 0.  So are nodes' values that are not finite, for the rows that do not see the node; those that do are told by `spoilt`.
+// By the 128 threads of a softmax group, before they hand over the weights.
 template <int D, int T>
-__device__ __noinline__ void clear_unseen(uint8_t* values, const BlockMask& m)
+__device__ __noinline__ void clear_unseen(uint8_t* values, const BlockMask& m, unsigned long long* spoilt)
 {
     constexpr int kChunks = T / 8;
     for (int i = 0; i < m.pages; ++i) {
-        uint32_t seen = m.settled[i];
+        uint32_t seen = m.settled[i], nodes = 0;
         const int from = max(m.node0[i], 0), to = min(m.node0[i] + T, m.held);  // its nodes (none: from >= to)
-        if (from < to) seen |= ((to - from >= 32 ? 0u : 1u << (to - from)) - 1u) << (from - m.node0[i]);
-        if (seen == 0xffffffffu >> (32 - T)) continue;
+        if (from < to) nodes = ((to - from >= 32 ? 0u : 1u << (to - from)) - 1u) << (from - m.node0[i]);
+        seen |= nodes;
+        if (seen == 0xffffffffu >> (32 - T) && nodes == 0) continue;
         for (int x = threadIdx.x & 127; x < D * kChunks; x += 128) {
             const int d = x / kChunks, ch = x % kChunks;
             const uint32_t bits = seen >> (8 * ch) & 255u;
-            if (bits == 255u) continue;
+            const uint32_t young = nodes >> (8 * ch) & 255u;
+            if (bits == 255u && young == 0) continue;
             const int at = T == 16 ? ch ^ (d >> 2 & 1) : ch ^ (d >> 1 & 3);
             uint4* q = reinterpret_cast<uint4*>(values + i * (T * D * 2) + d * (T * 2) + at * 16);
             uint4 v = *q;
@@ -319,10 +323,38 @@ __device__ __noinline__ void clear_unseen(uint8_t* values, const BlockMask& m)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
                 w[s] &= (bits >> (2 * s) & 1 ? 0xffffu : 0u) | (bits >> (2 * s + 1) & 1 ? 0xffff0000u : 0u);
+            // (an exponent of ones carries into the sign's place)
+            uint32_t wild = 0;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) wild |= ((w[s] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+            if (wild != 0) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t half = s & 1 ? 0x7f800000u : 0x7f80u;
+                    if ((young >> s & 1) && (w[s / 2] & half) == half) {
+                        w[s / 2] &= s & 1 ? 0xffffu : 0xffff0000u;
+                        atomicOr(spoilt, 1ull << (m.node0[i] + 8 * ch + s));
+                    }
+                }
+            }
             *q = v;
         }
     }
     fence_proxy_async_shared();
+}
+
+// which of 32 channels hold a value that is not finite in any of these nodes (looked up again: hardly ever met)
+template <int D, int T>
+__device__ __noinline__ uint32_t spoilt_channels(const TreeAttnParams& p, const Unit& u, uint64_t nodes, int channel)
+{
+    uint32_t found = 0;
+    for (; nodes != 0; nodes &= nodes - 1) {
+        const int t = u.seq + __ffsll(static_cast<long long>(nodes)) - 1, phys = p.block_table[u.index * p.Pmax + t / T];
+        const kvmm_bf16* v = p.v_pool + (static_cast<size_t>(phys) * D + channel) * T + t % T;  // (the page was copied)
+        for (int e = 0; e < 32; ++e)
+            if ((v[e * T] & 0x7f80u) == 0x7f80u) found |= 1u << e;
+    }
+    return found;
 }
 
 // ---- the issuing thread -------------------------------------------------------------
@@ -523,10 +555,14 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
     const uint32_t tS = mine + s * 128, tO = mine + 256 + s * 128;
     const float scale = p.scale_log2, slack = 8.f / scale;
     float4* const run = a.run + static_cast<size_t>(2 * blockIdx.x + s) * (D / 4) * a.tile_rows + r;  // (not used in short units)
-    uint32_t s_phase = 0, o_phase = 0, met = 0, nth = 0;
+    uint32_t s_phase = 0, o_phase = 0, met = 0, nth = 0, piece = 0;
     Unit u;
     int begin, count;
     while (next_piece<T>(a, k, u, begin, count)) {
+        // (Set before the other group's scores, which wait for both groups' queries; read last in the piece before the last one,
+        // which both groups have left.)
+        unsigned long long& spoilt = c.spoilt[piece++ & 1];
+        if (threadIdx.x == 0) spoilt = 0;
         const int row0 = u.row0 + (two ? s * 128 : 0), row = row0 + r;
         const int rows = min(max(u.row0 + u.rows - row0, 0), 128);  // of the tile
         const bool busy = warp * 32 < rows;                          // the warp has rows
@@ -615,7 +651,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
             if ((!two || s == 0) && !c.mask[(nth + blk) % kRing].whole) {
                 const uint32_t item = 2 * (nth + blk) + 1, slot = item % Smem<D>::kStages;
                 if (!__all_sync(kFullMask, wait_for(&c.full[slot], item / Smem<D>::kStages & 1, &c.gave_up))) return;
-                clear_unseen<D, T>(smem + (2 + slot) * Smem<D>::kTile, c.mask[(nth + blk) % kRing]);
+                clear_unseen<D, T>(smem + (2 + slot) * Smem<D>::kTile, c.mask[(nth + blk) % kRing], &spoilt);
             }
             tc_fence_before();
             __syncwarp();
@@ -653,6 +689,7 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
         if (busy) {
             const float inv = l != 0.f ? 1.f / l : 0.f;
             const size_t at = r < rows ? row_of(p, u, row) : 0;
+            const uint64_t wild = spoilt & bits;  // (bits of rows that do not exist are 0)
             for (int i = c0; i < c1; ++i) {
                 uint32_t x[32], y[32];
                 tmem_ld32(mine + 256 + (two ? s * 128 : 0) + 32 * i, x);
@@ -665,6 +702,13 @@ __device__ void softmax_rows(const Launch& a, uint8_t* smem, Control& c, Walk k)
                     o[e] = __uint_as_float(x[e]) * f0;
                     if (join) o[e] = fmaf(__uint_as_float(y[e]), f1, o[e]);
                 }
+                if (wild != 0) {
+                    const uint32_t channels = spoilt_channels<D, T>(p, u, wild, 32 * i);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (channels >> e & 1) o[e] = __uint_as_float(0x7fc00000u);
+                }
+                __syncwarp();
                 if (r < rows) {
                     if (whole) {
 #pragma unroll
