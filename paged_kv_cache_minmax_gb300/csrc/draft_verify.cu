@@ -14,13 +14,16 @@
 // through distributed shared memory.  The sums of the last pass lead to the drawn
 // token: the CTA, the warp, then one look at that warp's run again.
 //
-// Times (us in a row; the floor is the rows drawn from at a copy's rate): chains of
-// seven for 64 sequences, 131,072 tokens 23.5 (9.9); trees of 24 certain candidates
-// for 16 10.8 (1.2); trees of 16 drawn without replacement for 8, 100,003 tokens
-// 14.4 (0.9): a pass over the row for every rejected child that has a sibling left,
-// about 3 each; one chain of four, 32,000 tokens 7.1 (0.04).  The large case is
-// bound by the instructions of its pass, the small ones by the chain of loads (the
-// nodes, their probabilities, the row) and the cluster's barriers.
+// Times (us of a launch in a graph; the floor is the rows drawn from at a copy's rate):
+// chains of seven for 64 sequences, 131,072 tokens 23.1 (9.9); trees of 24 certain
+// candidates for 16 10.5 (1.2); trees of 16 drawn without replacement for 8, 100,003
+// tokens 11 to 27 (0.9) as their random numbers reject: a pass over the row, about 3,
+// for every rejected child that has a sibling left; one chain of four, 32,000 tokens
+// 6.7 (0.04).  The large case waits for the loads of its pass (a warp's run is four
+// rounds of load, wait and sum, at 29% of the memory's rate) and for the one warp
+// that looks again; the pass's instructions, 19 an entry, are some 4 of its time.  The
+// small ones wait for the chain of loads (the nodes, their probabilities, the row) and
+// the cluster's barriers.
 #include <type_traits>
 
 #include "common.cuh"

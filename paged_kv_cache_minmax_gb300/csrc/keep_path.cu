@@ -9,9 +9,10 @@
 // channels, by way of registers); rows move there, in order: a row's new place is
 // never behind its old one, so every row that is still to move is as it was.
 //
-// 32 sequences, 32 layers, 8 heads, trees of 16: 31.5 us against 13.9 for the bytes
-// at a copy's rate; bound by instructions (22 M; 64% of the issue slots) and the
-// shared-memory pipe.  One CTA that gathered values two bytes at a time took 67, a
+// 32 sequences, 32 layers, 8 heads, trees of 16: 31 us against 13.9 for the rows' bytes
+// at a copy's rate, 17.6 for the sectors they lie in (a value row's are all of its
+// page's); bound by waiting for the first warp's plan, by instructions (22 M; 64% of
+// the issue slots) and the shared-memory pipe.  One CTA that gathered values two bytes at a time took 67, a
 // warp that made its own plan of the moves 33, one that took all channels of a unit
 // in turn 38 to 40.  One sequence: 3.8 us, three dependent loads and the launch.
 #include "common.cuh"

@@ -27,19 +27,20 @@
 // tensor memory.  128 rows are the tensor cores' own tile; fewer rows leave part
 // of it unused, which costs nothing as long as the memory is the bound: a block
 // (64 KB with 128 channels) takes 2,800 cycles at a copy's rate, its products
-// about 1,500 a tile, its softmax 1,450 (128 exponentials a row at 16 a clock and
-// SM).  Two tiles take 3,000 of products, so the largest trees are bound by them.
+// about 2,300 a tile (Q K^T 650, each half's P V 850), its softmax some 2,000 (128
+// exponentials a row at 16 a clock and SM).  Two tiles take 4,500 of products, so the
+// largest trees are bound by them.
 //
 // Short units take a cluster of CTAs each, joined through distributed shared
 // memory.  Otherwise the blocks of all units are dealt evenly to one CTA an SM,
 // whatever the sequences' lengths; a unit that falls on several CTAs leaves parts
 // in the workspace, which a second launch joins.
 //
-// Times (us in a row; the floor is the bytes at a copy's rate): one 128K sequence,
-// 8 KV heads, 64 nodes x 4 heads 108 (79; 137 GFLOP, 1,270 TFLOP/s); 16 ragged
-// sequences of up to 16K tokens, pages of 32, 13 nodes x 5 heads 130 (116); eight
-// sequences, 128 selected pages, 16 nodes 22.9 (10.3); one of 4K 12.5 (2.5), which is
-// latency: lengths, table entry, first block 3.7, products and softmax 4, join 3.
+// Times (us of a launch in a graph; the floor is the bytes at a copy's rate): one 128K
+// sequence, 8 KV heads, 64 nodes x 4 heads 137 (79; 137 GFLOP, 1,000 TFLOP/s); 16
+// ragged sequences of up to 16K tokens, pages of 32, 13 nodes x 5 heads 135 (116);
+// eight sequences, 128 selected pages, 16 nodes 24.6 (10.3); one of 4K 13.3 (2.5), which
+// is latency: lengths, table entry, first block 3.7, products and softmax 5, join 3.
 #include <cstdint>
 
 #include "kernels.h"
@@ -56,7 +57,7 @@ constexpr int kUnitsAtOnce = 2048;
 constexpr int kShort = 128;      // blocks x tiles of a unit up to which a cluster takes it
 // Steps of a stream whose products tensor memory sums.  Its additions round toward zero, 16 a step: over 64 steps of sums that
 // grow steadily the result is low by up to 2^-14 (half of 1,024 x 2^-23).  Then the sums go to the workspace, where they are
-// added to the nearest.  (Without: 2^20 tokens of positive values in one CTA 2.3e-3 low, more than half of what rounding to
+// added to the nearest.  (Without: 2^20 tokens of positive values in one CTA 2.1e-3 low, more than half of what rounding to
 // bf16 may do.)
 constexpr int kRun = kShort / 2;
 
@@ -834,7 +835,7 @@ __device__ __forceinline__ float2 ld_cluster_v2(uint32_t local, uint32_t rank)
 }
 
 // K CTAs' and I quads' loads in flight: a remote one takes some 700 cycles.  (Pairs of CTAs have several quads a thread: two at
-// once took eight sequences of 128 pages a head from 23.9 to 22.9 us, four spill.)
+// once took eight sequences of 128 pages a head a microsecond less, four spill.)
 template <int D, int K, int I>
 __device__ __forceinline__ void join_quads(const Launch& a, const Unit& u, uint8_t* smem)
 {
@@ -1188,13 +1189,15 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream)
     for (a.b0 = 0; a.b0 < p.B; a.b0 += cut.batches) {
         a.nb = p.B - a.b0 < cut.batches ? p.B - a.b0 : cut.batches;
         a.units = a.nb * p.Hkv * cut.groups;
-        // A cluster a unit, of the most CTAs whose clusters all run at once (7 of 16, 8 of 12, 15 of 9), where units are short: no second launch, and
-        // no CTA looks through all units for its own.  Beyond that the SMs that whole clusters leave empty, and waiting for
-        // the longest of ragged sequences, cost more.  Clusters against dealing, 8 KV heads of 4 query heads, trees of 8
-        // (us): one sequence of 4K tokens 12.0, 14.6, of 12K 20.0, 20.5, of 24K (193 blocks) 30.0, 28.0; two of 8K 21.8,
-        // 24.1, of 16K 36.3, 33.3; four of 8K 31.2, 33.8; sixteen of 2K 30.2, 35.0; sixteen ragged ones of up to 16K, 13
-        // nodes x 5 heads 147, 128.  Two tiles, trees of 64: two of 4K 24.5, 27.3, four of 8K (65 blocks) 42.9, 47.2, but
-        // one of 1K, whose clusters of 12 CTAs have most to join, 16.4, 14.6.
+        // A cluster a unit, of the most CTAs whose clusters all run at once (7 of 16, 8 of 12, 15 of 9), where units are short:
+        // no second launch, and no CTA looks through all units for its own.  Beyond that the SMs that whole clusters leave
+        // empty, and waiting for the longest of ragged sequences, cost more; so do clusters of more than ten CTAs of two
+        // tiles, which have most to join.  Clusters against dealing (us; tables of the sequences' length), 8 KV heads of 4
+        // query heads, trees of 8: one sequence of 4K tokens 13.6, 16.0, of 12K 21.3, 22.9, of 24K (193 blocks) 33.2, 30.0;
+        // two of 8K 24.0, 27.5, of 16K 39.5, 36.8; four of 8K 33.3, 37.1; sixteen of 2K 31.9, 39.6; sixteen ragged ones of up
+        // to 16K, 13 nodes x 5 heads 167, 134.  Two tiles, trees of 64: two of 4K (clusters of 9) 28.0, 30.0, four of 4K 35.1,
+        // 40.6, of 8K (65 blocks) 53.0, 56.6; clusters of 12 and dealing, one of 2K 18.9, 17.8, of 4K 21.3, 21.3, of 8K 27.6,
+        // 25.9.  The rule misses one of 1K (9 blocks, clusters of 9): 18.6, 16.2.
         int c = 0;
         if (a.units <= known.sms) {
             c = 1;
